@@ -13,7 +13,8 @@ import os
 from .build import LIB, LIB_CHECKED, build  # noqa: F401
 
 __all__ = ["Workspace", "SplatError", "load_library", "LIB", "build", "token_dim",
-           "partials_dim", "grad_dim", "finalize_partials"]
+           "partials_dim", "grad_dim", "finalize_partials", "lookup", "lookup_backward", "ffn",
+           "ffn_backward"]
 
 _ERRORS = {
     -1: "INVALID_ARG", -2: "CAPACITY", -3: "STATE", -4: "CUDA", -5: "BOUNDS",
@@ -30,6 +31,8 @@ EXPORTS = [
     "splat_sort_depths_noalloc", "splat_score_partials", "splat_finalize_partials",
     "splat_backward", "splat_render_features", "splat_scatter", "splat_attribution",
     "splat_set_deterministic", "splat_check_status", "splat_checked_build",
+    "splat_lookup", "splat_lookup_scratch", "splat_lookup_backward", "splat_ffn",
+    "splat_ffn_scratch", "splat_ffn_backward",
 ]
 
 
@@ -107,6 +110,19 @@ def load_library(path: str | None = None):
     L.splat_check_status.restype = I
     L.splat_checked_build.argtypes = []
     L.splat_checked_build.restype = I
+    L.splat_lookup.argtypes = [V, LL, I, I, V, I, F, I, V, LL, V]
+    L.splat_lookup.restype = I
+    L.splat_lookup_scratch.argtypes = [I, I, I]
+    L.splat_lookup_scratch.restype = LL
+    L.splat_lookup_backward.argtypes = [V, LL, V, I, I, F, I, V, LL, I, V, LL, V]
+    L.splat_lookup_backward.restype = I
+    L.splat_ffn_scratch.argtypes = [I, I, I, I, I, I, I]
+    L.splat_ffn_scratch.restype = LL
+    L.splat_ffn.argtypes = [V, LL, V, V, V, V, LL, I, I, I, I, I, I, V, LL, V]
+    L.splat_ffn.restype = I
+    L.splat_ffn_backward.argtypes = [V, LL, V, LL, V, V, V, V, LL, V, V, V, I, I, I, I, I, I, V,
+                                     LL, V]
+    L.splat_ffn_backward.restype = I
     if path is None:
         _lib = L
     return L
@@ -348,3 +364,6 @@ class Workspace:
         self._check(self._L.splat_profile_read(self._h, ms, cnt, 1 if reset else 0))
         return {self._L.splat_kernel_name(i).decode(): (float(ms[i]), int(cnt[i]))
                 for i in range(n)}
+
+
+from .rows import ffn, ffn_backward, lookup, lookup_backward  # noqa: E402

@@ -10,7 +10,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsplat.so")
 LIB_CHECKED = os.path.join(PKG, "libsplat_checked.so")  # bounds-checked build (-DSPLAT_CHECKED)
 SOURCES = ["capi.cu", "project.cu", "binning.cu", "raster.cu", "finalize.cu", "backward.cu",
-           "attributes.cu", "noalloc.cu"]
+           "attributes.cu", "noalloc.cu", "rows.cu", "lookup.cu", "ffn.cu"]
+HEADERS = ["common.cuh", "traverse.cuh", "rows.cuh", "ffn.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -18,6 +19,7 @@ NVCC_FLAGS = [
     # the decision path relies on explicit, correctly rounded fp32 operations
     "-fmad=false", "-prec-div=true", "-prec-sqrt=true", "-ftz=false",
     "-Xcompiler", "-fPIC", "-shared",
+    "--threads", "0",  # the sources compile side by side
 ]
 
 
@@ -36,8 +38,8 @@ def up_to_date(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return False
     t = os.path.getmtime(lib)
-    deps = sources() + [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "traverse.cuh"),
-                        os.path.join(ROOT, "include", "splat.h")]
+    deps = sources() + [os.path.join(CSRC, h) for h in HEADERS] + [
+        os.path.join(ROOT, "include", "splat.h")]
     return all(os.path.getmtime(d) <= t for d in deps)
 
 

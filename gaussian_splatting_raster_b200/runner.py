@@ -1,10 +1,10 @@
 """Device-memory plumbing around the C ABI: move a scene's arrays into CUDA tensors, allocate the
-outputs, and issue the four calls in order. No arithmetic of the method happens here."""
+outputs, and issue the calls in order. No arithmetic of the method happens here."""
 from __future__ import annotations
 
 import dataclasses
 
-from . import Workspace, token_dim
+from . import Workspace, ffn, ffn_backward, lookup, lookup_backward, token_dim
 
 
 @dataclasses.dataclass
@@ -90,6 +90,66 @@ def render_and_backward(ws: Workspace, ds: DeviceScene, obs, out: Outputs, grads
     n = render(ws, ds, out, stream)
     ws.backward(obs, ds.log_scales, ds.quats, ds.sh, stream=stream, **grads)
     return n
+
+
+@dataclasses.dataclass
+class FeedForward:
+    """Weights of a feed-forward block: w_gate (None: no gate) and w_up [F, D], w_down [O, F]."""
+    w_gate: "object"
+    w_up: "object"
+    w_down: "object"
+    act: str = "gelu"
+
+    def zeros_like(self) -> "FeedForward":
+        import torch
+        return FeedForward(None if self.w_gate is None else torch.zeros_like(self.w_gate),
+                           torch.zeros_like(self.w_up), torch.zeros_like(self.w_down), self.act)
+
+
+def token_features(out: Outputs, block: FeedForward, feats, stream=None):
+    """The score tokens' projection (feats [G, O] from the tokens of the last score replay; the
+    rendering calls are fp32, so a bf16 or fp16 block gets its tokens rounded first)."""
+    ffn(out.tokens.to(block.w_up.dtype), block.w_gate, block.w_up, block.w_down, feats, block.act,
+        stream)
+
+
+@dataclasses.dataclass
+class Decoded:
+    """What decode_and_render keeps for its gradient: the looked-up rows [G, D] and the attributes
+    [G, C], in the table's type."""
+    rows: "object"
+    feats: "object"
+
+
+def decode_and_render(ws: Workspace, table, ids, scale: float, block: FeedForward, maps,
+                      stream=None) -> Decoded:
+    """Attribute maps of Gaussians that share table rows (anchors, a codebook): row ids[g] of table
+    [N, D], times scale, decoded by the block to C attributes per Gaussian and composited by the
+    last render into maps [V, H, W, C]."""
+    import torch
+    G, C = ids.shape[0], block.w_down.shape[0]
+    with torch.cuda.stream(stream):  # None: the current stream
+        d = Decoded(torch.empty((G, table.shape[1]), dtype=table.dtype, device=table.device),
+                    torch.empty((G, C), dtype=table.dtype, device=table.device))
+        lookup(table, ids, d.rows, scale)
+        ffn(d.rows, block.w_gate, block.w_up, block.w_down, d.feats, block.act)
+        ws.render_features(d.feats.float(), maps)
+    return d
+
+
+def decode_backward(ws: Workspace, ids, scale: float, block: FeedForward, d: Decoded, dmaps,
+                    dtable, dblock: FeedForward, stream=None):
+    """Gradients of decode_and_render with the render held, from dmaps [V, H, W, C]: into dtable
+    [N, D] and the weights of dblock."""
+    import torch
+    with torch.cuda.stream(stream):
+        dfeats = torch.empty(d.feats.shape, dtype=torch.float32, device=d.feats.device)
+        ws.scatter(dmaps, dfeats)
+        drows = torch.empty_like(d.rows)
+        ffn_backward(dfeats.to(d.feats.dtype), d.rows, block.w_gate, block.w_up, block.w_down,
+                     dx=drows, dw_gate=dblock.w_gate, dw_up=dblock.w_up, dw_down=dblock.w_down,
+                     act=block.act)
+        lookup_backward(drows, ids, dtable, scale)
 
 
 def workspace_for(ds: DeviceScene, lib=None) -> Workspace:

@@ -338,6 +338,78 @@ const char* splat_kernel_name(int id);
 #define SPLAT_NOALLOC_MAX_N 262144
 int splat_sort_depths_noalloc(const float* depths, int n, int* order, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Per-row operators: scaled table lookup and feed-forward block, each with its gradient. They
+ * stand on either side of the calls above. Before splat_render_features: the attribute rows of
+ * Gaussians that share an anchor or a codebook entry ("ATSplat": K offsets of one anchor) are
+ * looked up by index and decoded by a feed-forward block; splat_scatter's output goes the same way
+ * back, to the block's weights and the shared rows. After splat_score_replay: the projection of
+ * the token rows z_g ([P1] "Final Token and Updater", linear - GELU - linear).
+ *
+ * They need no workspace. Conventions of the file hold, with these differences:
+ *   - `dtype` is the type of every array of values in the call (sums, activations and statistics
+ *     are fp32 in the kernels); pointers are aligned to their elements, wider alignment is used
+ *     where it is there.
+ *   - Row arrays are given with the distance between rows in elements (`ld_*`, at most 2^28; >= the
+ *     row's width for outputs of more than one row; inputs may have any, 0 included). Weights are
+ *     contiguous. Whatever lies between or behind rows is neither read nor written.
+ *   - All arrays live on the current device, which is `stream`'s. An output may share no element
+ *     with another argument (SPLAT_ERR_INVALID_ARG; column ranges of one wider array are fine).
+ *   - `scratch` is the caller's: a device buffer of at least the bytes the scratch function of the
+ *     call reports for its sizes (0: it may be NULL), 16-byte aligned. Its contents mean nothing
+ *     between calls; two calls that may run at once (other streams, other captured graphs) take
+ *     two buffers.
+ *   - Calls only enqueue kernels on `stream`; they may be captured into a graph. There is no
+ *     message: the code says which kind of argument was refused (INVALID_ARG; CAPACITY for widths
+ *     above the stated limits). Refusals enqueue nothing.
+ *   - Results are the same bits on every run with the same arguments.
+ * ------------------------------------------------------------------------------------------- */
+typedef enum splat_dtype { SPLAT_F32 = 0, SPLAT_BF16 = 1, SPLAT_F16 = 2 } splat_dtype;
+typedef enum splat_act { SPLAT_ACT_SILU = 0, SPLAT_ACT_GELU = 1 } splat_act;
+
+/*
+ * out[i] = scale * table[ids[i]] for 0 <= ids[i] < N, a zero row for any other id (-1 marks a
+ * Gaussian without a row). table [N, C], ids [M] int32, out [M, C]; N, M >= 0, 1 <= C <= 8192.
+ */
+int splat_lookup(const void* table, long long ld_table, int N, int C, const int* ids, int M,
+                 float scale, int dtype, void* out, long long ld_out, void* stream);
+
+/*
+ * The lookup's gradient: dtable[n] = scale * sum of dout[i] over the i with ids[i] = n, every row
+ * written (zeros where no id points; ids outside [0, N) take no part). dout [M, C], dtable [N, C].
+ * Ids are brought into order first (a stable radix sort on the device, left out when they are in
+ * order already); each row's sum is fp32 in that order, rounded once to dtype.
+ */
+long long splat_lookup_scratch(int M, int N, int C);
+int splat_lookup_backward(const void* dout, long long ld_dout, const int* ids, int M, int C,
+                          float scale, int dtype, void* dtable, long long ld_dtable, int N,
+                          void* scratch, long long scratch_bytes, void* stream);
+
+/*
+ * Feed-forward block over rows, act = silu (a / (1 + e^-a)) or gelu (a Phi(a), the exact normal
+ * distribution function):
+ *   y = (act(x w_gate^T) * (x w_up^T)) w_down^T,   or with w_gate NULL  y = act(x w_up^T) w_down^T
+ * x [M, D], w_gate, w_up [F, D], w_down [O, F], y [M, O]; M >= 0, 1 <= D, O <= 128,
+ * 1 <= F <= 1024 (SPLAT_ERR_CAPACITY above). The hidden row act(a) * u is kept on chip, rounded
+ * once to dtype before the second product (bf16 and fp16: an fp16 hidden value above 65504 is
+ * infinite).
+ *
+ * splat_ffn_backward: from dy [M, O] the gradients dx [M, D], dw_gate, dw_up [F, D] and dw_down
+ * [O, F] (each may be NULL, not all; dw_gate only with w_gate). The hidden values are computed
+ * again from x; they and their gradients are rounded once to dtype before the products that use
+ * them; weight gradients are fp32 sums over all rows, rounded once. With M = 0 the weight
+ * gradients are zero.
+ */
+long long splat_ffn_scratch(int M, int D, int F, int O, int dtype, int gated, int backward);
+int splat_ffn(const void* x, long long ld_x, const void* w_gate, const void* w_up,
+              const void* w_down, void* y, long long ld_y, int M, int D, int F, int O, int dtype,
+              int act, void* scratch, long long scratch_bytes, void* stream);
+int splat_ffn_backward(const void* dy, long long ld_dy, const void* x, long long ld_x,
+                       const void* w_gate, const void* w_up, const void* w_down, void* dx,
+                       long long ld_dx, void* dw_gate, void* dw_up, void* dw_down, int M, int D,
+                       int F, int O, int dtype, int act, void* scratch, long long scratch_bytes,
+                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif
