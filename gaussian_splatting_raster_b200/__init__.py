@@ -14,7 +14,7 @@ from .build import LIB, LIB_CHECKED, build  # noqa: F401
 
 __all__ = ["Workspace", "SplatError", "load_library", "LIB", "build", "token_dim",
            "partials_dim", "grad_dim", "finalize_partials", "lookup", "lookup_backward", "ffn",
-           "ffn_backward"]
+           "ffn_backward", "rows_status"]
 
 _ERRORS = {
     -1: "INVALID_ARG", -2: "CAPACITY", -3: "STATE", -4: "CUDA", -5: "BOUNDS",
@@ -32,7 +32,7 @@ EXPORTS = [
     "splat_backward", "splat_render_features", "splat_scatter", "splat_attribution",
     "splat_set_deterministic", "splat_check_status", "splat_checked_build",
     "splat_lookup", "splat_lookup_scratch", "splat_lookup_backward", "splat_ffn",
-    "splat_ffn_scratch", "splat_ffn_backward",
+    "splat_ffn_scratch", "splat_ffn_backward", "splat_rows_status",
 ]
 
 
@@ -123,6 +123,8 @@ def load_library(path: str | None = None):
     L.splat_ffn_backward.argtypes = [V, LL, V, LL, V, V, V, V, LL, V, V, V, I, I, I, I, I, I, V,
                                      LL, V]
     L.splat_ffn_backward.restype = I
+    L.splat_rows_status.argtypes = [V]
+    L.splat_rows_status.restype = I
     if path is None:
         _lib = L
     return L
@@ -366,4 +368,4 @@ class Workspace:
                 for i in range(n)}
 
 
-from .rows import ffn, ffn_backward, lookup, lookup_backward  # noqa: E402
+from .rows import ffn, ffn_backward, lookup, lookup_backward, rows_status  # noqa: E402

@@ -10,8 +10,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsplat.so")
 LIB_CHECKED = os.path.join(PKG, "libsplat_checked.so")  # bounds-checked build (-DSPLAT_CHECKED)
 SOURCES = ["capi.cu", "project.cu", "binning.cu", "raster.cu", "finalize.cu", "backward.cu",
-           "attributes.cu", "noalloc.cu", "rows.cu", "lookup.cu", "ffn.cu"]
-HEADERS = ["common.cuh", "traverse.cuh", "rows.cuh", "ffn.cuh"]
+           "attributes.cu", "noalloc.cu", "rows.cu", "lookup.cu", "ffn.cu", "ffn_tc.cu"]
+HEADERS = ["common.cuh", "traverse.cuh", "rows.cuh", "ffn.cuh", "tc.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p) {
         part[(size_t)f * p.D + k] = ga[c][j];
         if (GATED) part[FD + (size_t)f * p.D + k] = gu[c][j];
       }
-      if (k < p.O) part[(GATED ? 2 : 1) * FD + (size_t)k * p.F + f] = gd[c][j];
+      if (k < p.O) part[(GATED ? 2 : 1) * FD + (size_t)f * p.O + k] = gd[c][j];
     }
 }
 
@@ -326,19 +326,14 @@ __global__ void __launch_bounds__(kT) k_ffn_join(FfnArgs p) {
   float s = 0.0f;
 #pragma unroll 4
   for (int k = 0; k < p.splits; ++k) s += p.part[k * n + i];
-  T* dst;
-  size_t at = i;
+  const size_t down = i - (GATED ? 2 : 1) * FD;  // of dWd^T, when i is past the others
   if (GATED && i < FD) {
-    dst = (T*)p.dwg;
-  } else {
-    if (GATED) at -= FD;
-    dst = (T*)p.dwu;
-    if (at >= FD) {
-      at -= FD;
-      dst = (T*)p.dwd;
-    }
+    if (p.dwg) ((T*)p.dwg)[i] = from_f<T>(s);
+  } else if (i < (GATED ? 2 : 1) * FD) {
+    if (p.dwu) ((T*)p.dwu)[GATED ? i - FD : i] = from_f<T>(s);
+  } else if (p.dwd) {
+    ((T*)p.dwd)[down % p.O * p.F + down / p.O] = from_f<T>(s);
   }
-  if (dst) dst[at] = from_f<T>(s);
 }
 
 int last_error() {
@@ -377,6 +372,12 @@ int run_forward(const FfnArgs& p, cudaStream_t st) {
   return last_error();
 }
 
+template <typename T, bool GATED> int run_join(const FfnArgs& p, cudaStream_t st) {
+  const size_t n = ((GATED ? 2 : 1) * (size_t)p.D + p.O) * p.F;
+  k_ffn_join<T, GATED><<<(unsigned)((n + kT - 1) / kT), kT, 0, st>>>(p);
+  return last_error();
+}
+
 template <typename T, int ACT, bool GATED>
 int run_backward(const FfnArgs& p, cudaStream_t st) {
   if (p.dx && p.M > 0) {
@@ -389,24 +390,35 @@ int run_backward(const FfnArgs& p, cudaStream_t st) {
     if (!allow_smem(k_ffn_dw<T, ACT, GATED>, smem)) return SPLAT_ERR_CUDA;
     const dim3 grid((p.F + kChunk - 1) / kChunk, p.splits);
     k_ffn_dw<T, ACT, GATED><<<grid, kT, smem, st>>>(p);
-    const size_t n = ((GATED ? 2 : 1) * (size_t)p.D + p.O) * p.F;
-    k_ffn_join<T, GATED><<<(unsigned)((n + kT - 1) / kT), kT, 0, st>>>(p);
+    return run_join<T, GATED>(p, st);
   }
   return last_error();
 }
 
-template <typename T>
-int dispatch(const FfnArgs& p, int act, bool backward, cudaStream_t st) {
-  if (act == SPLAT_ACT_SILU) {
-    if (p.wg) return backward ? run_backward<T, SPLAT_ACT_SILU, true>(p, st)
-                              : run_forward<T, SPLAT_ACT_SILU, true>(p, st);
-    return backward ? run_backward<T, SPLAT_ACT_SILU, false>(p, st)
-                    : run_forward<T, SPLAT_ACT_SILU, false>(p, st);
+template <typename T, int ACT, bool GATED>
+int run(const FfnArgs& p, bool backward, cudaStream_t st) {
+  return backward ? run_backward<T, ACT, GATED>(p, st) : run_forward<T, ACT, GATED>(p, st);
+}
+
+// fp32 on the fp32 lanes, bf16 and fp16 on the tensor cores
+int dispatch(FfnArgs& p, int dtype, int act, bool backward, void* scratch, cudaStream_t st) {
+  const bool gated = p.wg != nullptr;
+  if (dtype == SPLAT_F32) {
+    p.part = (float*)scratch;
+    p.splits = dw_splits(p.M, p.F);
+    if (act == SPLAT_ACT_SILU)
+      return gated ? run<float, SPLAT_ACT_SILU, true>(p, backward, st)
+                   : run<float, SPLAT_ACT_SILU, false>(p, backward, st);
+    return gated ? run<float, SPLAT_ACT_GELU, true>(p, backward, st)
+                 : run<float, SPLAT_ACT_GELU, false>(p, backward, st);
   }
-  if (p.wg) return backward ? run_backward<T, SPLAT_ACT_GELU, true>(p, st)
-                            : run_forward<T, SPLAT_ACT_GELU, true>(p, st);
-  return backward ? run_backward<T, SPLAT_ACT_GELU, false>(p, st)
-                  : run_forward<T, SPLAT_ACT_GELU, false>(p, st);
+  p.part = (float*)((char*)scratch + ffn_tc_image_bytes(p.D, p.F, p.O, gated));
+  p.splits = ffn_tc_splits(p.M, p.F);
+  const int rc = ffn_tc_run(p, dtype, act, backward, scratch, st);
+  if (rc != SPLAT_OK || !(p.dwg || p.dwu || p.dwd)) return rc;
+  if (dtype == SPLAT_BF16)
+    return gated ? run_join<__nv_bfloat16, true>(p, st) : run_join<__nv_bfloat16, false>(p, st);
+  return gated ? run_join<__half, true>(p, st) : run_join<__half, false>(p, st);
 }
 
 int check_sizes(int M, int D, int F, int O, int dtype, int act) {
@@ -426,8 +438,12 @@ using namespace splat::rows;
 extern "C" {
 
 long long splat_ffn_scratch(int M, int D, int F, int O, int dtype, int gated, int backward) {
-  if (check_sizes(M, D, F, O, dtype, SPLAT_ACT_SILU) != SPLAT_OK || !backward) return 0;
-  const long long n = (long long)F * ((gated ? 2 : 1) * D + O) * 4 * dw_splits(M, F);
+  if (check_sizes(M, D, F, O, dtype, SPLAT_ACT_SILU) != SPLAT_OK) return 0;
+  const bool tc = dtype != SPLAT_F32;
+  long long n = tc ? (long long)ffn_tc_image_bytes(D, F, O, gated != 0) : 0;
+  if (backward)
+    n += (long long)F * ((gated ? 2 : 1) * D + O) * 4 *
+         (tc ? ffn_tc_splits(M, F) : dw_splits(M, F));
   return (n + 255) & ~255LL;
 }
 
@@ -460,9 +476,7 @@ int splat_ffn(const void* x, long long ld_x, const void* w_gate, const void* w_u
   p.F = F;
   p.O = O;
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == SPLAT_F32) return dispatch<float>(p, act, false, st);
-  if (dtype == SPLAT_BF16) return dispatch<__nv_bfloat16>(p, act, false, st);
-  return dispatch<__half>(p, act, false, st);
+  return dispatch(p, dtype, act, false, scratch, st);
 }
 
 int splat_ffn_backward(const void* dy, long long ld_dy, const void* x, long long ld_x,
@@ -505,12 +519,17 @@ int splat_ffn_backward(const void* dy, long long ld_dy, const void* x, long long
   p.D = D;
   p.F = F;
   p.O = O;
-  p.part = (float*)scratch;
-  p.splits = dw_splits(M, F);
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == SPLAT_F32) return dispatch<float>(p, act, true, st);
-  if (dtype == SPLAT_BF16) return dispatch<__nv_bfloat16>(p, act, true, st);
-  return dispatch<__half>(p, act, true, st);
+  return dispatch(p, dtype, act, true, scratch, st);
+}
+
+int splat_rows_status(void* stream) {
+  unsigned int v = 0;
+  if (rows_status_take(&v, (cudaStream_t)stream) != cudaSuccess) {
+    cudaGetLastError();
+    return SPLAT_ERR_CUDA;
+  }
+  return v ? SPLAT_ERR_DEVICE_TIMEOUT : SPLAT_OK;
 }
 
 }  // extern "C"

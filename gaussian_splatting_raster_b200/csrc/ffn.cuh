@@ -26,7 +26,7 @@ struct FfnArgs {
   void *y, *dx, *dwg, *dwu, *dwd;
   long long ldx, ldy, lddy, lddx;
   int M, D, F, O;
-  float* part;   // [splits] partial weight gradients (dWg, dWu [F, D] each, dWd [O, F]), fp32
+  float* part;   // [splits] partial weight gradients, fp32: dWg, dWu [F, D] each, dWd^T [F, O]
   int splits;
 };
 
@@ -50,6 +50,14 @@ __device__ __forceinline__ float act_and_slope(float a, float& slope) {
   slope = fmaf(a * 0.3989422804014327f, expf(-0.5f * a * a), cdf);
   return a * cdf;
 }
+
+// tensor-core kernels (ffn_tc.cu; bf16 and fp16): bytes of the packed weights, row splits of the
+// weight gradients, and the kernels but for the splits' sum
+size_t ffn_tc_image_bytes(int D, int F, int O, bool gated);
+int ffn_tc_splits(long long M, int F);
+int ffn_tc_run(const FfnArgs& f, int dtype, int act, bool backward, void* img, cudaStream_t st);
+// the status word of their waits, read and cleared (waits for the stream)
+cudaError_t rows_status_take(unsigned int* out, cudaStream_t st);
 
 }  // namespace rows
 }  // namespace splat

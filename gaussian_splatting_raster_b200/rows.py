@@ -167,3 +167,12 @@ def ffn_backward(dy, x, w_gate, w_up, w_down, dx=None, dw_gate=None, dw_up=None,
     _call(L.splat_ffn_backward, "ffn_backward", x.device, stream,
           (py, ldy, px, ldx, *w, pd, ldd, *dw, M, D, F, O, dt, a),
           L.splat_ffn_scratch(M, D, F, O, dt, w_gate is not None, 1))
+
+
+def rows_status(stream=None):
+    """Raise SplatError(DEVICE_TIMEOUT) when a bounded wait of a feed-forward kernel ran out on the
+    current device since the last call (waits for the stream)."""
+    s = stream if stream is not None else torch.cuda.current_stream()
+    rc = load_library().splat_rows_status(s.cuda_stream)
+    if rc != 0:
+        raise SplatError(rc, "a bounded wait ran out" if rc == -6 else "reading the status failed")

@@ -53,7 +53,7 @@ typedef enum splat_status {
   SPLAT_ERR_STATE = -3,          /* calls out of order */
   SPLAT_ERR_CUDA = -4,           /* a CUDA runtime call or kernel launch failed */
   SPLAT_ERR_BOUNDS = -5,         /* a device-side bounds check failed (reported, access skipped) */
-  SPLAT_ERR_DEVICE_TIMEOUT = -6, /* reserved: a bounded device-side wait ran out */
+  SPLAT_ERR_DEVICE_TIMEOUT = -6, /* a bounded device-side wait ran out */
   SPLAT_ERR_OOM = -7             /* device allocation failed */
 } splat_status;
 
@@ -409,6 +409,14 @@ int splat_ffn_backward(const void* dy, long long ld_dy, const void* x, long long
                        long long ld_dx, void* dw_gate, void* dw_up, void* dw_down, int M, int D,
                        int F, int O, int dtype, int act, void* scratch, long long scratch_bytes,
                        void* stream);
+
+/*
+ * Waits inside the feed-forward kernels (for their own copies and products) are bounded at about
+ * four seconds. When one ran out on the current device since the last call, the results of the
+ * call it belonged to mean nothing and this returns SPLAT_ERR_DEVICE_TIMEOUT once. Waits for
+ * `stream`; not to be captured.
+ */
+int splat_rows_status(void* stream);
 
 #ifdef __cplusplus
 }
