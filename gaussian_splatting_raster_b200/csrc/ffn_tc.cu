@@ -37,14 +37,21 @@ constexpr int kSmemLimit = 232448 - 2048;  // 227 KB less the alignment slack an
 
 __device__ unsigned int g_rows_status;
 
+// A row array as the loads see it: 16-byte pieces may be taken from [lo, hi) only.
+struct RowSrc {
+  const uint8_t *base, *lo, *hi;  // lo, hi: 16-byte aligned, inside the array
+  long long ld;                   // bytes
+  int cols, aligned;              // aligned: every row starts and ends at 16 bytes
+};
+
 struct TcArgs {
   FfnArgs f;
   const uint8_t* img;   // packed weights, chunk after chunk
   int nch, stage_bytes; // chunks; bytes of one
   int nst, ng;          // weight stages in shared memory; groups
   int dp, op;           // D and O rounded up to 16
-  int x_vec, dy_vec, out_vec;  // bytes per access of x, dy, and y or dx
-  uint32_t x_magic, dy_magic;  // dividers by the 16-byte pieces per row
+  RowSrc x, dy;
+  int out_aligned;      // y's or dx's rows start and end at 16 bytes
   long long tiles;
 };
 
@@ -64,41 +71,71 @@ template <> struct Two<__half> {
   }
 };
 
-// 1 / v and e^v from the special function unit (relative error below 2^-22 each; the results are
-// rounded to 8 or 11 bits)
-__device__ __forceinline__ float rcp_fast(float v) { return __fdividef(1.0f, v); }
-__device__ __forceinline__ float exp_fast(float v) { return __expf(v); }
-
-// Phi(a) and e^{-a^2/2}: Abramowitz and Stegun 7.1.26 for erfc at |a| / sqrt 2, absolute error
-// 0.75e-7 in Phi; one exponential serves Phi and the density.
-__device__ __forceinline__ float normal_cdf(float a, float& e) {
-  const float z = fabsf(a) * 0.70710678118654752f;
-  const float t = rcp_fast(fmaf(0.3275911f, z, 1.0f));
-  e = exp_fast(-z * z);
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  q = 0.5f * (q * t) * e;
-  return a >= 0.0f ? 1.0f - q : q;
+// 2^v and 1 / v of the special function unit: relative error below 2^-22 each, for results that are
+// rounded to 8 or 11 bits. The unit takes one value per lane group and cycle (16 an SM), which is
+// what bounds these kernels at narrow widths, so four reciprocals are taken as one: with
+// r = 1 / (p0 p1 p2 p3) each is r times the product of the other three.
+__device__ __forceinline__ float ex2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ void rcp4(const float (&p)[4], float (&r)[4]) {
+  const float m01 = p[0] * p[1], m23 = p[2] * p[3];
+  const float i = rcp_fast(m01 * m23);
+  const float i01 = i * m23, i23 = i * m01;
+  r[0] = i01 * p[1];
+  r[1] = i01 * p[0];
+  r[2] = i23 * p[3];
+  r[3] = i23 * p[2];
 }
 
-template <int ACT> __device__ __forceinline__ float act_fast(float a) {
-  if (ACT == SPLAT_ACT_SILU) return a * rcp_fast(1.0f + exp_fast(-a));
-  float e;
-  return a * normal_cdf(a, e);
-}
-
-template <int ACT> __device__ __forceinline__ float act_slope_fast(float a, float& slope) {
+// act and its slope for four values. MODE-independent; without SLOPE the slope is not formed.
+//   silu: s = 1 / (1 + 2^t), t = -a log2 e held at 31 so that four factors stay finite: s is then
+//         never below 2^-31, which differs from the true value by less than an fp32 step of 1/128.
+//   gelu: Phi by Abramowitz and Stegun 7.1.26 (erfc at z = |a| / sqrt 2, absolute error 0.75e-7 in
+//         Phi), z held at 10 where Phi(-|a|) has long become zero; one power e^{-a^2/2} serves Phi
+//         and the density.
+// An argument that is no number gives no number: both are multiplied by a, or built from it.
+template <int ACT, bool SLOPE>
+__device__ __forceinline__ void act4(const float* a, float* f, float* slope) {
+  float p[4], r[4];
   if (ACT == SPLAT_ACT_SILU) {
-    const float s = rcp_fast(1.0f + exp_fast(-a)), f = a * s;
-    slope = fmaf(f, 1.0f - s, s);
-    return f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = 1.0f + ex2_fast(fminf(a[i] * -1.4426950408889634f, 31.0f));
+    rcp4(p, r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = a[i] * r[i];
+      if (SLOPE) slope[i] = fmaf(f[i], 1.0f - r[i], r[i]);
+    }
+  } else {
+    float z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      z[i] = fminf(fabsf(a[i]) * 0.70710678118654752f, 10.0f);
+      p[i] = fmaf(0.3275911f, z[i], 1.0f);
+    }
+    rcp4(p, r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float e = ex2_fast(z[i] * z[i] * -1.4426950408889634f);
+      float q = fmaf(0.5307027145f, r[i], -0.7265760135f);  // half the published coefficients
+      q = fmaf(q, r[i], 0.7107068705f);
+      q = fmaf(q, r[i], -0.142248368f);
+      q = fmaf(q, r[i], 0.127414796f);
+      q = q * r[i] * e;
+      const float c = a[i] >= 0.0f ? 1.0f - q : q;
+      f[i] = a[i] * c;
+      if (SLOPE) slope[i] = fmaf(a[i] * 0.3989422804014327f, e, c);
+    }
   }
-  float e;
-  const float c = normal_cdf(a, e);
-  slope = fmaf(a * 0.3989422804014327f, e, c);
-  return a * c;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -147,84 +184,116 @@ k_pack(TcArgs p, uint8_t* __restrict__ img) {
 // row tiles
 // ---------------------------------------------------------------------------------------------
 
-// elements [8 c, 8 c + 8) of a row of `cols`, zeros behind its end
-__device__ __forceinline__ uint4 fetch8(const uint16_t* row, int c, int cols, int vec) {
-  const int e0 = c * 8;
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (vec == 16) {
-    if (e0 < cols) v = __ldg(reinterpret_cast<const uint4*>(row + e0));
-  } else if (vec == 8) {
-    const uint2* s = reinterpret_cast<const uint2*>(row + e0);
-    uint2 a = make_uint2(0u, 0u), b = a;
-    if (e0 < cols) a = __ldg(s);
-    if (e0 + 4 < cols) b = __ldg(s + 1);
-    v = make_uint4(a.x, a.y, b.x, b.y);
-  } else if (vec == 4) {
-    const uint32_t* s = reinterpret_cast<const uint32_t*>(row + e0);
-    if (e0 < cols) v.x = __ldg(s);
-    if (e0 + 2 < cols) v.y = __ldg(s + 1);
-    if (e0 + 4 < cols) v.z = __ldg(s + 2);
-    if (e0 + 6 < cols) v.w = __ldg(s + 3);
-  } else {
-    uint32_t h[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) h[k] = e0 + k < cols ? (uint32_t)__ldg(row + e0 + k) : 0u;
-    v = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
-                   h[6] | (h[7] << 16));
-  }
-  return v;
-}
+// A group takes its tile of rows [r0, r0 + 128) with eight threads to a row: thread t has piece
+// t & 7 (16 bytes, 8 elements) of each 64-column block of rows t / 8 + 32 j. The swizzle and a
+// row's offset from 16-byte alignment are then the same for all four j. Rows >= M are zeros, and
+// so are elements behind a row's end up to the next multiple of 16 (the MMAs' step; nothing reads
+// what lies behind).
 
-// One group's tile of rows [r0, r0 + 128) in registers (each thread np pieces), then in shared
-// memory. np = pieces per row / 2 <= 8; rows >= M are zeros.
-struct RowRegs {
-  uint4 v[8];
-};
-
-__device__ __forceinline__ void fetch_rows(RowRegs& g, const void* src, long long ld, long long r0,
-                                           long long M, int cols, int pieces, uint32_t magic,
-                                           int vec, int tid) {
+// aligned rows: one 64-column block's loads, started and then stored
+__device__ __forceinline__ void fetch_rows(const RowSrc& s, int block, long long r0, long long M,
+                                           int tid, uint4 (&v)[4]) {
+  const int c = block * 8 + (tid & 7);
+  const long long r = r0 + (tid >> 3);
+  const uint8_t* p = s.base + r * s.ld + c * 16;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (2 * k >= pieces) break;
-    const int q = tid + k * kGroupThreads;
-    const int r = (int)__umulhi((uint32_t)q, magic), c = q - r * pieces;
-    g.v[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (r0 + r < M) g.v[k] = fetch8((const uint16_t*)src + (r0 + r) * ld, c, cols, vec);
+  for (int j = 0; j < 4; ++j) {
+    v[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (c * 8 < s.cols && r + 32 * j < M)
+      v[j] = __ldg(reinterpret_cast<const uint4*>(p + 32 * j * s.ld));
   }
 }
 
-__device__ __forceinline__ void store_rows(const RowRegs& g, uint8_t* dst, int pieces,
-                                           uint32_t magic, int tid) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (2 * k >= pieces) break;
-    const int q = tid + k * kGroupThreads;
-    const int r = (int)__umulhi((uint32_t)q, magic), c = q - r * pieces;
-    *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-        g.v[k];
-  }
+__device__ __forceinline__ uint8_t* piece_at(uint8_t* dst, int block, int tid) {
+  return dst + block * 16384 + (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4);
 }
 
-// 8 values of a row from column e0, those before `cols`
-__device__ __forceinline__ void put8(uint16_t* row, int e0, int cols, uint4 v, int vec) {
-  if (e0 >= cols) return;
-  if (vec == 16) {
-    *reinterpret_cast<uint4*>(row + e0) = v;
-  } else if (vec == 8) {
-    *reinterpret_cast<uint2*>(row + e0) = make_uint2(v.x, v.y);
-    if (e0 + 4 < cols) *reinterpret_cast<uint2*>(row + e0 + 4) = make_uint2(v.z, v.w);
-  } else {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void store_rows(int block, int tid, const uint4 (&v)[4], uint8_t* dst) {
+  uint8_t* q = piece_at(dst, block, tid);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (vec == 4) {
-        if (e0 + 2 * k < cols) *reinterpret_cast<uint32_t*>(row + e0 + 2 * k) = w[k];
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(q + j * 4096) = v[j];
+}
+
+// any other rows: the aligned 16-byte pieces around each piece (odd widths start anywhere), shifted
+// into place. Pieces that reach over the array's ends are gathered element by element.
+__device__ __forceinline__ void gather_rows(const RowSrc& s, int block, long long r0, long long M,
+                                            int tid, uint8_t* dst) {
+  const int c = block * 8 + (tid & 7);
+  const long long r = r0 + (tid >> 3);
+  const uint8_t* p = s.base + r * s.ld + c * 16;
+  const int n = min(8, s.cols - c * 8);  // elements wanted
+  const uint32_t off = (uint32_t)(uintptr_t)p & 15u;
+  const bool two = (int)off + 2 * n > 16;
+  uint8_t* q = piece_at(dst, block, tid);
+#pragma unroll
+  for (int j = 0; j < 4; ++j, p += 32 * s.ld) {
+    uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    if (n > 0 && r + 32 * j < M) {
+      const uint8_t* a = p - off;
+      if (a >= s.lo && a + (two ? 32 : 16) <= s.hi) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a));
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        if (two) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(a + 16));
+          w[4] = u.x, w[5] = u.y, w[6] = u.z, w[7] = u.w;
+        }
       } else {
-        if (e0 + 2 * k < cols) row[e0 + 2 * k] = (uint16_t)w[k];
-        if (e0 + 2 * k + 1 < cols) row[e0 + 2 * k + 1] = (uint16_t)(w[k] >> 16);
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (2 * k >= (int)off && 2 * k < (int)off + 2 * n)
+            w[k >> 1] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(a + 2 * k))
+                         << ((k & 1) * 16);
       }
     }
+    if (off & 4u) {
+#pragma unroll
+      for (int k = 0; k < 7; ++k) w[k] = w[k + 1];
+    }
+    if (off & 8u) {
+#pragma unroll
+      for (int k = 0; k < 5; ++k) w[k] = w[k + 2];
+    }
+    const uint32_t sh = (off & 2u) * 8u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      w[k] = __funnelshift_r(w[k], w[k + 1], sh);
+      if (n < 8) w[k] = n >= 2 * k + 2 ? w[k] : n == 2 * k + 1 ? w[k] & 0xFFFFu : 0u;
+    }
+    *reinterpret_cast<uint4*>(q + j * 4096) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// the rows' lines on their way into L2
+__device__ __forceinline__ void prefetch_row(const RowSrc& s, long long r, long long M) {
+  if (r >= M) return;
+  const uint8_t* p = s.base + r * s.ld;
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p + s.cols * 2 - 2));
+}
+
+// One 64-column block of results (columns col0 ..) from shared memory to a row array: aligned rows
+// in 16-byte pieces, others element by element with neighbouring lanes on neighbouring elements.
+__device__ __forceinline__ void write_rows(const uint8_t* src, uint8_t* base, long long ld,
+                                           int aligned, int col0, int cols, long long r0,
+                                           long long M, int tid) {
+  if (aligned) {
+    const int c = tid & 7;
+    const long long r = r0 + (tid >> 3);
+    if (col0 + c * 8 >= cols) return;
+    const uint8_t* q = src + (tid >> 3) * 128 + ((c ^ ((tid >> 3) & 7)) << 4);
+    uint8_t* p = base + r * ld + col0 * 2 + c * 16;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (r + 32 * j < M)
+        *reinterpret_cast<uint4*>(p + 32 * j * ld) = *reinterpret_cast<const uint4*>(q + j * 4096);
+  } else {
+    const int lane = tid & 31;
+    const int n = min(64, cols - col0);
+    for (int r = tid >> 5; r < kTile && r0 + r < M; r += kGroupThreads / 32)
+      for (int e = lane; e < n; e += 32)
+        *reinterpret_cast<uint16_t*>(base + (r0 + r) * ld + (col0 + e) * 2) =
+            *reinterpret_cast<const uint16_t*>(src + r * 128 + (((e >> 3) ^ (r & 7)) << 4) +
+                                               (e & 7) * 2);
   }
 }
 
@@ -276,7 +345,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
     s_failed = 0;
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
+      mbar_init(empty(s), p.ng);
     }
     for (int g = 0; g < kMaxGroups; ++g) {
       mbar_init(gu_full(g), 1);
@@ -309,83 +378,140 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
 
   if (warp == kMaxGroups * 8) {
     // ------------------------------------------------------------------------- MMA issue
-    if (lane == 0 && nt > 0) {
+    // (the whole warp waits, one lane issues)
+    if (nt > 0) {
       const int kx = p.dp >> 4, ko = p.op >> 4;
       const uint32_t id_gu = idesc(BF, WR, false, false), id_dh = idesc(BF, 64, false, true);
       const uint32_t id_y = idesc(BF, p.op, false, false), id_dx = idesc(BF, p.dp, false, true);
       const uint32_t id_wx = idesc(BF, p.dp, true, true), id_wy = idesc(BF, p.op, true, true);
-      auto xs = [&](int g) { return sbase + groups0 + g * gbytes; };
-      auto ys = [&](int g) { return xs(g) + nbx * 16384; };
-      auto hs = [&](int g) { return xs(g) + (nbx + (MODE == kFwd ? 0 : nby)) * 16384; };
-      auto ws = [&](int s) { return sbase + s * p.stage_bytes; };
-      auto down = [&](int s) { return ws(s) + nbx * WR * 128; };
+      // descriptors count in 16 bytes: a step of 16 along K is 2 in a K-major tile (4 steps to a
+      // 64-column block), 128 in an MN-major one; weights' blocks have WR rows
+      constexpr uint32_t kBlk = 16384 >> 4, kWBlk = WR * 128 >> 4;
+      const uint32_t x0 = sbase + groups0, y0 = x0 + nbx * 16384;
+      const uint32_t h0 = x0 + (nbx + (MODE == kFwd ? 0 : nby)) * 16384;
+      const uint32_t dx_k = desc_lo(x0, 16), dy_k = desc_lo(y0, 16), dh_k = desc_lo(h0, 16);
+      const uint32_t dx_mn = desc_lo(x0, 16384), dy_mn = desc_lo(y0, 16384), dh_mn = desc_lo(h0, 16384);
+      const uint32_t dw_k = desc_lo(sbase, 16), dw_mn = desc_lo(sbase, WR * 128);
+      const uint32_t dd_k = desc_lo(sbase + nbx * WR * 128, 16);
+      const uint32_t gs = gbytes >> 4, ss = p.stage_bytes >> 4;
       // A|U (and dH) of group g from stage s
       auto first_product = [&](int g, int s) {
-        const uint32_t d = tmem + g * tg;
-        for (int k = 0; k < kx; ++k)
-          mma(d, desc(xs(g) + (k >> 2) * 16384 + (k & 3) * 32, 16),
-              desc(ws(s) + (k >> 2) * (WR * 128) + (k & 3) * 32, 16), id_gu, k > 0);
-        if (MODE != kFwd)
-          for (int k = 0; k < ko; ++k)
-            mma(d + 128, desc(ys(g) + (k >> 2) * 16384 + (k & 3) * 32, 16),
-                desc(down(s) + k * 2048, 16), id_dh, k > 0);
-        commit(gu_full(g));
-      };
-      uint32_t ph_h[kMaxGroups] = {0, 0}, ph_x[kMaxGroups] = {0, 0};
-      auto wait_h = [&](int g) {
-        mbar_wait(h_ready(g), ph_h[g], failed, status);
-        ph_h[g] ^= 1;
-        fence_after();
-      };
-      auto wait_x = [&](int g) {
-        mbar_wait(x_ready(g), ph_x[g], failed, status);
-        ph_x[g] ^= 1;
-        fence_after();
-      };
-      const bool ring = nch > p.nst;
-      auto wait_full = [&](long long j) {  // j-th chunk use
-        if (ring || j < nch)
-          mbar_wait(full((int)(j % p.nst)), (uint32_t)((j / p.nst) & 1), failed, status);
-      };
-      const long long total = (long long)nt * nch;
-      wait_full(0);
-      for (int g = 0; g < p.ng; ++g) {
-        wait_x(g);
-        first_product(g, 0);
-      }
-      for (long long j = 0; j < total; ++j) {
-        const int c = (int)(j % nch);
-        const int s = ring ? (int)(j % p.nst) : c;
-        const int sn = ring ? (int)((j + 1) % p.nst) : (c + 1) % nch;
-        if (j + 1 < total) wait_full(j + 1);
-        for (int g = 0; g < p.ng; ++g) {
+        if (elect_one()) {
           const uint32_t d = tmem + g * tg;
-          wait_h(g);
-          if (MODE == kFwd) {
-            for (int k = 0; k < 4; ++k)
-              mma(d + 128, desc(hs(g) + k * 32, 16), desc(down(s) + k * 32, 16), id_y,
-                  c > 0 || k > 0);
-          } else if (MODE == kDx) {
-            for (int k = 0; k < WR / 16; ++k)
-              mma(d + 192, desc(hs(g) + (k >> 2) * 16384 + (k & 3) * 32, 16),
-                  desc(ws(s) + k * 2048, WR * 128), id_dx, c > 0 || k > 0);
-          } else {
+          const uint32_t a = dx_k + g * gs, b = dw_k + s * ss;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < kx)
+              mma(d, a + (k >> 2) * kBlk + (k & 3) * 2, b + (k >> 2) * kWBlk + (k & 3) * 2, id_gu,
+                  k > 0);
+          if (MODE != kFwd) {
+            const uint32_t ay = dy_k + g * gs, bd = dd_k + s * ss;
+#pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma(acc_gu, desc(hs(g) + k * 2048, 16384), desc(xs(g) + k * 2048, 16384), id_wx,
-                  j > 0 || g > 0 || k > 0);
-            for (int k = 0; k < 8; ++k)
-              mma(acc_d, desc(hs(g) + (GATED ? 16384 : 0) + k * 2048, 16384),
-                  desc(ys(g) + k * 2048, 16384), id_wy, j > 0 || g > 0 || k > 0);
+              if (k < ko)
+                mma(d + 128, ay + (k >> 2) * kBlk + (k & 3) * 2, bd + k * 128, id_dh, k > 0);
           }
-          if (MODE == kDw || c == nch - 1) commit(out_done(g));
-          if (ring && g == p.ng - 1) commit(empty(s));
-          if (j + 1 < total) {
-            if (MODE == kDw) wait_x(g);
-            first_product(g, sn);
+          commit(gu_full(g));
+        }
+        __syncwarp();
+      };
+      auto second_product = [&](int g, int s, bool add, bool begun, bool last_chunk, bool ring,
+                                bool last) {
+        if (elect_one()) {
+          const uint32_t d = tmem + g * tg;
+          if (MODE == kFwd) {
+            const uint32_t a = dh_k + g * gs, b = dd_k + s * ss;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma(d + 128, a + k * 2, b + k * 2, id_y, add || k > 0);
+          } else if (MODE == kDx) {
+            const uint32_t a = dh_k + g * gs, b = dw_mn + s * ss;
+#pragma unroll
+            for (int k = 0; k < WR / 16; ++k)
+              mma(d + 192, a + (k >> 2) * kBlk + (k & 3) * 2, b + k * 128, id_dx, add || k > 0);
+          } else {
+            const uint32_t a = dh_mn + g * gs, b = dx_mn + g * gs;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma(acc_gu, a + k * 128, b + k * 128, id_wx, begun || k > 0);
+            const uint32_t ad = a + (GATED ? kBlk : 0), bd = dy_mn + g * gs;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma(acc_d, ad + k * 128, bd + k * 128, id_wy, begun || k > 0);
+          }
+          if (last_chunk) commit(out_done(g));
+          if (ring) commit(empty(s));
+          if (last) commit(all_done);
+        }
+        __syncwarp();
+      };
+      // Each group goes through: first product (its rows and the chunk's weights are there), hidden
+      // operand ready, second product. The groups are served in the order they become ready.
+      const bool ring = nch > p.nst;
+      struct State {
+        int left, c, s;    // chunks to go, chunk, weight stage
+        uint32_t ph;       // bit 0 weights, bit 1 hidden operand, bit 2 rows
+        bool fresh;        // the stage's weights are to be waited for
+        bool first;        // the first product is next
+        bool rows;         // ... of a new tile
+      };
+      State st[kMaxGroups];
+      int left = p.ng * nt * nch;
+#pragma unroll
+      for (int g = 0; g < kMaxGroups; ++g) st[g] = {g < p.ng ? nt * nch : 0, 0, 0, 0u, true, true, true};
+      bool begun = false;
+      int turn = 0;  // weights: both groups add to one accumulator, always in the same order
+      long long since = clock64();
+      auto is_there = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_try(bar, parity)) || *failed;
+      };
+      while (left > 0) {
+        bool moved = false;
+#pragma unroll
+        for (int g = 0; g < kMaxGroups; ++g) {
+          State& t = st[g];
+          if (t.left == 0) continue;
+          if (t.first) {
+            if (t.fresh && !is_there(full(t.s), t.ph & 1)) continue;
+            if (t.rows && !is_there(x_ready(g), (t.ph >> 2) & 1)) continue;
+            fence_after();
+            if (t.rows) t.ph ^= 4;
+            t.rows = false;
+            first_product(g, t.s);
+            t.first = false;
+            moved = true;
+          } else if ((MODE != kDw || g == turn) && is_there(h_ready(g), (t.ph >> 1) & 1)) {
+            fence_after();
+            t.ph ^= 2;
+            const bool last_chunk = t.c == nch - 1;
+            --left;
+            --t.left;
+            if (p.ng > 1) turn ^= 1;
+            second_product(g, t.s, t.c > 0, begun, last_chunk, ring, left == 0);
+            begun = true;
+            t.c = last_chunk ? 0 : t.c + 1;
+            if (++t.s == p.nst) {
+              t.s = 0;
+              t.ph ^= 1;
+              t.fresh = ring;
+            }
+            t.first = true;
+            t.rows = last_chunk;
+            moved = true;
+            // within a tile the next first product follows at once when its weights are there
+            if (t.left > 0 && !t.rows && (!t.fresh || is_there(full(t.s), t.ph & 1))) {
+              fence_after();
+              first_product(g, t.s);
+              t.first = false;
+            }
           }
         }
+        if (moved) {
+          since = clock64();
+        } else if (clock64() - since > kWaitClocks) {
+          *failed = 1;
+          atomicOr(status, 1u);
+        }
       }
-      commit(all_done);
     }
   } else if (warp == kMaxGroups * 8 + 1) {
     // ------------------------------------------------------------------------- weight loads
@@ -419,17 +545,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
       const uint32_t row_lanes = (uint32_t)(warp & 3) << 21;  // 32 * quadrant in the lane field
       const uint32_t d = tmem + g * tg + row_lanes;
       const int row = (warp & 3) * 32 + lane, half = (warp >> 2) & 1;
-      const int xp = p.dp >> 3, yp = p.op >> 3;  // 16-byte pieces per row
-      RowRegs xr, yr;
-      auto fetch = [&](int n) {
-        const long long r0 = (first + g + n * step) * kTile;
-        fetch_rows(xr, p.f.x, p.f.ldx, r0, p.f.M, p.f.D, xp, p.x_magic, p.x_vec, tid);
-        if (MODE != kFwd)
-          fetch_rows(yr, p.f.dy, p.f.lddy, r0, p.f.M, p.f.O, yp, p.dy_magic, p.dy_vec, tid);
-      };
-      auto store = [&]() {
-        store_rows(xr, Xs, xp, p.x_magic, tid);
-        if (MODE != kFwd) store_rows(yr, Ys, yp, p.dy_magic, tid);
+      auto prefetch = [&](int n) {
+        if (n >= nt) return;
+        const long long r = (first + g + n * step) * kTile + (tid & (kTile - 1));
+        if (tid < kTile)
+          prefetch_row(p.x, r, p.f.M);
+        else if (MODE != kFwd)
+          prefetch_row(p.dy, r, p.f.M);
       };
       auto arrive = [&](uint32_t bar) {
         fence_async_shared();
@@ -437,91 +559,157 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
       };
-      fetch(0);
-      store();
-      arrive(x_ready(g));
+      auto group_sync = [&]() {
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "n"(kGroupThreads) : "memory");
+      };
+      // the rows of step n; in weights mode the tile's old rows are free once out_done came
       uint32_t ph_gu = 0, ph_out = 0;
-      for (int n = 0; n < nt; ++n) {
-        for (int c = 0; c < nch; ++c) {
-          const bool more = c == nch - 1 && n + 1 < nt;
-          if (more) fetch(n + 1);
-          mbar_wait(gu_full(g), ph_gu, failed, status);
-          ph_gu ^= 1;
-          fence_after();
-          // this thread: row `row`, units half * 32 .. + 32
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int u0 = half * 32 + q * 8;
-            uint32_t ra[8], ru[8], rd[8];
-            tmem_ld8(d + u0, ra);
-            if (GATED) tmem_ld8(d + 64 + u0, ru);
-            if (MODE != kFwd) tmem_ld8(d + 128 + u0, rd);
-            tmem_wait(ra);
-            if (GATED) tmem_wait(ru);
-            if (MODE != kFwd) tmem_wait(rd);
-            float h[8], da[8], du[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float a = __uint_as_float(ra[e]);
-              const float u = GATED ? __uint_as_float(ru[e]) : 1.0f;
-              if (MODE == kFwd) {
-                h[e] = act_fast<ACT>(a);
-                if (GATED) h[e] *= u;
-              } else {
-                const float dh = __uint_as_float(rd[e]);
-                float sl;
-                const float f = act_slope_fast<ACT>(a, sl);
-                h[e] = GATED ? f * u : f;
-                da[e] = GATED ? dh * u * sl : dh * sl;
-                du[e] = dh * f;
-              }
-            }
-            const int at = row * 128 + (((u0 >> 3) ^ (row & 7)) << 4);
-            auto put = [&](int block, const float* v) {
-              *reinterpret_cast<uint4*>(Hs + block * 16384 + at) =
-                  make_uint4(Two<T>::pack(v[0], v[1]), Two<T>::pack(v[2], v[3]),
-                             Two<T>::pack(v[4], v[5]), Two<T>::pack(v[6], v[7]));
-            };
-            if (MODE == kFwd) {
-              put(0, h);
-            } else {
-              put(0, da);
-              if (GATED) put(1, du);
-              if (MODE == kDw) put(GATED ? 2 : 1, h);
-            }
-          }
-          // the tile's last first product is done: its rows may make room for the next tile's
-          if (MODE != kDw && more) store();
-          arrive(h_ready(g));
-        }
-        // the second product is done
+      auto wait_out = [&]() {
         mbar_wait(out_done(g), ph_out, failed, status);
         ph_out ^= 1;
         fence_after();
-        if (MODE == kDw) {
-          if (n + 1 < nt) {
-            store();
-            arrive(x_ready(g));
+      };
+      auto load = [&](int n, bool wait) {
+        const long long r0 = (first + g + n * step) * kTile;
+        uint4 bx[4], by[4];
+        if (p.x.aligned) fetch_rows(p.x, 0, r0, p.f.M, tid, bx);
+        if (MODE != kFwd && p.dy.aligned) fetch_rows(p.dy, 0, r0, p.f.M, tid, by);
+        if (wait) wait_out();
+        auto rest = [&](const RowSrc& src, int blocks, uint4 (&v)[4], uint8_t* dst) {
+          if (src.aligned) {
+            store_rows(0, tid, v, dst);
+            if (blocks > 1) {
+              fetch_rows(src, 1, r0, p.f.M, tid, v);
+              store_rows(1, tid, v, dst);
+            }
+          } else {
+            for (int b = 0; b < blocks; ++b) gather_rows(src, b, r0, p.f.M, tid, dst);
           }
-        } else {
-          const long long r = (first + g + n * step) * kTile + row;
-          const int cols = MODE == kFwd ? p.f.O : p.f.D;
-          const long long ld = MODE == kFwd ? p.f.ldy : p.f.lddx;
-          uint16_t* out = (uint16_t*)(MODE == kFwd ? p.f.y : p.f.dx) + r * ld;
-          const uint32_t src = d + (MODE == kFwd ? 128 : 192);
-          for (int e0 = half * 8; e0 < cols; e0 += 16) {
-            uint32_t v[8];
-            tmem_ld8(src + e0, v);
-            tmem_wait(v);
-            float o[8];
+        };
+        rest(p.x, nbx, bx, Xs);
+        if (MODE != kFwd) rest(p.dy, nby, by, Ys);
+        arrive(x_ready(g));
+      };
+      // this thread: row `row` of the tile, units half * 32 .. + 32, taken kUnits at a time; the
+      // next units' accumulators are on their way while one set is worked on
+      constexpr int kUnits = MODE == kFwd ? 16 : 8;
+      constexpr int kSteps = 32 / kUnits;
+      auto get = [&](int q, uint32_t (&ra)[kUnits], uint32_t (&ru)[kUnits],
+                     uint32_t (&rd)[kUnits]) {
+        const uint32_t at = d + half * 32 + q * kUnits;
+        tmem_ld(at, ra);
+        if (GATED) tmem_ld(at + 64, ru);
+        if (MODE != kFwd) tmem_ld(at + 128, rd);
+      };
+      auto work = [&](int q, const uint32_t (&ra)[kUnits], const uint32_t (&ru)[kUnits],
+                      const uint32_t (&rd)[kUnits]) {
+        uint32_t h[kUnits / 2], da[kUnits / 2], du[kUnits / 2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(v[e]);
-            if (r < p.f.M)
-              put8(out, e0, cols,
-                   make_uint4(Two<T>::pack(o[0], o[1]), Two<T>::pack(o[2], o[3]),
-                              Two<T>::pack(o[4], o[5]), Two<T>::pack(o[6], o[7])),
-                   p.out_vec);
+        for (int e = 0; e < kUnits; e += 4) {
+          float a[4], f[4], sl[4], vh[4], va[4], vu[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = __uint_as_float(ra[e + i]);
+          act4<ACT, MODE != kFwd>(a, f, sl);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float u = GATED ? __uint_as_float(ru[e + i]) : 1.0f;
+            vh[i] = GATED ? f[i] * u : f[i];
+            if (MODE != kFwd) {
+              const float dh = __uint_as_float(rd[e + i]);
+              va[i] = GATED ? dh * u * sl[i] : dh * sl[i];
+              vu[i] = dh * f[i];
+            }
           }
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            h[(e + i) / 2] = Two<T>::pack(vh[i], vh[i + 1]);
+            if (MODE != kFwd) {
+              da[(e + i) / 2] = Two<T>::pack(va[i], va[i + 1]);
+              du[(e + i) / 2] = Two<T>::pack(vu[i], vu[i + 1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kUnits; e += 8) {
+          const int piece = half * 4 + (q * kUnits + e) / 8;
+          uint8_t* at = Hs + row * 128 + ((piece ^ (row & 7)) << 4);
+          auto put = [&](int block, const uint32_t* v) {
+            *reinterpret_cast<uint4*>(at + block * 16384) = make_uint4(v[0], v[1], v[2], v[3]);
+          };
+          if (MODE == kFwd) {
+            put(0, h + e / 2);
+          } else {
+            put(0, da + e / 2);
+            if (GATED) put(1, du + e / 2);
+            if (MODE == kDw) put(GATED ? 2 : 1, h + e / 2);
+          }
+        }
+      };
+      auto landed = [&](uint32_t (&ra)[kUnits], uint32_t (&ru)[kUnits], uint32_t (&rd)[kUnits]) {
+        tmem_wait(ra);
+        if (GATED) tmem_wait(ru);
+        if (MODE != kFwd) tmem_wait(rd);
+      };
+
+      prefetch(1);
+      load(0, false);
+      for (int n = 0; n < nt; ++n) {
+        prefetch(n + 2);
+        for (int c = 0; c < nch; ++c) {
+          mbar_wait(gu_full(g), ph_gu, failed, status);
+          ph_gu ^= 1;
+          fence_after();
+          uint32_t a0[kUnits], u0[kUnits], d0[kUnits], a1[kUnits], u1[kUnits], d1[kUnits];
+          get(0, a0, u0, d0);
+#pragma unroll
+          for (int q = 0; q < kSteps; q += 2) {
+            landed(a0, u0, d0);
+            get(q + 1, a1, u1, d1);
+            work(q, a0, u0, d0);
+            landed(a1, u1, d1);
+            if (q + 2 < kSteps) get(q + 2, a0, u0, d0);
+            work(q + 1, a1, u1, d1);
+          }
+          arrive(h_ready(g));
+        }
+        // the tile's first products are done, so its rows make room for the next tile's (weights:
+        // after the second product, which reads them too)
+        const bool more = n + 1 < nt;
+        if (more) load(n + 1, MODE == kDw);
+        if (MODE != kDw) {
+          wait_out();
+          // results to shared memory (the hidden operand's place, free now), then out
+          const int cols = MODE == kFwd ? p.f.O : p.f.D;
+          const uint32_t src = d + (MODE == kFwd ? 128 : 192) + half * 32;
+          for (int b = 0; b * 64 < cols; ++b) {
+            if (b * 64 + half * 32 < cols) {
+              uint32_t v0[16], v1[16];
+              tmem_ld(src + b * 64, v0);
+              tmem_ld(src + b * 64 + 16, v1);  // (inside the accumulator's 32-column padding)
+              tmem_wait(v0);
+              tmem_wait(v1);
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) {
+                  const int i = (e + k) & 15;
+                  w[k / 2] = e < 16 ? Two<T>::pack(__uint_as_float(v0[i]), __uint_as_float(v0[i + 1]))
+                                    : Two<T>::pack(__uint_as_float(v1[i]), __uint_as_float(v1[i + 1]));
+                }
+                *reinterpret_cast<uint4*>(Hs + row * 128 +
+                                          (((half * 4 + e / 8) ^ (row & 7)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+            group_sync();
+            write_rows(Hs, (uint8_t*)(MODE == kFwd ? p.f.y : p.f.dx),
+                       2 * (MODE == kFwd ? p.f.ldy : p.f.lddx), p.out_aligned, b * 64, cols,
+                       (first + g + n * step) * kTile, p.f.M, tid);
+            group_sync();
+          }
+        } else if (!more) {
+          wait_out();
         }
       }
     }
@@ -545,7 +733,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
                                  : (row >= 64 ? FD : 0) + (size_t)f * p.f.D);
       for (int e0 = half * 8; e0 < cols; e0 += 16) {
         uint32_t v[8];
-        tmem_ld8((which ? acc_d : acc_gu) + row_lanes + e0, v);
+        tmem_ld((which ? acc_d : acc_gu) + row_lanes + e0, v);
         tmem_wait(v);
         if (mine)
 #pragma unroll
@@ -569,14 +757,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
 // host side
 // ---------------------------------------------------------------------------------------------
 
-int vec_of(const void* p, long long ld, int cols) {
-  const uintptr_t all = (uintptr_t)p | (uintptr_t)(ld * 2) | (uintptr_t)(cols * 2);
-  int v = 16;
-  while (v > 2 && (all & (uintptr_t)(v - 1))) v >>= 1;
-  return v;
+bool aligned16(const void* p, long long ld, int cols) {
+  return (((uintptr_t)p | (uintptr_t)(ld * 2) | (uintptr_t)(cols * 2)) & 15) == 0;
 }
 
-uint32_t magic_of(int d) { return (uint32_t)(((1ULL << 32) + d - 1) / d); }
+RowSrc row_src(const void* p, long long ld, long long rows, int cols) {
+  RowSrc s = {};
+  if (rows <= 0) return s;
+  s.base = (const uint8_t*)p;
+  s.ld = rows > 1 ? ld * 2 : 0;
+  s.cols = cols;
+  s.aligned = aligned16(p, s.ld / 2, cols);
+  s.lo = (const uint8_t*)(((uintptr_t)p + 15) & ~(uintptr_t)15);
+  s.hi = (const uint8_t*)(((uintptr_t)p + (uintptr_t)((rows - 1) * ld * 2 + cols * 2)) &
+                          ~(uintptr_t)15);
+  return s;
+}
 
 int pad16(int v) { return (v + 15) & ~15; }
 
@@ -586,12 +782,11 @@ int stage_bytes(int D, int O, bool gated) {
 
 template <int MODE, typename T, int ACT, bool GATED>
 int launch(TcArgs p, cudaStream_t st) {
-  p.x_vec = vec_of(p.f.x, p.f.M > 1 ? p.f.ldx : 0, p.f.D);
-  if (MODE != kFwd) p.dy_vec = vec_of(p.f.dy, p.f.M > 1 ? p.f.lddy : 0, p.f.O);
-  if (MODE == kFwd) p.out_vec = vec_of(p.f.y, p.f.M > 1 ? p.f.ldy : 0, p.f.O);
-  if (MODE == kDx) p.out_vec = vec_of(p.f.dx, p.f.M > 1 ? p.f.lddx : 0, p.f.D);
-  p.x_magic = magic_of(p.dp >> 3);
-  p.dy_magic = magic_of(p.op >> 3);
+  const bool one = p.f.M <= 1;  // a single row's stride is never used
+  p.x = row_src(p.f.x, p.f.ldx, p.f.M, p.f.D);
+  if (MODE != kFwd) p.dy = row_src(p.f.dy, p.f.lddy, p.f.M, p.f.O);
+  if (MODE == kFwd) p.out_aligned = aligned16(p.f.y, one ? 0 : p.f.ldy, p.f.O);
+  if (MODE == kDx) p.out_aligned = aligned16(p.f.dx, one ? 0 : p.f.lddx, p.f.D);
   const int nch = MODE == kDw ? 1 : p.nch, gb = smem_group(MODE, p.dp, p.op, GATED);
   const int extra = MODE == kDw ? ((p.dp + 31) & ~31) + ((p.op + 31) & ~31) : 0;
   // two groups where tensor memory and shared memory hold them with two weight stages

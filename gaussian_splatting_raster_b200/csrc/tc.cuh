@@ -93,12 +93,16 @@ __device__ __forceinline__ void commit(uint32_t bar) {
                : "memory");
 }
 
-// Shared-memory matrix descriptor, 128-byte swizzle. K-major: groups of 8 rows lie 1,024 bytes
-// apart (stride offset), the leading offset is not used. MN-major: groups of 8 K rows lie 1,024
-// bytes apart (stride offset), blocks of 64 columns `block_bytes` apart (leading offset).
-__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t block_bytes) {
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(block_bytes >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Shared-memory matrix descriptor, 128-byte swizzle: its low word (start address and leading
+// offset, in 16 bytes); the high word is the same for all tiles. K-major: groups of 8 rows lie
+// 1,024 bytes apart (stride offset), the leading offset is not used. MN-major: groups of 8 K rows
+// lie 1,024 bytes apart (stride offset), blocks of 64 columns `block_bytes` apart (leading offset).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t block_bytes) {
+  return ((addr & 0x3FFFF) >> 4) | ((block_bytes >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc(uint32_t lo) {
+  constexpr uint32_t hi = (1024 >> 4) | (1u << 14) | (2u << 29);
+  return ((uint64_t)hi << 32) | lo;
 }
 
 // Instruction descriptor: fp32 accumulator, both operands bf16 or both fp16, M = 128.
@@ -108,7 +112,23 @@ __device__ __forceinline__ uint32_t idesc(bool bf16, int n, bool a_mn, bool b_mn
          ((128u >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
+// One lane of a converged warp (the same one each time). Blocks that issue MMAs are entered under
+// it, in loops with fixed counts and descriptors formed beforehand: an MMA of 128 x 128 x 16 takes
+// 64 cycles, and with the lane chosen by an ordinary comparison and the descriptors formed inside
+// a counted loop its issue alone took 105.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n.reg .pred P;\n"
+      "elect.sync _|P, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, P;\n}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id,
+                                    bool add) {
+  const uint64_t a = desc(a_lo), b = desc(b_lo);
   asm volatile(
       "{\n.reg .pred p;\n"
       "setp.ne.u32 p, %4, 0;\n"
@@ -118,7 +138,7 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 }
 
 // 32 lanes x 16 (8) columns of fp32 from TMEM; lane = the warp's quadrant of rows
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -127,7 +147,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
         "=r"(v[14]), "=r"(v[15])
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&v)[8]) {
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[8]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
