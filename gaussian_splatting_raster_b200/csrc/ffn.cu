@@ -138,6 +138,110 @@ __global__ void __launch_bounds__(kT, 1) k_ffn(FfnArgs p) {
       }
 }
 
+// ---------------------------------------------------------------------------------------------
+// a few rows
+// ---------------------------------------------------------------------------------------------
+// Bound by latency: the weights have to come from L2 once. A cluster of eight CTAs shares kFew
+// rows; each CTA takes every eighth group of hidden units, a warp four units at a time (its lanes
+// along D, then one sum over the warp for each), and forms its part of y from them; the first CTA
+// adds the eight parts in order through distributed shared memory. x and the weights are read in
+// whole rows by neighbouring lanes whatever their alignment.
+constexpr int kCluster = 8;
+constexpr int kFew = 4;        // rows of a cluster
+constexpr int kFewThreads = 256;
+constexpr int kFewSingle = 18;   // up to one cluster a row fills the machine
+constexpr int kFewRows = 128;    // most rows taken this way
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <typename T, int ACT, bool GATED, int R>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kFewThreads)
+k_ffn_few(FfnArgs p) {
+  constexpr int kUnits = kMaxHidden / kCluster;  // most units of a CTA
+  __shared__ float s_h[R][kUnits];
+  __shared__ float s_y[kCluster][R][kMaxWidth];  // (the first CTA's is used)
+  // (the wait below: every CTA of the cluster has started before its shared memory is written)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int rank = blockIdx.x % kCluster, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long r0 = (long long)(blockIdx.x / kCluster) * R;
+  const T *x = (const T*)p.x, *wg = (const T*)p.wg, *wu = (const T*)p.wu, *wd = (const T*)p.wd;
+  const int per = (p.F + kCluster - 1) / kCluster;
+  const int f0 = min(p.F, rank * per), n = min(p.F, f0 + per) - f0;
+  float xr[R][4];  // columns lane + 32 k
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int d = lane + 32 * k;
+      xr[i][k] = d < p.D && r0 + i < p.M ? to_f<T>(x[(r0 + i) * p.ldx + d]) : 0.0f;
+    }
+  constexpr int U = 4;
+  for (int j0 = warp * U; j0 < n; j0 += kFewThreads / 32 * U) {
+    float wa[U][4], wb[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int d = lane + 32 * k;
+        const bool ok = d < p.D && j0 + u < n;
+        const size_t at = (size_t)(f0 + j0 + u) * p.D + d;
+        wa[u][k] = ok ? to_f<T>((GATED ? wg : wu)[at]) : 0.0f;
+        if (GATED) wb[u][k] = ok ? to_f<T>(wu[at]) : 0.0f;
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          a = fmaf(xr[i][k], wa[u][k], a);
+          if (GATED) b = fmaf(xr[i][k], wb[u][k], b);
+        }
+        a = warp_sum(a);
+        float h = act_of<ACT>(a);
+        if (GATED) h *= warp_sum(b);
+        if (lane == 0 && j0 + u < n) s_h[i][j0 + u] = to_f<T>(from_f<T>(h));
+      }
+  }
+  __syncthreads();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // this CTA's part of y, written into the first CTA's shared memory
+  float* dst = &s_y[rank][0][0];
+  uint64_t remote;
+  asm("mapa.u64 %0, %1, 0;" : "=l"(remote) : "l"(dst));
+  for (int o = warp; o < p.O; o += kFewThreads / 32) {
+    float acc[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) acc[i] = 0.0f;
+    for (int j = lane; j < n; j += 32) {
+      const float w = to_f<T>(wd[(size_t)o * p.F + f0 + j]);
+#pragma unroll
+      for (int i = 0; i < R; ++i) acc[i] = fmaf(s_h[i][j], w, acc[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      acc[i] = warp_sum(acc[i]);
+      if (lane == 0) reinterpret_cast<float*>(remote)[i * kMaxWidth + o] = acc[i];
+    }
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+  if (rank != 0) return;
+  T* y = (T*)p.y;
+  for (int q = threadIdx.x; q < R * p.O; q += kFewThreads) {
+    const int i = q / p.O, o = q - i * p.O;
+    float v = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) v += s_y[c][i][o];
+    if (r0 + i < p.M) y[(r0 + i) * p.ldy + o] = from_f<T>(v);
+  }
+}
+
 // a, u, dh of one 64-row tile and chunk, turned into da, du (and h) in place
 template <int ACT, bool GATED>
 __device__ __forceinline__ void hidden_grads(const float* Xs, const float* Ys, const float* Ws,
@@ -359,6 +463,17 @@ int dw_splits(long long M, int F) {
 }
 
 template <typename T, int ACT, bool GATED>
+int run_few(const FfnArgs& p, cudaStream_t st) {
+  if (p.M <= kFewSingle) {
+    k_ffn_few<T, ACT, GATED, 1><<<p.M * kCluster, kFewThreads, 0, st>>>(p);
+  } else {
+    k_ffn_few<T, ACT, GATED, kFew>
+        <<<(p.M + kFew - 1) / kFew * kCluster, kFewThreads, 0, st>>>(p);
+  }
+  return last_error();
+}
+
+template <typename T, int ACT, bool GATED>
 int run_forward(const FfnArgs& p, cudaStream_t st) {
   const int smem = fwd_smem(p.D, p.O);
   const unsigned grid = (unsigned)(((long long)p.M + kFwdRows - 1) / kFwdRows);
@@ -395,30 +510,36 @@ int run_backward(const FfnArgs& p, cudaStream_t st) {
   return last_error();
 }
 
+// A few rows by the clusters; otherwise fp32 on the fp32 lanes, bf16 and fp16 on the tensor cores.
 template <typename T, int ACT, bool GATED>
-int run(const FfnArgs& p, bool backward, cudaStream_t st) {
-  return backward ? run_backward<T, ACT, GATED>(p, st) : run_forward<T, ACT, GATED>(p, st);
-}
-
-// fp32 on the fp32 lanes, bf16 and fp16 on the tensor cores
-int dispatch(FfnArgs& p, int dtype, int act, bool backward, void* scratch, cudaStream_t st) {
-  const bool gated = p.wg != nullptr;
-  if (dtype == SPLAT_F32) {
+int run(FfnArgs& p, int dtype, bool backward, void* scratch, cudaStream_t st) {
+  if (!backward && p.M <= kFewRows) return run_few<T, ACT, GATED>(p, st);
+  if constexpr (sizeof(T) == 4) {
     p.part = (float*)scratch;
     p.splits = dw_splits(p.M, p.F);
-    if (act == SPLAT_ACT_SILU)
-      return gated ? run<float, SPLAT_ACT_SILU, true>(p, backward, st)
-                   : run<float, SPLAT_ACT_SILU, false>(p, backward, st);
-    return gated ? run<float, SPLAT_ACT_GELU, true>(p, backward, st)
-                 : run<float, SPLAT_ACT_GELU, false>(p, backward, st);
+    return backward ? run_backward<T, ACT, GATED>(p, st) : run_forward<T, ACT, GATED>(p, st);
+  } else {
+    p.part = (float*)((char*)scratch + ffn_tc_image_bytes(p.D, p.F, p.O, GATED));
+    p.splits = ffn_tc_splits(p.M, p.F);
+    const int rc = ffn_tc_run(p, dtype, ACT, backward, scratch, st);
+    if (rc != SPLAT_OK || !(p.dwg || p.dwu || p.dwd)) return rc;
+    return run_join<T, GATED>(p, st);
   }
-  p.part = (float*)((char*)scratch + ffn_tc_image_bytes(p.D, p.F, p.O, gated));
-  p.splits = ffn_tc_splits(p.M, p.F);
-  const int rc = ffn_tc_run(p, dtype, act, backward, scratch, st);
-  if (rc != SPLAT_OK || !(p.dwg || p.dwu || p.dwd)) return rc;
-  if (dtype == SPLAT_BF16)
-    return gated ? run_join<__nv_bfloat16, true>(p, st) : run_join<__nv_bfloat16, false>(p, st);
-  return gated ? run_join<__half, true>(p, st) : run_join<__half, false>(p, st);
+}
+
+template <typename T>
+int run_type(FfnArgs& p, int dtype, int act, bool backward, void* scratch, cudaStream_t st) {
+  if (act == SPLAT_ACT_SILU)
+    return p.wg ? run<T, SPLAT_ACT_SILU, true>(p, dtype, backward, scratch, st)
+                : run<T, SPLAT_ACT_SILU, false>(p, dtype, backward, scratch, st);
+  return p.wg ? run<T, SPLAT_ACT_GELU, true>(p, dtype, backward, scratch, st)
+              : run<T, SPLAT_ACT_GELU, false>(p, dtype, backward, scratch, st);
+}
+
+int dispatch(FfnArgs& p, int dtype, int act, bool backward, void* scratch, cudaStream_t st) {
+  if (dtype == SPLAT_F32) return run_type<float>(p, dtype, act, backward, scratch, st);
+  if (dtype == SPLAT_BF16) return run_type<__nv_bfloat16>(p, dtype, act, backward, scratch, st);
+  return run_type<__half>(p, dtype, act, backward, scratch, st);
 }
 
 int check_sizes(int M, int D, int F, int O, int dtype, int act) {
@@ -439,6 +560,7 @@ extern "C" {
 
 long long splat_ffn_scratch(int M, int D, int F, int O, int dtype, int gated, int backward) {
   if (check_sizes(M, D, F, O, dtype, SPLAT_ACT_SILU) != SPLAT_OK) return 0;
+  if (!backward && M <= kFewRows) return 0;
   const bool tc = dtype != SPLAT_F32;
   long long n = tc ? (long long)ffn_tc_image_bytes(D, F, O, gated != 0) : 0;
   if (backward)
@@ -521,15 +643,6 @@ int splat_ffn_backward(const void* dy, long long ld_dy, const void* x, long long
   p.O = O;
   cudaStream_t st = (cudaStream_t)stream;
   return dispatch(p, dtype, act, true, scratch, st);
-}
-
-int splat_rows_status(void* stream) {
-  unsigned int v = 0;
-  if (rows_status_take(&v, (cudaStream_t)stream) != cudaSuccess) {
-    cudaGetLastError();
-    return SPLAT_ERR_CUDA;
-  }
-  return v ? SPLAT_ERR_DEVICE_TIMEOUT : SPLAT_OK;
 }
 
 }  // extern "C"

@@ -56,8 +56,6 @@ __device__ __forceinline__ float act_and_slope(float a, float& slope) {
 size_t ffn_tc_image_bytes(int D, int F, int O, bool gated);
 int ffn_tc_splits(long long M, int F);
 int ffn_tc_run(const FfnArgs& f, int dtype, int act, bool backward, void* img, cudaStream_t st);
-// the status word of their waits, read and cleared (waits for the stream)
-cudaError_t rows_status_take(unsigned int* out, cudaStream_t st);
 
 }  // namespace rows
 }  // namespace splat

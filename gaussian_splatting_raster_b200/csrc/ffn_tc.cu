@@ -857,7 +857,7 @@ int ffn_tc_run(const FfnArgs& f, int dtype, int act, bool backward, void* img, c
                              : run_type<__half>(f, act, backward, (uint8_t*)img, st);
 }
 
-cudaError_t rows_status_take(unsigned int* out, cudaStream_t st) {
+cudaError_t ffn_status_take(unsigned int* out, cudaStream_t st) {
   const unsigned int zero = 0;
   cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_rows_status, sizeof *out, 0,
                                             cudaMemcpyDeviceToHost, st);

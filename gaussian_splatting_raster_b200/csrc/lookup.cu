@@ -17,6 +17,8 @@
 // them. A group of lanes that spans one row sums kRun consecutive entries; runs that end inside
 // the group are written at once, the rest are joined first within the CTA (shared memory), then
 // across CTAs from fp32 partial rows by the finishing kernel, which also zeroes rows nobody uses.
+#include <algorithm>
+
 #include "rows.cuh"
 
 namespace splat {
@@ -43,6 +45,18 @@ template <typename T, int VB> union Vec {
   __device__ Vec() {}
 };
 
+// a row's vector: as one access where it lies inside the array (the elements behind the row's end
+// belong to the gap or the next row and are not used), else its n elements
+template <typename T, int VB>
+__device__ __forceinline__ void get_row(Vec<T, VB>& v, const T* p, int n, const T* end) {
+  if (p + Vec<T, VB>::N <= end) {
+    v.raw = __ldg(reinterpret_cast<const typename Bytes<VB>::type*>(p));
+  } else {
+#pragma unroll
+    for (int e = 0; e < Vec<T, VB>::N; ++e) v.e[e] = e < n ? p[e] : from_f<T>(0.0f);
+  }
+}
+
 // ---------------------------------------------------------------------------------------------
 // lookup
 // ---------------------------------------------------------------------------------------------
@@ -52,11 +66,12 @@ template <typename T, int VB> union Vec {
 template <typename T, int VB>
 __global__ void __launch_bounds__(kThreads)
 k_lookup(const T* __restrict__ table, long long ldt, unsigned N, const int* __restrict__ ids,
-         long long M, int vpr, uint32_t magic, int rpb, float scale, T* __restrict__ out,
+         long long M, int C, int vpr, uint32_t magic, int rpb, float scale, T* __restrict__ out,
          long long ldo) {
   using V = Vec<T, VB>;
   constexpr int U = 4;
   const long long r0 = (long long)blockIdx.x * rpb;
+  const T* end = table + (long long)(N - 1) * ldt + C;
   const int nv = (int)min((long long)rpb, M - r0) * vpr;
   for (int l0 = threadIdx.x; l0 < nv; l0 += kThreads * U) {
     V v[U];
@@ -71,8 +86,7 @@ k_lookup(const T* __restrict__ table, long long ldt, unsigned N, const int* __re
 #pragma unroll
       for (int e = 0; e < V::N; ++e) v[k].e[e] = from_f<T>(0.0f);
       if (id < N)
-        v[k].raw = __ldg(reinterpret_cast<const typename Bytes<VB>::type*>(
-            table + (long long)id * ldt + col[k]));
+        get_row<T, VB>(v[k], table + (long long)id * ldt + col[k], C - col[k], end);
       else
         row[k] = ~row[k];  // a zero row, not scaled: s may be infinite
     }
@@ -86,8 +100,14 @@ k_lookup(const T* __restrict__ table, long long ldt, unsigned N, const int* __re
       } else {
         r = ~r;
       }
-      __stcs(reinterpret_cast<typename Bytes<VB>::type*>(out + (r0 + r) * ldo + col[k]),
-             v[k].raw);
+      T* dst = out + (r0 + r) * ldo + col[k];
+      if (col[k] + V::N <= C) {
+        __stcs(reinterpret_cast<typename Bytes<VB>::type*>(dst), v[k].raw);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V::N; ++e)
+          if (col[k] + e < C) dst[e] = v[k].e[e];
+      }
     }
   }
 }
@@ -95,107 +115,90 @@ k_lookup(const T* __restrict__ table, long long ldt, unsigned N, const int* __re
 // ---------------------------------------------------------------------------------------------
 // stable order of the ids
 // ---------------------------------------------------------------------------------------------
+// LSD radix sort of (id, row) pairs, digits of up to 10 bits. One kernel reads the ids once for the
+// digit totals of every pass and for whether they are in order already; each pass is then one
+// kernel of at most 296 CTAs, two to an SM, each with a contiguous share of the items: it counts
+// its digits, learns from its predecessors how many of each lie before (look-back: every CTA
+// publishes its own counts, and the sum including all before it as soon as it has that), then
+// takes its share tile by tile, ranks a tile in shared memory, puts it in digit order there and
+// writes runs. (One tile a CTA would read its items once less, but 720 CTAs at 5.9 M items then
+// wait for one another in a chain: 123 us a pass.)
+
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+
+__device__ unsigned int g_lookup_status;
 
 __device__ __forceinline__ uint32_t key_of(int id, uint32_t N) {
   return (uint32_t)id < N ? (uint32_t)id : N;  // what belongs to no row sorts last
 }
 
-// Digit counts of each CTA's items. FIRST: from the ids; also marks CTAs that hold a descent (so
-// the order of the ids needs no sort when there is none) and clears the runs' bounds. Later
-// passes read pairs and do nothing when the ids were in order.
-template <bool FIRST>
-__global__ void __launch_bounds__(kThreads)
-k_hist(const int* __restrict__ ids, const uint2* __restrict__ pairs, unsigned M, uint32_t N,
-       int shift, int bits, unsigned per_block, int* __restrict__ hist, int* __restrict__ descent,
-       const int* __restrict__ unsorted, uint2* __restrict__ bounds) {
-  __shared__ int cnt[kMaxDigits];
-  if (!FIRST && !*unsorted) return;
-  const int nd = 1 << bits;
-  for (int d = threadIdx.x; d < nd; d += kThreads) cnt[d] = 0;
+struct SortArgs {
+  const int* ids;
+  uint2 *in, *out;
+  unsigned M;
+  uint32_t N;
+  int pass, passes, bits;
+  int vec;              // ids lie at 16 bytes
+  uint2* bounds;        // [N] first and one-past-last sorted entry of each id
+  // cleared before each call:
+  int* total;           // [passes][1 << bits] items of each digit
+  int* unsorted;        // whether some id is smaller than the one before it
+  unsigned* ticket;     // [passes] CTAs started
+  unsigned* state;      // [passes][CTAs][1 << bits] look-back words
+  unsigned nblk, share;  // CTAs of a pass, items of one
+};
+
+__global__ void __launch_bounds__(kThreads) k_clear(uint4* p, long long n) {
+  for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n;
+       i += (long long)gridDim.x * kThreads)
+    p[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+__global__ void __launch_bounds__(kThreads) k_survey(SortArgs a) {
+  __shared__ int cnt[3 * kMaxDigits];
+  const int nd = 1 << a.bits, n = a.passes * nd;
+  for (int d = threadIdx.x; d < n; d += kThreads) cnt[d] = 0;
   __syncthreads();
-  const unsigned b = blockIdx.x * per_block, e = min(M, b + per_block);
   int down = 0;
-  for (unsigned i = b + threadIdx.x; i < e; i += kThreads) {
-    uint32_t k;
-    if (FIRST) {
-      k = key_of(ids[i], N);
-      if (i > 0 && key_of(ids[i - 1], N) > k) down = 1;
-    } else {
-      k = pairs[i].x;
-    }
-    atomicAdd(&cnt[(k >> shift) & (nd - 1)], 1);
-  }
-  if (FIRST) {
-    down = __syncthreads_or(down);
-    if (threadIdx.x == 0) descent[blockIdx.x] = down;
-    for (unsigned n = blockIdx.x * kThreads + threadIdx.x; n < N; n += gridDim.x * kThreads)
-      bounds[n] = make_uint2(0u, 0u);
-  } else {
-    __syncthreads();
-  }
-  for (int d = threadIdx.x; d < nd; d += kThreads)
-    hist[(size_t)d * gridDim.x + blockIdx.x] = cnt[d];
-}
-
-// Per digit (one warp each): its counts over the CTAs, scanned in place, and their total. FIRST:
-// digit 0's warp also folds the descent marks into the one flag the other kernels read.
-template <bool FIRST>
-__global__ void __launch_bounds__(kThreads)
-k_digit_scan(int* __restrict__ hist, int nblk, int nd, int* __restrict__ total,
-             const int* __restrict__ descent, int* __restrict__ unsorted) {
-  const int d = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (d >= nd) return;
-  if (!FIRST && !*unsorted) return;
-  int* h = hist + (size_t)d * nblk;
-  int run = 0, any = 0;
-  for (int b = 0; b < nblk; b += 32) {
-    const int i = b + lane;
-    const int c = i < nblk ? h[i] : 0;
-    if (FIRST && d == 0 && i < nblk) any |= descent[i];
-    int s = c;
+  // threads take 16 consecutive ids at a time (a warp's loads share their lines)
+  const unsigned long long stride = (unsigned long long)gridDim.x * kThreads * 16;
+  for (unsigned long long i0 = (blockIdx.x * (unsigned long long)kThreads + threadIdx.x) * 16;
+       i0 < a.M; i0 += stride) {
+    int id[16];
+    uint32_t prev = i0 > 0 ? key_of(a.ids[i0 - 1], a.N) : 0u;
+    if (a.vec && i0 + 16 <= a.M) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += t;
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<int4*>(id + 4 * k) =
+            __ldg(reinterpret_cast<const int4*>(a.ids + i0) + k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) id[k] = i0 + k < a.M ? a.ids[i0 + k] : -1;
     }
-    if (i < nblk) h[i] = run + s - c;
-    run += __shfl_sync(0xffffffffu, s, 31);
+    const int n = (int)min(16ULL, a.M - i0);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (k >= n) break;
+      const uint32_t key = key_of(id[k], a.N);
+      if (prev > key) down = 1;
+      prev = key;
+      for (int p = 0; p < a.passes; ++p)
+        atomicAdd(&cnt[p * nd + ((key >> (p * a.bits)) & (nd - 1))], 1);
+    }
   }
-  if (lane == 0) total[d] = run;
-  if (FIRST && d == 0) {
-    any = __any_sync(0xffffffffu, any);
-    if (lane == 0) *unsorted = any;
-  }
+  down = __syncthreads_or(down);
+  if (threadIdx.x == 0 && down) *a.unsorted = 1;
+  for (int d = threadIdx.x; d < n; d += kThreads)
+    if (cnt[d]) atomicAdd(&a.total[d], cnt[d]);
+  for (unsigned i = blockIdx.x * kThreads + threadIdx.x; i < a.N; i += gridDim.x * kThreads)
+    a.bounds[i] = make_uint2(0u, 0u);
 }
 
-// Stable scatter of one pass. Each warp owns a contiguous part of the CTA's items: its digit
-// counts are taken first, then every item's place is its digit's base (digits before, CTAs
-// before, warps before) plus its rank among the warp's earlier items of that digit.
-template <bool FIRST>
-__global__ void __launch_bounds__(kThreads)
-k_scatter_pairs(const int* __restrict__ ids, const uint2* __restrict__ in, unsigned M, uint32_t N,
-                int shift, int bits, unsigned per_block, const int* __restrict__ hist,
-                const int* __restrict__ total, const int* __restrict__ unsorted,
-                uint2* __restrict__ out) {
-  __shared__ int cnt[kWarps][kMaxDigits];
-  __shared__ int wsum[kWarps];
-  if (!*unsorted) return;
-  const int nd = 1 << bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int d = threadIdx.x; d < nd * kWarps; d += kThreads) cnt[d / nd][d % nd] = 0;
-  __syncthreads();
-  const unsigned per_warp = per_block / kWarps;  // a multiple of 32
-  const unsigned wb = min(M, blockIdx.x * per_block + warp * per_warp), we = min(M, wb + per_warp);
-  for (unsigned i = wb + lane; i < we; i += 32) {
-    const uint32_t k = FIRST ? key_of(ids[i], N) : in[i].x;
-    atomicAdd(&cnt[warp][(k >> shift) & (nd - 1)], 1);
-  }
-  __syncthreads();
-  // thread t owns digits [t * q, t * q + q): exclusive scan of the digits' totals over the CTA
-  const int q = (nd + kThreads - 1) / kThreads;
-  const int d0 = threadIdx.x * q;
-  int mine = 0;
-  for (int d = d0; d < min(nd, d0 + q); ++d) mine += total[d];
-  int s = mine;
+// exclusive sum over the CTA of one value per thread
+__device__ __forceinline__ int cta_exclusive(int v, int* wsum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int s = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int t = __shfl_up_sync(0xffffffffu, s, o);
@@ -203,33 +206,179 @@ k_scatter_pairs(const int* __restrict__ ids, const uint2* __restrict__ in, unsig
   }
   if (lane == 31) wsum[warp] = s;
   __syncthreads();
-  int base = s - mine;
+  int base = s - v;
   for (int w = 0; w < warp; ++w) base += wsum[w];
-  for (int d = d0; d < min(nd, d0 + q); ++d) {
-    int at = base + hist[(size_t)d * gridDim.x + blockIdx.x];
-    base += total[d];
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const int c = cnt[w][d];
-      cnt[w][d] = at;
-      at += c;
-    }
+  __syncthreads();
+  return base;
+}
+
+// Look-back words: 0 nothing yet; the CTA's own count plus one; or, with the top bit, the count of
+// all CTAs up to and including it (at most 2^31 - 1).
+enum : unsigned { kAll = 1u << 31 };
+
+// items of a thread and tile: ITEMS, each warp's contiguous, a lane's 32 apart
+template <int ITEMS>
+__global__ void __launch_bounds__(kSortThreads, 2) k_sort_pass(SortArgs a) {
+  extern __shared__ __align__(16) int sort_smem[];
+  __shared__ int wsum[kSortWarps];
+  __shared__ unsigned s_blk;
+  if (!*a.unsorted) return;
+  const int nd = 1 << a.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int shift = a.pass * a.bits;
+  constexpr int kItems = kSortThreads * ITEMS;
+  uint32_t* mask = reinterpret_cast<uint32_t*>(sort_smem);  // [warps][nd] lanes that hold a digit;
+  uint2* sorted = reinterpret_cast<uint2*>(sort_smem);      // then the tile's items in digit order
+  int* next = sort_smem + max(kSortWarps * nd, 2 * kItems);  // [nd] global place of the next item
+  int* delta = next + nd;                                    // [nd] global minus local place
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(delta + nd);   // [warps][nd]
+  // CTAs number themselves in the order they start, so those a CTA looks back to have started
+  if (threadIdx.x == 0) s_blk = atomicAdd(&a.ticket[a.pass], 1u);
+  for (int d = threadIdx.x; d < nd; d += kSortThreads) next[d] = 0;
+  __syncthreads();
+  const unsigned blk = s_blk;
+  const unsigned begin = min(a.M, blk * a.share), end = min(a.M, begin + a.share);
+  auto item = [&](unsigned i) {
+    return a.pass == 0 ? make_uint2(key_of(a.ids[i], a.N), i) : a.in[i];
+  };
+#pragma unroll 8
+  for (unsigned i = begin + threadIdx.x; i < end; i += kSortThreads) {
+    const uint32_t k = a.pass == 0 ? key_of(a.ids[i], a.N) : a.in[i].x;
+    atomicAdd(&next[(k >> shift) & (nd - 1)], 1);
   }
   __syncthreads();
-  for (unsigned b = wb; b < we; b += 32) {
-    const unsigned i = b + lane;
-    const bool ok = i < we;
-    uint2 kv = make_uint2(0u, 0u);
-    if (ok) kv = FIRST ? make_uint2(key_of(ids[i], N), i) : in[i];
-    const uint32_t dig = ok ? (kv.x >> shift) & (nd - 1) : (uint32_t)nd + lane;
-    const uint32_t peers = __match_any_sync(0xffffffffu, dig);
-    const int rank = __popc(peers & ((1u << lane) - 1u));
-    int at = 0;
-    if (ok) at = cnt[warp][dig] + rank;
-    __syncwarp();
-    if (ok && rank == 0) cnt[warp][dig] += __popc(peers);
-    __syncwarp();
-    if (ok) out[at] = kv;
+  // thread t owns digits [t q, t q + q)
+  const int q = (nd + kSortThreads - 1) / kSortThreads;  // 1 or 2
+  const int d0 = threadIdx.x * q;
+  unsigned* state = a.state + (size_t)a.pass * a.nblk * nd;
+  int tot[2] = {0, 0}, own[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int d = d0 + j;
+    if (j >= q || d >= nd) continue;
+    own[j] = next[d];
+    tot[j] = a.total[a.pass * nd + d];
+    *(volatile unsigned*)(state + (size_t)blk * nd + d) =
+        blk == 0 ? kAll | (unsigned)own[j] : (unsigned)own[j] + 1u;
+  }
+  const int gbase = cta_exclusive(tot[0] + tot[1], wsum);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int d = d0 + j;
+    if (j >= q || d >= nd) continue;
+    // items of the digit in earlier CTAs, eight of them asked at a time
+    unsigned before = 0;
+    const long long t0 = clock64();
+    for (unsigned p = blk; p > 0;) {
+      unsigned w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        w[k] = p > k ? *(volatile unsigned*)(state + (size_t)(p - 1 - k) * nd + d) : kAll;
+      const unsigned asked = p;
+      bool done = false;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (done || p != asked - k || w[k] == 0) continue;  // w = 0: not published yet
+        if (w[k] & kAll) {
+          before += w[k] & ~kAll;
+          done = true;
+        } else {
+          before += w[k] - 1u;
+          --p;
+        }
+      }
+      if (done) break;
+      if (p == asked && clock64() - t0 > 8000000000LL) {
+        atomicOr(&g_lookup_status, 1u);
+        break;
+      }
+    }
+    if (blk > 0)
+      *(volatile unsigned*)(state + (size_t)blk * nd + d) = kAll | (before + (unsigned)own[j]);
+    next[d] = gbase + (j ? tot[0] : 0) + (int)before;
+  }
+  for (unsigned t0 = begin; t0 < end; t0 += kItems) {
+    const unsigned n = min((unsigned)kItems, end - t0);
+    const unsigned b = t0 + warp * 32 * ITEMS;
+    __syncthreads();
+    for (int d = threadIdx.x; d < nd * kSortWarps; d += kSortThreads) {
+      mask[d] = 0u;
+      cnt[d] = 0;
+    }
+    uint2 kv[ITEMS];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const unsigned i = b + k * 32 + lane;
+      kv[k] = make_uint2(0xFFFFFFFFu, 0u);
+      if (i < end) kv[k] = item(i);
+    }
+    __syncthreads();
+    // ranks within the warp: a digit's count so far plus the lanes before that hold it too. The
+    // lanes find each other through a word per digit (one vote per bit, or the match instruction,
+    // took twice as long).
+    uint16_t rank[ITEMS];
+    uint16_t* mine = cnt + warp * nd;
+    uint32_t* lanes = mask + warp * nd;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const bool ok = b + k * 32 + lane < end;
+      const uint32_t dig = (kv[k].x >> shift) & (nd - 1);
+      if (ok) atomicOr(&lanes[dig], 1u << lane);
+      __syncwarp();
+      uint32_t peers = 0u, base = 0u;
+      if (ok) {
+        peers = lanes[dig];
+        base = mine[dig];
+      }
+      const uint32_t before = __popc(peers & ((1u << lane) - 1u));
+      __syncwarp();
+      if (ok && before == 0) {
+        mine[dig] = (uint16_t)(base + __popc(peers));
+        lanes[dig] = 0u;
+      }
+      __syncwarp();
+      rank[k] = (uint16_t)(base + before);
+    }
+    __syncthreads();
+    int sum[2] = {0, 0};
+    uint16_t c[2][kSortWarps];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int d = d0 + j;
+      if (j >= q || d >= nd) continue;
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) c[j][w] = cnt[w * nd + d];
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) sum[j] += c[j][w];
+    }
+    const int lbase = cta_exclusive(sum[0] + sum[1], wsum);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int d = d0 + j;
+      if (j >= q || d >= nd) continue;
+      int l = lbase + (j ? sum[0] : 0);
+      delta[d] = next[d] - l;
+      next[d] += sum[j];
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) {  // a tile has at most 8,192 items
+        cnt[w * nd + d] = (uint16_t)l;
+        l += c[j][w];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)
+      if (b + k * 32 + lane < end)
+        rank[k] = (uint16_t)(rank[k] + mine[(kv[k].x >> shift) & (nd - 1)]);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)
+      if (b + k * 32 + lane < end) sorted[rank[k]] = kv[k];
+    __syncthreads();
+    for (unsigned i = threadIdx.x; i < n; i += kSortThreads) {
+      const uint2 v = sorted[i];
+      const unsigned at = i + delta[(v.x >> shift) & (nd - 1)];
+      if (at < a.M) a.out[at] = v;  // (always, unless a wait ran out)
+    }
   }
 }
 
@@ -251,17 +400,23 @@ struct RunArgs {
   float* tail;    // [CTAs][C] part of the run that leaves it, when it starts in it
 };
 
-__device__ __forceinline__ uint2 entry(const RunArgs& a, bool sorted, unsigned i) {
-  return sorted ? make_uint2(key_of(a.ids[i], a.N), i) : a.pairs[i];
-}
-
+// n of a vector's elements (a row's last vector may be short)
 template <typename T, int VB>
-__device__ __forceinline__ void put_row(T* dst, const float* acc, float scale) {
+__device__ __forceinline__ void put_row(T* dst, const float* acc, float scale, int n) {
   Vec<T, VB> v;
 #pragma unroll
   for (int e = 0; e < Vec<T, VB>::N; ++e) v.e[e] = from_f<T>(scale * acc[e]);
-  *reinterpret_cast<typename Bytes<VB>::type*>(dst) = v.raw;
+  if (n >= Vec<T, VB>::N && ((uintptr_t)dst & (VB - 1)) == 0) {
+    *reinterpret_cast<typename Bytes<VB>::type*>(dst) = v.raw;
+  } else {
+#pragma unroll
+    for (int e = 0; e < Vec<T, VB>::N; ++e)
+      if (e < n) dst[e] = v.e[e];
+  }
 }
+
+constexpr int kMinLanes = 4;  // lanes per row at least: bounds the staged entries
+constexpr int kMaxEntries = kThreads / kMinLanes * kRun;
 
 template <typename T, int VB>
 __global__ void __launch_bounds__(kThreads)
@@ -269,60 +424,71 @@ k_runs(RunArgs a, const T* __restrict__ dout, long long ldd, T* __restrict__ dta
        long long ldt) {
   using V = Vec<T, VB>;
   constexpr int VE = V::N;
-  __shared__ float s_head[kThreads * VE], s_tail[kThreads * VE];
-  __shared__ uint8_t s_kind[kThreads];  // per group: bit 0 head ends here, bit 1 head passes
-                                        // through, bit 2 a run starts and leaves
+  // the CTA's entries; then, in the same place, the groups' sums of runs that cross them
+  __shared__ __align__(16) uint2 s_entry[kMaxEntries + 2];
+  static_assert(sizeof(s_entry) >= 2 * kThreads * VE * sizeof(float), "");
+  __shared__ uint8_t s_kind[kThreads / kMinLanes];  // per group: bit 0 head ends here, bit 1 head
+                                                    // passes through, bit 2 a run starts and leaves
   const int GL = 1 << a.gl_log, NG = kThreads >> a.gl_log;
   const int g = threadIdx.x >> a.gl_log, gl = threadIdx.x & (GL - 1);
   const int col = (blockIdx.y * GL + gl) * VE;
-  const bool act = col < a.C;
+  const int left = a.C - col;  // elements of the row from here on
+  const bool act = left > 0;
   const bool sorted = !*a.unsorted;
   const unsigned blk0 = blockIdx.x * (unsigned)(NG * kRun);
-  const unsigned i0 = min(a.M, blk0 + g * kRun), i1 = min(a.M, i0 + kRun);
+  const int count = (int)min((unsigned)(NG * kRun), a.M - blk0);
+  // entries blk0 - 1 .. blk0 + count: entry i of the CTA is s_entry[i + 1]
+  for (int i = threadIdx.x; i < count + 2; i += kThreads) {
+    uint2 kv = make_uint2(0xFFFFFFFFu, 0u);  // no id
+    const long long j = (long long)blk0 + i - 1;
+    if (j >= 0 && j < a.M)
+      kv = sorted ? make_uint2(key_of(a.ids[j], a.N), (uint32_t)j) : a.pairs[j];
+    if (kv.y >= a.M) kv.x = a.N;  // (only when a wait of the sort ran out)
+    s_entry[i] = kv;
+  }
+  __syncthreads();
+  const T* end = dout + (long long)(a.M - 1) * ldd + a.C;
+  const int i0 = min(count, g * kRun), i1 = min(count, i0 + kRun);
   const bool mark = gl == 0 && blockIdx.y == 0;
   int kind = 0;
   uint32_t leaving = a.N;  // the id of the run that leaves
-  float acc[VE];
+  float acc[VE], first[VE];  // the run at hand; the one that entered, once it ended
 #pragma unroll
-  for (int e = 0; e < VE; ++e) acc[e] = 0.0f;
+  for (int e = 0; e < VE; ++e) acc[e] = first[e] = 0.0f;
   if (i0 < i1) {
-    uint32_t cur = entry(a, sorted, i0).x;
-    bool head = i0 > 0 && entry(a, sorted, i0 - 1).x == cur;
-    if (!head && mark && cur < a.N) a.bounds[cur].x = i0;
-    constexpr int U = 4;
-    for (unsigned i = i0; i < i1 && cur < a.N; i += U) {
-      uint2 kv[U];
+    uint32_t cur = s_entry[i0 + 1].x;
+    bool head = s_entry[i0].x == cur;
+    if (!head && mark && cur < a.N) a.bounds[cur].x = blk0 + i0;
+    constexpr int U = VB == 16 ? 4 : 8;
+    for (int i = i0; i < i1 && cur < a.N; i += U) {
+      uint32_t key[U];
       V v[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        kv[k] = make_uint2(a.N, 0u);
-        if (i + k < i1) kv[k] = entry(a, sorted, i + k);
-      }
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
+        const uint2 kv = s_entry[min(i + k, i1 - 1) + 1];
+        key[k] = kv.x;
 #pragma unroll
         for (int e = 0; e < VE; ++e) v[k].e[e] = from_f<T>(0.0f);
-        if (kv[k].x < a.N && act)
-          v[k].raw = __ldcs(reinterpret_cast<const typename Bytes<VB>::type*>(
-              dout + (long long)kv[k].y * ldd + col));
+        if (i + k < i1 && kv.x < a.N && act)
+          get_row<T, VB>(v[k], dout + (long long)kv.y * ldd + col, left, end);
       }
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         if (i + k >= i1) break;
-        if (kv[k].x != cur) {  // the run before ended at i + k
+        if (key[k] != cur) {  // the run before ended at i + k
           if (cur < a.N) {
             if (head) {
               kind |= 1;
 #pragma unroll
-              for (int e = 0; e < VE; ++e) s_head[threadIdx.x * VE + e] = acc[e];
+              for (int e = 0; e < VE; ++e) first[e] = acc[e];
             } else if (act) {
-              put_row<T, VB>(dtable + (long long)cur * ldt + col, acc, a.scale);
+              put_row<T, VB>(dtable + (long long)cur * ldt + col, acc, a.scale, left);
             }
-            if (mark) a.bounds[cur].y = i + k;
+            if (mark) a.bounds[cur].y = blk0 + i + k;
           }
-          cur = kv[k].x;
+          cur = key[k];
           head = false;
-          if (mark && cur < a.N) a.bounds[cur].x = i + k;
+          if (mark && cur < a.N) a.bounds[cur].x = blk0 + i + k;
 #pragma unroll
           for (int e = 0; e < VE; ++e) acc[e] = 0.0f;
         }
@@ -331,43 +497,45 @@ k_runs(RunArgs a, const T* __restrict__ dout, long long ldd, T* __restrict__ dta
       }
     }
     if (cur < a.N) {
-      const bool goes_on = i1 < a.M && entry(a, sorted, i1).x == cur;
-      if (!goes_on && mark) a.bounds[cur].y = i1;
+      const bool goes_on = s_entry[i1 + 1].x == cur;
+      if (!goes_on && mark) a.bounds[cur].y = blk0 + i1;
       if (head) {
         kind |= goes_on ? 2 : 1;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) s_head[threadIdx.x * VE + e] = acc[e];
+        for (int e = 0; e < VE; ++e) first[e] = acc[e];
       } else if (goes_on) {
         kind |= 4;
         leaving = cur;
-#pragma unroll
-        for (int e = 0; e < VE; ++e) s_tail[threadIdx.x * VE + e] = acc[e];
       } else if (act) {
-        put_row<T, VB>(dtable + (long long)cur * ldt + col, acc, a.scale);
+        put_row<T, VB>(dtable + (long long)cur * ldt + col, acc, a.scale, left);
       }
     }
   }
+  __syncthreads();
+  float* s_head = reinterpret_cast<float*>(s_entry);
+#pragma unroll
+  for (int e = 0; e < VE; ++e) s_head[threadIdx.x * VE + e] = first[e];
   if (gl == 0) s_kind[g] = (uint8_t)kind;
   __syncthreads();
   // runs that cross groups: from the group where they start, or from the CTA's first group for
   // the one that entered the CTA
-  const bool enters = g == 0 && (kind & 3);
   if (!act) return;
-  if (enters) {
+  const int n = min(left, VE);
+  if (g == 0 && (kind & 3)) {
+    float sum[VE];
 #pragma unroll
-    for (int e = 0; e < VE; ++e) acc[e] = 0.0f;
+    for (int e = 0; e < VE; ++e) sum[e] = 0.0f;
     for (int h = 0; h < NG; ++h) {
 #pragma unroll
-      for (int e = 0; e < VE; ++e) acc[e] += s_head[((h << a.gl_log) + gl) * VE + e];
+      for (int e = 0; e < VE; ++e) sum[e] += s_head[((h << a.gl_log) + gl) * VE + e];
       if (!(s_kind[h] & 2)) break;
     }
     float* p = a.head + (size_t)blockIdx.x * a.C + col;
 #pragma unroll
-    for (int e = 0; e < VE; ++e) p[e] = acc[e];
+    for (int e = 0; e < VE; ++e)
+      if (e < n) p[e] = sum[e];
   }
   if (kind & 4) {
-#pragma unroll
-    for (int e = 0; e < VE; ++e) acc[e] = s_tail[threadIdx.x * VE + e];
     bool open = true;
     for (int h = g + 1; h < NG && open; ++h) {
 #pragma unroll
@@ -375,11 +543,12 @@ k_runs(RunArgs a, const T* __restrict__ dout, long long ldd, T* __restrict__ dta
       open = (s_kind[h] & 2) != 0;
     }
     if (!open) {
-      put_row<T, VB>(dtable + (long long)leaving * ldt + col, acc, a.scale);
+      put_row<T, VB>(dtable + (long long)leaving * ldt + col, acc, a.scale, left);
     } else {
       float* p = a.tail + (size_t)blockIdx.x * a.C + col;
 #pragma unroll
-      for (int e = 0; e < VE; ++e) p[e] = acc[e];
+      for (int e = 0; e < VE; ++e)
+        if (e < n) p[e] = acc[e];
     }
   }
 }
@@ -394,11 +563,12 @@ __global__ void __launch_bounds__(kThreads)
 k_join(RunArgs a, T* __restrict__ dtable, long long ldt) {
   constexpr int VE = Vec<T, VB>::N;
   __shared__ float s_part[kThreads * VE];
-  __shared__ uint32_t s_long[kThreads];
+  __shared__ uint32_t s_long[kThreads / kMinLanes];
   const int GL = 1 << a.gl_log, NG = kThreads >> a.gl_log;
   const int g = threadIdx.x >> a.gl_log, gl = threadIdx.x & (GL - 1);
   const int col = (blockIdx.y * GL + gl) * VE;
-  const bool act = col < a.C;
+  const int left = a.C - col, cnt = min(left, VE);
+  const bool act = left > 0;
   const unsigned per_cta = NG * kRun;
   const uint32_t n = blockIdx.x * NG + g;
   uint32_t lng = a.N;
@@ -409,7 +579,7 @@ k_join(RunArgs a, T* __restrict__ dtable, long long ldt) {
     const uint2 se = a.bounds[n];
     T* dst = dtable + (long long)n * ldt + col;
     if (se.x == se.y) {
-      if (act) put_row<T, VB>(dst, acc, 0.0f);
+      if (act) put_row<T, VB>(dst, acc, 0.0f, left);
     } else {
       const unsigned b0 = se.x / per_cta, b1 = (se.y - 1) / per_cta;
       if (b1 - b0 > kLong) {
@@ -417,13 +587,14 @@ k_join(RunArgs a, T* __restrict__ dtable, long long ldt) {
       } else if (b1 > b0 && act) {
         const float* p = a.tail + (size_t)b0 * a.C + col;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) acc[e] = p[e];
+        for (int e = 0; e < VE; ++e) acc[e] = e < cnt ? p[e] : 0.0f;
         for (unsigned b = b0 + 1; b <= b1; ++b) {
           const float* h = a.head + (size_t)b * a.C + col;
 #pragma unroll
-          for (int e = 0; e < VE; ++e) acc[e] += h[e];
+          for (int e = 0; e < VE; ++e)
+            if (e < cnt) acc[e] += h[e];
         }
-        put_row<T, VB>(dst, acc, a.scale);
+        put_row<T, VB>(dst, acc, a.scale, left);
       }
     }
   }
@@ -443,7 +614,8 @@ k_join(RunArgs a, T* __restrict__ dtable, long long ldt) {
       for (unsigned b = h0; b < h1; ++b) {
         const float* h = a.head + (size_t)b * a.C + col;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) acc[e] += h[e];
+        for (int e = 0; e < VE; ++e)
+            if (e < cnt) acc[e] += h[e];
       }
     }
 #pragma unroll
@@ -452,12 +624,12 @@ k_join(RunArgs a, T* __restrict__ dtable, long long ldt) {
     if (g == 0 && act) {
       const float* p = a.tail + (size_t)b0 * a.C + col;
 #pragma unroll
-      for (int e = 0; e < VE; ++e) acc[e] = p[e];
+      for (int e = 0; e < VE; ++e) acc[e] = e < cnt ? p[e] : 0.0f;
       for (int h = 0; h < NG; ++h) {
 #pragma unroll
         for (int e = 0; e < VE; ++e) acc[e] += s_part[((h << a.gl_log) + gl) * VE + e];
       }
-      put_row<T, VB>(dtable + (long long)m * ldt + col, acc, a.scale);
+      put_row<T, VB>(dtable + (long long)m * ldt + col, acc, a.scale, left);
     }
     __syncthreads();
   }
@@ -467,19 +639,19 @@ k_join(RunArgs a, T* __restrict__ dtable, long long ldt) {
 // host side
 // ---------------------------------------------------------------------------------------------
 
-// widest access (bytes) that keeps every vector of every row aligned and whole
-int vector_bytes(int elem, int C, const void* p, long long ldp, const void* q, long long ldq) {
+// widest access (bytes) that keeps every vector of every row aligned (a row's last may be short)
+int vector_bytes(int elem, const void* p, long long ldp, const void* q, long long ldq) {
   const uintptr_t all = (uintptr_t)p | (uintptr_t)q | (uintptr_t)(ldp * elem) |
-                        (uintptr_t)(ldq * elem) | (uintptr_t)(C * elem);
+                        (uintptr_t)(ldq * elem);
   int vb = 16;
   while (vb > elem && (all & (uintptr_t)(vb - 1))) vb >>= 1;
   return vb;
 }
 
 struct Plan {
-  int passes, bits, nd;
-  unsigned per_block, nblk;
-  size_t pairs0, pairs1, hist, descent, total, unsorted, bounds, head, tail, bytes;
+  int passes, bits, nd, items;
+  unsigned nblk, share;
+  size_t clear, pairs0, pairs1, total, unsorted, ticket, state, bounds, head, tail, bytes;
 };
 
 size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -491,24 +663,27 @@ Plan make_plan(long long M, long long N, int C) {
   p.passes = (need + kMaxBits - 1) / kMaxBits;
   p.bits = (need + p.passes - 1) / p.passes;
   p.nd = 1 << p.bits;
-  // enough CTAs for two per SM, at most 8,192 items each
-  long long per = (M + 295) / 296;
-  per = (per + kThreads - 1) / kThreads * kThreads;
-  per = per < kThreads ? kThreads : per > 8192 ? 8192 : per;
-  p.per_block = (unsigned)per;
-  p.nblk = (unsigned)((M + per - 1) / per);
+  // tiles of 8,192 items, or of 2,048 while that leaves SMs without one; as many to a CTA as keep
+  // the CTAs at two an SM
+  p.items = M > 8192LL * 148 ? 16 : 4;
+  const long long tile = (long long)kSortThreads * p.items, tiles = (M + tile - 1) / tile;
+  const long long per = (tiles + 295) / 296;
+  p.share = (unsigned)std::min(per * tile, 1LL << 31);
+  p.nblk = (unsigned)((tiles + per - 1) / per);
   size_t o = 0;
   auto take = [&](size_t b) {
     const size_t at = o;
     o += up(b);
     return at;
   };
+  // cleared at the start of a call
+  p.total = take((size_t)p.passes * p.nd * 4);
+  p.unsorted = take(4);
+  p.ticket = take((size_t)p.passes * 4);
+  p.state = take((size_t)p.passes * p.nblk * p.nd * 4);
+  p.clear = o;
   p.pairs0 = take((size_t)M * 8);
   p.pairs1 = take(p.passes > 1 ? (size_t)M * 8 : 0);
-  p.hist = take((size_t)p.nd * p.nblk * 4);
-  p.descent = take((size_t)p.nblk * 4);
-  p.total = take((size_t)p.nd * 4);
-  p.unsorted = take(4);
   p.bounds = take((size_t)N * 8);
   const size_t ctas = ((size_t)M + kWarps * kRun - 1) / (kWarps * kRun);  // at 32 lanes a row
   p.head = take(ctas * C * 4);
@@ -524,18 +699,18 @@ int last_error() {
 template <typename T, int VB>
 int run_lookup(const T* table, long long ldt, int N, const int* ids, long long M, int C,
                float scale, T* out, long long ldo, cudaStream_t st) {
-  const int vpr = C / Vec<T, VB>::N;
+  const int vpr = (C + Vec<T, VB>::N - 1) / Vec<T, VB>::N;
   const int rpb = vpr >= 1024 ? 1 : 1024 / vpr;
   const uint32_t magic = (uint32_t)(((1ULL << 32) + vpr - 1) / vpr);
   k_lookup<T, VB><<<(unsigned)((M + rpb - 1) / rpb), kThreads, 0, st>>>(
-      table, ldt, (unsigned)N, ids, M, vpr, magic, rpb, scale, out, ldo);
+      table, ldt, (unsigned)N, ids, M, C, vpr, magic, rpb, scale, out, ldo);
   return last_error();
 }
 
 template <typename T, int VB>
 int run_sums(RunArgs a, const T* dout, long long ldd, T* dtable, long long ldt, cudaStream_t st) {
-  const int vpr = a.C / Vec<T, VB>::N;
-  a.gl_log = 0;
+  const int vpr = (a.C + Vec<T, VB>::N - 1) / Vec<T, VB>::N;
+  a.gl_log = 2;
   while (a.gl_log < 5 && (1 << a.gl_log) < vpr) ++a.gl_log;
   const int GL = 1 << a.gl_log, NG = kThreads / GL;
   const unsigned cols = (vpr + GL - 1) / GL;
@@ -549,46 +724,51 @@ template <typename T>
 int run_backward(const T* dout, long long ldd, const int* ids, long long M, int N, int C,
                  float scale, T* dtable, long long ldt, char* scratch, cudaStream_t st) {
   const Plan p = make_plan(M, N, C);
-  int* hist = (int*)(scratch + p.hist);
-  int* descent = (int*)(scratch + p.descent);
-  int* total = (int*)(scratch + p.total);
-  int* unsorted = (int*)(scratch + p.unsorted);
-  uint2* bounds = (uint2*)(scratch + p.bounds);
+  SortArgs q;
+  q.ids = ids;
+  q.vec = ((uintptr_t)ids & 15) == 0;
+  q.M = (unsigned)M;
+  q.N = (uint32_t)N;
+  q.passes = p.passes;
+  q.bits = p.bits;
+  q.bounds = (uint2*)(scratch + p.bounds);
+  q.total = (int*)(scratch + p.total);
+  q.unsorted = (int*)(scratch + p.unsorted);
+  q.ticket = (unsigned*)(scratch + p.ticket);
+  q.state = (unsigned*)(scratch + p.state);
+  q.nblk = p.nblk;
+  q.share = p.share;
   uint2* buf[2] = {(uint2*)(scratch + p.pairs0), (uint2*)(scratch + p.pairs1)};
-  const unsigned m = (unsigned)M, scan_ctas = (p.nd + kWarps - 1) / kWarps;
+  const long long words = (long long)(p.clear / 16);
+  k_clear<<<(unsigned)std::min((words + kThreads - 1) / kThreads, 148LL * 8), kThreads, 0, st>>>(
+      (uint4*)scratch, words);
+  const long long want = (std::max(M, (long long)N) + kThreads * 16 - 1) / (kThreads * 16);
+  k_survey<<<(unsigned)std::min(want, 148LL * 4), kThreads, 0, st>>>(q);
+  const int smem = std::max(kSortWarps * p.nd * 4, kSortThreads * p.items * 8) + p.nd * 8 +
+                   kSortWarps * p.nd * 2;
+  auto pass = p.items == 16 ? k_sort_pass<16> : k_sort_pass<4>;
+  if (cudaFuncSetAttribute(pass, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
+    return last_error();
   for (int i = 0; i < p.passes; ++i) {
-    const int shift = i * p.bits;
-    uint2* out = buf[i & 1];
-    const uint2* in = buf[(i & 1) ^ 1];
-    if (i == 0) {
-      k_hist<true><<<p.nblk, kThreads, 0, st>>>(ids, nullptr, m, N, shift, p.bits, p.per_block,
-                                                hist, descent, unsorted, bounds);
-      k_digit_scan<true><<<scan_ctas, kThreads, 0, st>>>(hist, p.nblk, p.nd, total, descent,
-                                                         unsorted);
-      k_scatter_pairs<true><<<p.nblk, kThreads, 0, st>>>(ids, nullptr, m, N, shift, p.bits,
-                                                         p.per_block, hist, total, unsorted, out);
-    } else {
-      k_hist<false><<<p.nblk, kThreads, 0, st>>>(nullptr, in, m, N, shift, p.bits, p.per_block,
-                                                 hist, nullptr, unsorted, nullptr);
-      k_digit_scan<false><<<scan_ctas, kThreads, 0, st>>>(hist, p.nblk, p.nd, total, nullptr,
-                                                          unsorted);
-      k_scatter_pairs<false><<<p.nblk, kThreads, 0, st>>>(nullptr, in, m, N, shift, p.bits,
-                                                          p.per_block, hist, total, unsorted, out);
-    }
+    q.pass = i;
+    q.in = buf[(i & 1) ^ 1];
+    q.out = buf[i & 1];
+    pass<<<p.nblk, kSortThreads, smem, st>>>(q);
   }
   RunArgs a;
   a.ids = ids;
   a.pairs = buf[(p.passes - 1) & 1];
-  a.unsorted = unsorted;
-  a.M = m;
+  a.unsorted = q.unsorted;
+  a.M = (unsigned)M;
   a.N = (uint32_t)N;
   a.C = C;
   a.gl_log = 0;
   a.scale = scale;
-  a.bounds = bounds;
+  a.bounds = q.bounds;
   a.head = (float*)(scratch + p.head);
   a.tail = (float*)(scratch + p.tail);
-  const int vb = vector_bytes(sizeof(T), C, dout, ldd, dtable, ldt);
+  const int vb = vector_bytes(sizeof(T), dout, ldd, dout, ldd);
   switch (vb) {
     case 16: return run_sums<T, 16>(a, dout, ldd, dtable, ldt, st);
     case 8: return run_sums<T, 8>(a, dout, ldd, dtable, ldt, st);
@@ -601,7 +781,7 @@ int run_backward(const T* dout, long long ldd, const int* ids, long long M, int 
 template <typename T>
 int run_forward(const T* table, long long ldt, const int* ids, long long M, int N, int C,
                 float scale, T* out, long long ldo, cudaStream_t st) {
-  const int vb = vector_bytes(sizeof(T), C, table, ldt, out, ldo);
+  const int vb = vector_bytes(sizeof(T), table, ldt, out, ldo);
   switch (vb) {
     case 16: return run_lookup<T, 16>(table, ldt, N, ids, M, C, scale, out, ldo, st);
     case 8: return run_lookup<T, 8>(table, ldt, N, ids, M, C, scale, out, ldo, st);
@@ -624,6 +804,17 @@ __global__ void k_zero_rows(char* p, long long row_bytes, long long ld_bytes, lo
 }
 
 }  // namespace
+
+cudaError_t lookup_status_take(unsigned int* out, cudaStream_t st) {
+  const unsigned int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_lookup_status, sizeof *out, 0,
+                                            cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess)
+    e = cudaMemcpyToSymbolAsync(g_lookup_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice,
+                                st);
+  return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+}
+
 }  // namespace rows
 }  // namespace splat
 

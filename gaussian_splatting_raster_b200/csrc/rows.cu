@@ -61,3 +61,13 @@ int check_spans(const Span* s, int n) {
 
 }  // namespace rows
 }  // namespace splat
+
+extern "C" int splat_rows_status(void* stream) {
+  unsigned int a = 0, b = 0;
+  if (splat::rows::lookup_status_take(&a, (cudaStream_t)stream) != cudaSuccess ||
+      splat::rows::ffn_status_take(&b, (cudaStream_t)stream) != cudaSuccess) {
+    cudaGetLastError();
+    return SPLAT_ERR_CUDA;
+  }
+  return a | b ? SPLAT_ERR_DEVICE_TIMEOUT : SPLAT_OK;
+}

@@ -52,5 +52,10 @@ constexpr long long kMaxLd = 1LL << 28;  // keeps every byte offset of 2^31 rows
 // needs no device is checked first.
 int check_spans(const Span* s, int n);
 
+// The status words of the waits inside the lookup's and the feed-forward block's kernels, read and
+// cleared (waits for the stream).
+cudaError_t lookup_status_take(unsigned int* out, cudaStream_t st);
+cudaError_t ffn_status_take(unsigned int* out, cudaStream_t st);
+
 }  // namespace rows
 }  // namespace splat

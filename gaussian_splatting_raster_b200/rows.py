@@ -24,9 +24,9 @@ def _rows(t, name, like, shape):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != like.dtype:
         raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if t.numel() == 0:
         return None, shape[1]
@@ -62,29 +62,34 @@ def _ids(ids, like):
         raise TypeError(f"ids must be torch.int32, got {ids.dtype}")
     if ids.dim() != 1 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous vector")
-    if ids.device != like.device:
+    if ids.get_device() != like.get_device():
         raise ValueError(f"ids is on {ids.device}, expected {like.device}")
     return ids.data_ptr(), ids.shape[0]
 
 
-def _call(fn, what, device, stream, args, scratch_bytes=None):
-    """fn(*args[, scratch, bytes], stream) on the tensors' device; raises on a refusal."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return _launch(fn, what, device, torch.cuda.current_stream(device), args, scratch_bytes)
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    with torch.cuda.device(device):
-        s = stream if stream is not None else torch.cuda.current_stream(device)
-        with torch.cuda.stream(s):  # scratch belongs to the stream that uses it
-            return _launch(fn, what, device, s, args, scratch_bytes)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without an object
 
 
-def _launch(fn, what, device, stream, args, scratch_bytes):
+def _call(fn, what, t, stream, args, scratch_bytes=None):
+    """fn(*args[, scratch, bytes], stream) on the device of tensor t; raises on a refusal."""
+    dev = t.get_device()
+    if stream is None and dev == torch.cuda.current_device():
+        return _launch(fn, what, t, _raw_stream(dev), args, scratch_bytes)
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    with torch.cuda.device(dev):
+        if stream is None:
+            return _launch(fn, what, t, _raw_stream(dev), args, scratch_bytes)
+        with torch.cuda.stream(stream):  # scratch belongs to the stream that uses it
+            return _launch(fn, what, t, stream.cuda_stream, args, scratch_bytes)
+
+
+def _launch(fn, what, t, stream, args, scratch_bytes):
     if scratch_bytes is not None:
-        scratch = (torch.empty(scratch_bytes, dtype=torch.uint8, device=device)
+        scratch = (torch.empty(scratch_bytes, dtype=torch.uint8, device=t.device)
                    if scratch_bytes else None)
         args = (*args, scratch.data_ptr() if scratch_bytes else None, scratch_bytes)
-    rc = fn(*args, stream.cuda_stream)
+    rc = fn(*args, stream)
     if rc != 0:
         raise SplatError(rc, f"{what} refused its arguments" if rc in (-1, -2) else
                          f"{what} failed")
@@ -98,7 +103,7 @@ def lookup(table, ids, out, scale: float = 1.0, stream=None):
     pi, M = _ids(ids, table)
     pt, ldt = _rows(table, "table", table, (N, C))
     po, ldo = _rows(out, "out", table, (M, C))
-    _call(load_library().splat_lookup, "lookup", table.device, stream,
+    _call(load_library().splat_lookup, "lookup", table, stream,
           (pt, ldt, N, C, pi, M, scale, _DTYPES[table.dtype], po, ldo))
 
 
@@ -116,7 +121,7 @@ def lookup_backward(dout, ids, dtable, scale: float = 1.0, stream=None):
     pd, ldd = _rows(dout, "dout", dout, (M, C))
     pt, ldt = _rows(dtable, "dtable", dout, (N, C))
     L = load_library()
-    _call(L.splat_lookup_backward, "lookup_backward", dout.device, stream,
+    _call(L.splat_lookup_backward, "lookup_backward", dout, stream,
           (pd, ldd, pi, M, C, scale, _DTYPES[dout.dtype], pt, ldt, N),
           L.splat_lookup_scratch(M, N, C))
 
@@ -145,7 +150,7 @@ def ffn(x, w_gate, w_up, w_down, y, act: str = "silu", stream=None):
     px, ldx = _rows(x, "x", x, (M, D))
     py, ldy = _rows(y, "y", x, (M, O))
     L, dt = load_library(), _DTYPES[x.dtype]
-    _call(L.splat_ffn, "ffn", x.device, stream, (px, ldx, *w, py, ldy, M, D, F, O, dt, a),
+    _call(L.splat_ffn, "ffn", x, stream, (px, ldx, *w, py, ldy, M, D, F, O, dt, a),
           L.splat_ffn_scratch(M, D, F, O, dt, w_gate is not None, 0))
 
 
@@ -164,7 +169,7 @@ def ffn_backward(dy, x, w_gate, w_up, w_down, dx=None, dw_gate=None, dw_up=None,
     if M == 0 and dx is not None and all(p is None for p in dw):
         return
     L, dt = load_library(), _DTYPES[x.dtype]
-    _call(L.splat_ffn_backward, "ffn_backward", x.device, stream,
+    _call(L.splat_ffn_backward, "ffn_backward", x, stream,
           (py, ldy, px, ldx, *w, pd, ldd, *dw, M, D, F, O, dt, a),
           L.splat_ffn_scratch(M, D, F, O, dt, w_gate is not None, 1))
 

@@ -352,7 +352,7 @@ int splat_sort_depths_noalloc(const float* depths, int n, int* order, void* stre
  *     where it is there.
  *   - Row arrays are given with the distance between rows in elements (`ld_*`, at most 2^28; >= the
  *     row's width for outputs of more than one row; inputs may have any, 0 included). Weights are
- *     contiguous. Whatever lies between or behind rows is neither read nor written.
+ *     contiguous. What lies between rows is never written, and never used.
  *   - All arrays live on the current device, which is `stream`'s. An output may share no element
  *     with another argument (SPLAT_ERR_INVALID_ARG; column ranges of one wider array are fine).
  *   - `scratch` is the caller's: a device buffer of at least the bytes the scratch function of the
@@ -411,8 +411,8 @@ int splat_ffn_backward(const void* dy, long long ld_dy, const void* x, long long
                        void* stream);
 
 /*
- * Waits inside the feed-forward kernels (for their own copies and products) are bounded at about
- * four seconds. When one ran out on the current device since the last call, the results of the
+ * Waits inside these kernels (for their own copies, products and earlier blocks) are bounded at
+ * about four seconds. When one ran out on the current device since the last call, the results of the
  * call it belonged to mean nothing and this returns SPLAT_ERR_DEVICE_TIMEOUT once. Waits for
  * `stream`; not to be captured.
  */
