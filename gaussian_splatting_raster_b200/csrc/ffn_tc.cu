@@ -11,12 +11,19 @@
 // to leave TMEM per tile and chunk (M F D / 64 fp32 sums), which costs more than computing the
 // hidden values twice.
 //
-// A CTA has up to two groups of eight warps, each with its own tile, shared memory and TMEM, which
-// take turns: while one turns accumulators into hidden values, the tensor cores work for the
-// other. One thread issues all MMAs, one all weight loads. Weights are packed once per call into
-// the layout the MMAs read (zeros beyond F, D and O), so a chunk is one contiguous bulk copy; all
-// chunks stay in shared memory where they fit. Row tiles are read with plain loads, which take any
-// row distance and alignment (token rows have odd widths), straight into the swizzled layout.
+// A CTA's work is one sequence of items, (tile, chunk) or tiles. Two groups of eight warps turn
+// accumulators into hidden values, item by item in turn; one warp issues all MMAs, the first
+// products of up to three items ahead of the second product of the item that is ready; one thread
+// loads weights. So the tensor cores and the groups wait for one another only at the ends of the
+// sequence: what bounds a narrow block is the groups' arithmetic (special function unit and issue
+// slots), a wide one the tensor cores. (With an accumulator per group, a group waited about as
+// long for its products as it worked on them.) Weights are packed once per call into the layout the
+// MMAs read (zeros beyond F, D and O), so a chunk is one contiguous bulk copy; all chunks stay in
+// shared memory where they fit. Row tiles are read with plain loads, which take any row distance
+// and alignment (token rows have odd widths), straight into the swizzled layout, a tile or two
+// ahead.
+#include <algorithm>
+
 #include "ffn.cuh"
 #include "tc.cuh"
 
@@ -29,9 +36,10 @@ using namespace tc;
 enum Mode { kFwd, kDx, kDw };
 
 constexpr int kGroupThreads = 256;
-constexpr int kMaxGroups = 2;
-constexpr int kTcThreads = kMaxGroups * kGroupThreads + 64;  // + MMA warp + weight warp
+constexpr int kGroupWarps = kGroupThreads / 32;
+constexpr int kTcThreads = 2 * kGroupThreads + 64;  // + MMA warp + weight warp
 constexpr int kMaxStages = 16;
+constexpr int kMaxGu = 3, kMaxRows = 3;  // accumulators of first products; row tiles
 constexpr int kTile = 128;
 constexpr int kSmemLimit = 232448 - 2048;  // 227 KB less the alignment slack and the barriers
 
@@ -48,7 +56,9 @@ struct TcArgs {
   FfnArgs f;
   const uint8_t* img;   // packed weights, chunk after chunk
   int nch, stage_bytes; // chunks; bytes of one
-  int nst, ng;          // weight stages in shared memory; groups
+  int nst, nx, nh;      // weight stages, row tiles and hidden operands in shared memory
+  int ngu, no;          // accumulators of first products and of outputs in TMEM
+  int staged;           // outputs have places of their own in shared memory
   int dp, op;           // D and O rounded up to 16
   RowSrc x, dy;
   int out_aligned;      // y's or dx's rows start and end at 16 bytes
@@ -301,209 +311,191 @@ __device__ __forceinline__ void write_rows(const uint8_t* src, uint8_t* base, lo
 // the kernel
 // ---------------------------------------------------------------------------------------------
 
-// TMEM columns of one group: forward A|U 128, Y; dx A|U 128, dH 64, dX; weights A|U 128, dH 64
-// (dW accumulators behind both groups').
-__host__ __device__ constexpr int tmem_group(int mode, int dp, int op) {
-  return mode == kFwd ? 128 + ((op + 31) & ~31)
-                      : mode == kDx ? 192 + ((dp + 31) & ~31) : 192;
+// TMEM columns of a first product: A|U (A), and dH behind it in the gradients
+__host__ __device__ constexpr int gu_cols(int mode, bool gated) {
+  return (gated ? 128 : 64) + (mode == kFwd ? 0 : 64);
 }
+__host__ __device__ constexpr int pad32(int v) { return (v + 31) & ~31; }
 
-// shared memory of one group: its row tiles, and its hidden operand (h; da, du; da, du, h)
-__host__ __device__ constexpr int smem_group(int mode, int dp, int op, bool gated) {
-  return ((dp + 63) / 64 + (mode == kFwd ? 0 : (op + 63) / 64) +
-          (mode == kFwd ? 1 : (gated ? 2 : 1) + (mode == kDw ? 1 : 0))) * 16384;
+// shared memory of a row tile, and of a hidden operand (h; da, du; da, du, h)
+__host__ __device__ constexpr int rows_bytes(int mode, int dp, int op) {
+  return ((dp + 63) / 64 + (mode == kFwd ? 0 : (op + 63) / 64)) * 16384;
+}
+__host__ __device__ constexpr int hidden_bytes(int mode, bool gated) {
+  return (mode == kFwd ? 1 : (gated ? 2 : 1) + (mode == kDw ? 1 : 0)) * 16384;
 }
 
 template <int MODE, typename T, int ACT, bool GATED>
 __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t s_bar[2 * kMaxStages + 4 * kMaxGroups + 1];
+  constexpr int kBars = 2 * kMaxStages + kMaxGu + kMaxRows + 2 + 2 + 2 + 2 + 1;
+  __shared__ __align__(8) uint64_t s_bar[kBars];
   __shared__ uint32_t s_tmem;
   __shared__ int s_failed;
   constexpr int WR = GATED ? 128 : 64;
   constexpr bool BF = Two<T>::kBf16;
+  constexpr uint32_t kGu = gu_cols(MODE, GATED);
+  constexpr uint32_t kHBytes = hidden_bytes(MODE, GATED);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   const uint32_t sbase = smem_addr(smem);
   const int nbx = (p.dp + 63) >> 6, nby = (p.op + 63) >> 6;
-  const uint32_t groups0 = p.nst * p.stage_bytes;
-  const int gbytes = smem_group(MODE, p.dp, p.op, GATED);
+  const uint32_t xbytes = rows_bytes(MODE, p.dp, p.op);
+  const uint32_t x_off = p.nst * p.stage_bytes, h_off = x_off + p.nx * xbytes;
   const uint32_t bars = smem_addr(s_bar);
-  // weights of a stage: full, empty; per group: accumulators ready, hidden operand ready, second
-  // product done, row tile ready (weights only)
-  auto full = [&](int s) { return bars + 8 * s; };
-  auto empty = [&](int s) { return bars + 8 * (kMaxStages + s); };
-  auto gu_full = [&](int g) { return bars + 8 * (2 * kMaxStages + 4 * g); };
-  auto h_ready = [&](int g) { return bars + 8 * (2 * kMaxStages + 4 * g + 1); };
-  auto out_done = [&](int g) { return bars + 8 * (2 * kMaxStages + 4 * g + 2); };
-  auto x_ready = [&](int g) { return bars + 8 * (2 * kMaxStages + 4 * g + 3); };
-  const uint32_t all_done = bars + 8 * (2 * kMaxStages + 4 * kMaxGroups);
+  auto full = [&](int k) { return bars + 8 * k; };                    // a stage's weights are there
+  auto empty = [&](int k) { return bars + 8 * (kMaxStages + k); };    // ... are used
+  constexpr int kB0 = 2 * kMaxStages;
+  auto gu_full = [&](int k) { return bars + 8 * (kB0 + k); };         // a first product is done
+  auto x_ready = [&](int k) { return bars + 8 * (kB0 + kMaxGu + k); };  // a row tile is there
+  constexpr int kB1 = kB0 + kMaxGu + kMaxRows;
+  auto h_ready = [&](int k) { return bars + 8 * (kB1 + k); };     // item's hidden operand, by parity
+  auto done = [&](int k) { return bars + 8 * (kB1 + 2 + k); };    // item's second product, by parity
+  auto out_full = [&](int k) { return bars + 8 * (kB1 + 4 + k); };  // a tile's output is complete
+  auto out_free = [&](int k) { return bars + 8 * (kB1 + 6 + k); };  // ... has been read
+  const uint32_t all_done = bars + 8 * (kB1 + 8);
   volatile int* failed = &s_failed;
   unsigned int* status = &g_rows_status;
 
   if (threadIdx.x == 0) {
     s_failed = 0;
-    for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), p.ng);
+    for (int k = 0; k < kBars; ++k) {
+      const bool by_warps = (k >= kB0 + kMaxGu && k < kB1 + 2) || k == kB1 + 6 || k == kB1 + 7;
+      mbar_init(bars + 8 * k, by_warps ? kGroupWarps : 1);
     }
-    for (int g = 0; g < kMaxGroups; ++g) {
-      mbar_init(gu_full(g), 1);
-      mbar_init(h_ready(g), kGroupThreads / 32);
-      mbar_init(out_done(g), 1);
-      mbar_init(x_ready(g), kGroupThreads / 32);
-    }
-    mbar_init(all_done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_shared();
   }
   constexpr uint32_t kCols = 512;
-  if (warp == kMaxGroups * 8) tmem_alloc(smem_addr(&s_tmem), kCols);
+  if (warp == 2 * kGroupWarps) tmem_alloc(smem_addr(&s_tmem), kCols);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = s_tmem;
+  // behind the first products: outputs (forward, dx), or [da|du]^T X and [du|h]^T dY
+  const uint32_t acc = tmem + p.ngu * kGu;
+  const uint32_t acc_step = MODE == kFwd ? pad32(p.op) : pad32(p.dp);
 
   const int chunk0 = MODE == kDw ? blockIdx.x % p.nch : 0;
   const int nch = MODE == kDw ? 1 : p.nch;
   const int ctas = MODE == kDw ? p.f.splits : gridDim.x;
   const int me = MODE == kDw ? blockIdx.x / p.nch : blockIdx.x;
-  const long long step = (long long)ctas * p.ng;
-  // steps of this CTA (both groups take the same number; a group without a tile has zero rows)
-  const long long first = (long long)me * p.ng;
-  const int nt = first < p.tiles ? (int)((p.tiles - first + step - 1) / step) : 0;
-  const uint32_t tg = tmem_group(MODE, p.dp, p.op);
-  const uint32_t acc_gu = tmem + p.ng * tg;  // weights: [da|du]^T X, then [du|h]^T dY
-  const uint32_t acc_d = acc_gu + ((p.dp + 31) & ~31);
+  const int nt = me < p.tiles ? (int)((p.tiles - me + ctas - 1) / ctas) : 0;  // tiles me + n ctas
+  const int total = nt * nch;                                                 // items
+  const bool ring = nch > p.nst;
+  // Barriers of first products. A wait tells a phase by its parity, so it must know that the phase
+  // before is over and the one behind cannot be: with two barriers or more, item i - 2 (which the
+  // waiting group has seen) or one before it has the phase before on item i's.
+  const int gu_bars = max(p.ngu, 2);
 
-  if (warp == kMaxGroups * 8) {
+  if (warp == 2 * kGroupWarps) {
     // ------------------------------------------------------------------------- MMA issue
-    // (the whole warp waits, one lane issues)
+    // (the whole warp polls, one lane issues)
     if (nt > 0) {
       const int kx = p.dp >> 4, ko = p.op >> 4;
       const uint32_t id_gu = idesc(BF, WR, false, false), id_dh = idesc(BF, 64, false, true);
-      const uint32_t id_y = idesc(BF, p.op, false, false), id_dx = idesc(BF, p.dp, false, true);
-      const uint32_t id_wx = idesc(BF, p.dp, true, true), id_wy = idesc(BF, p.op, true, true);
+      const uint32_t id_out = MODE == kFwd  ? idesc(BF, p.op, false, false)
+                              : MODE == kDx ? idesc(BF, p.dp, false, true)
+                                            : idesc(BF, p.dp, true, true);
+      const uint32_t id_wy = idesc(BF, p.op, true, true);
       // descriptors count in 16 bytes: a step of 16 along K is 2 in a K-major tile (4 steps to a
       // 64-column block), 128 in an MN-major one; weights' blocks have WR rows
       constexpr uint32_t kBlk = 16384 >> 4, kWBlk = WR * 128 >> 4;
-      const uint32_t x0 = sbase + groups0, y0 = x0 + nbx * 16384;
-      const uint32_t h0 = x0 + (nbx + (MODE == kFwd ? 0 : nby)) * 16384;
-      const uint32_t dx_k = desc_lo(x0, 16), dy_k = desc_lo(y0, 16), dh_k = desc_lo(h0, 16);
-      const uint32_t dx_mn = desc_lo(x0, 16384), dy_mn = desc_lo(y0, 16384), dh_mn = desc_lo(h0, 16384);
-      const uint32_t dw_k = desc_lo(sbase, 16), dw_mn = desc_lo(sbase, WR * 128);
-      const uint32_t dd_k = desc_lo(sbase + nbx * WR * 128, 16);
-      const uint32_t gs = gbytes >> 4, ss = p.stage_bytes >> 4;
-      // A|U (and dH) of group g from stage s
-      auto first_product = [&](int g, int s) {
+      const uint32_t xs = xbytes >> 4, ss = p.stage_bytes >> 4;
+      const uint32_t x_k = desc_lo(sbase + x_off, 16), h_k = desc_lo(sbase + h_off, 16);
+      const uint32_t w_k = desc_lo(sbase, 16);
+      constexpr uint32_t kMn = (16384 >> 4) << 16, kWMn = (WR * 128 >> 4) << 16, kK = 1u << 16;
+      const uint32_t y_off = nbx * kBlk, down_off = nbx * kWBlk;
+      // A|U (and dH) of a row tile and a weight stage
+      auto first_product = [&](int gu, int bar, int xb, int s) {
         if (elect_one()) {
-          const uint32_t d = tmem + g * tg;
-          const uint32_t a = dx_k + g * gs, b = dw_k + s * ss;
+          const uint32_t d = tmem + gu * kGu;
+          const uint32_t a = x_k + xb * xs, b = w_k + s * ss;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             if (k < kx)
               mma(d, a + (k >> 2) * kBlk + (k & 3) * 2, b + (k >> 2) * kWBlk + (k & 3) * 2, id_gu,
                   k > 0);
           if (MODE != kFwd) {
-            const uint32_t ay = dy_k + g * gs, bd = dd_k + s * ss;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               if (k < ko)
-                mma(d + 128, ay + (k >> 2) * kBlk + (k & 3) * 2, bd + k * 128, id_dh, k > 0);
+                mma(d + WR, a + y_off + (k >> 2) * kBlk + (k & 3) * 2, b + down_off + k * 128,
+                    id_dh, k > 0);
           }
-          commit(gu_full(g));
+          commit(gu_full(bar));
         }
         __syncwarp();
       };
-      auto second_product = [&](int g, int s, bool add, bool begun, bool last_chunk, bool ring,
-                                bool last) {
+      auto second_product = [&](int i, int hb, int xb, int s, int o, bool add, bool last_chunk) {
         if (elect_one()) {
-          const uint32_t d = tmem + g * tg;
+          const uint32_t h = h_k + hb * (kHBytes >> 4), w = w_k + s * ss;
           if (MODE == kFwd) {
-            const uint32_t a = dh_k + g * gs, b = dd_k + s * ss;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma(d + 128, a + k * 2, b + k * 2, id_y, add || k > 0);
+            for (int k = 0; k < 4; ++k)
+              mma(acc + o * acc_step, h + k * 2, w + down_off + k * 2, id_out, add || k > 0);
           } else if (MODE == kDx) {
-            const uint32_t a = dh_k + g * gs, b = dw_mn + s * ss;
 #pragma unroll
             for (int k = 0; k < WR / 16; ++k)
-              mma(d + 192, a + (k >> 2) * kBlk + (k & 3) * 2, b + k * 128, id_dx, add || k > 0);
+              mma(acc + o * acc_step, h + (k >> 2) * kBlk + (k & 3) * 2,
+                  w - kK + kWMn + k * 128, id_out, add || k > 0);
           } else {
-            const uint32_t a = dh_mn + g * gs, b = dx_mn + g * gs;
+            const uint32_t hm = h - kK + kMn, x = x_k - kK + kMn + xb * xs;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mma(acc, hm + k * 128, x + k * 128, id_out, add || k > 0);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma(acc_gu, a + k * 128, b + k * 128, id_wx, begun || k > 0);
-            const uint32_t ad = a + (GATED ? kBlk : 0), bd = dy_mn + g * gs;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma(acc_d, ad + k * 128, bd + k * 128, id_wy, begun || k > 0);
+              mma(acc + acc_step, hm + (GATED ? kBlk : 0) + k * 128, x + y_off + k * 128, id_wy,
+                  add || k > 0);
           }
-          if (last_chunk) commit(out_done(g));
+          commit(done(i & 1));
+          if (MODE != kDw && last_chunk) commit(out_full(o));
           if (ring) commit(empty(s));
-          if (last) commit(all_done);
+          if (i == total - 1) commit(all_done);
         }
         __syncwarp();
       };
-      // Each group goes through: first product (its rows and the chunk's weights are there), hidden
-      // operand ready, second product. The groups are served in the order they become ready.
-      const bool ring = nch > p.nst;
-      struct State {
-        int left, c, s;    // chunks to go, chunk, weight stage
-        uint32_t ph;       // bit 0 weights, bit 1 hidden operand, bit 2 rows
-        bool fresh;        // the stage's weights are to be waited for
-        bool first;        // the first product is next
-        bool rows;         // ... of a new tile
-      };
-      State st[kMaxGroups];
-      int left = p.ng * nt * nch;
-#pragma unroll
-      for (int g = 0; g < kMaxGroups; ++g) st[g] = {g < p.ng ? nt * nch : 0, 0, 0, 0u, true, true, true};
-      bool begun = false;
-      int turn = 0;  // weights: both groups add to one accumulator, always in the same order
-      long long since = clock64();
       auto is_there = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_try(bar, parity)) || *failed;
       };
-      while (left > 0) {
+      // next first product: item, chunk, buffer and parity of accumulator, rows, weights
+      int i1 = 0, c1 = 0, gu = 0, gb = 0, x1 = 0, s1 = 0;
+      uint32_t px = 0, pw = 0;
+      bool fresh = true;  // the stage's weights are to be waited for
+      // next second product: item, chunk, hidden operand, rows, weights, output and its parity
+      int i2 = 0, c2 = 0, hb = 0, x2 = 0, s2 = 0, o2 = 0;
+      uint32_t po = 1;  // (the first round of outputs has nobody to wait for)
+      long long since = clock64();
+      while (i2 < total) {
         bool moved = false;
-#pragma unroll
-        for (int g = 0; g < kMaxGroups; ++g) {
-          State& t = st[g];
-          if (t.left == 0) continue;
-          if (t.first) {
-            if (t.fresh && !is_there(full(t.s), t.ph & 1)) continue;
-            if (t.rows && !is_there(x_ready(g), (t.ph >> 2) & 1)) continue;
-            fence_after();
-            if (t.rows) t.ph ^= 4;
-            t.rows = false;
-            first_product(g, t.s);
-            t.first = false;
-            moved = true;
-          } else if ((MODE != kDw || g == turn) && is_there(h_ready(g), (t.ph >> 1) & 1)) {
-            fence_after();
-            t.ph ^= 2;
-            const bool last_chunk = t.c == nch - 1;
-            --left;
-            --t.left;
-            if (p.ng > 1) turn ^= 1;
-            second_product(g, t.s, t.c > 0, begun, last_chunk, ring, left == 0);
-            begun = true;
-            t.c = last_chunk ? 0 : t.c + 1;
-            if (++t.s == p.nst) {
-              t.s = 0;
-              t.ph ^= 1;
-              t.fresh = ring;
-            }
-            t.first = true;
-            t.rows = last_chunk;
-            moved = true;
-            // within a tile the next first product follows at once when its weights are there
-            if (t.left > 0 && !t.rows && (!t.fresh || is_there(full(t.s), t.ph & 1))) {
-              fence_after();
-              first_product(g, t.s);
-              t.first = false;
-            }
+        if (i2 < i1 && is_there(h_ready(i2 & 1), (i2 >> 1) & 1) &&
+            (MODE == kDw || c2 > 0 || is_there(out_free(o2), po))) {
+          fence_after();
+          const bool last = c2 == nch - 1;
+          second_product(i2, hb, x2, s2, o2, MODE == kDw ? i2 > 0 : c2 > 0, last);
+          ++i2;
+          if (++hb == p.nh) hb = 0;
+          if (++s2 == p.nst) s2 = 0;
+          c2 = last ? 0 : c2 + 1;
+          if (last) {
+            if (++x2 == p.nx) x2 = 0;
+            if (++o2 == p.no) o2 = 0, po ^= 1;
           }
+          moved = true;
+        }
+        if (i1 < total && i1 < i2 + p.ngu && (c1 > 0 || is_there(x_ready(x1), px)) &&
+            (!fresh || is_there(full(s1), pw))) {
+          fence_after();
+          first_product(gu, gb, x1, s1);
+          ++i1;
+          if (++gb == gu_bars) gb = 0;
+          if (++gu == p.ngu) gu = 0;
+          if (++s1 == p.nst) s1 = 0, pw ^= 1, fresh = ring;
+          if (++c1 == nch) {
+            c1 = 0;
+            if (++x1 == p.nx) x1 = 0, px ^= 1;
+          }
+          moved = true;
         }
         if (moved) {
           since = clock64();
@@ -513,209 +505,218 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
         }
       }
     }
-  } else if (warp == kMaxGroups * 8 + 1) {
+  } else if (warp == 2 * kGroupWarps + 1) {
     // ------------------------------------------------------------------------- weight loads
     if (lane == 0 && nt > 0) {
-      const bool ring = nch > p.nst;
-      const long long total = ring ? (long long)nt * nch : nch;
-      for (long long j = 0; j < total; ++j) {
-        const int s = (int)(j % p.nst);
-        if (j >= p.nst)
-          mbar_wait(empty(s), (uint32_t)((j / p.nst - 1) & 1), failed, status);
+      const int uses = ring ? total : nch;
+      int j = 0;
+      for (; j < uses; ++j) {
+        const int s = j % p.nst;
+        if (j >= p.nst) mbar_wait(empty(s), (j / p.nst - 1) & 1, failed, status);
+        // (after a failed wait the stage's last phase may still be open: nothing more is started)
+        if (*failed) break;
         mbar_expect(full(s), p.stage_bytes);
         bulk_load(sbase + s * p.stage_bytes,
-                  p.img + (size_t)(chunk0 + (int)(j % nch)) * p.stage_bytes, p.stage_bytes,
-                  full(s));
+                  p.img + (size_t)(chunk0 + j % nch) * p.stage_bytes, p.stage_bytes, full(s));
       }
       // no copy may be in flight when the CTA ends, after a failed wait either
-      for (long long j = total > p.nst ? total - p.nst : 0; j < total; ++j) {
-        const long long t0 = clock64();
-        while (!mbar_try(full((int)(j % p.nst)), (uint32_t)((j / p.nst) & 1)) &&
-               clock64() - t0 < kWaitClocks) {
-        }
-      }
+      for (int k = max(0, j - p.nst); k < j; ++k) mbar_drain(full(k % p.nst), (k / p.nst) & 1);
     }
-  } else {
+  } else if (nt > 0) {
     // ------------------------------------------------------------------------- row groups
-    const int g = warp >> 3, tid = threadIdx.x & (kGroupThreads - 1);
-    if (g < p.ng && nt > 0) {
-      uint8_t* Xs = smem + groups0 + (size_t)g * gbytes;
+    const int g = warp / kGroupWarps, tid = threadIdx.x & (kGroupThreads - 1);
+    const uint32_t row_lanes = (uint32_t)(warp & 3) << 21;  // 32 * quadrant in the lane field
+    const int row = (warp & 3) * 32 + lane, half = (warp >> 2) & 1;
+    auto arrive = [&](uint32_t bar) {
+      fence_async_shared();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    auto wait = [&](uint32_t bar, int phase) {
+      mbar_wait(bar, phase & 1, failed, status);
+      fence_after();
+    };
+    auto group_sync = [&]() {
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "n"(kGroupThreads) : "memory");
+    };
+    auto first_row = [&](int n) { return ((long long)me + (long long)n * ctas) * kTile; };
+    // tile n into its buffer, which is free; the tile behind the next on its way to L2
+    auto load = [&](int n) {
+      const long long r0 = first_row(n);
+      uint8_t* Xs = smem + x_off + (n % p.nx) * xbytes;
       uint8_t* Ys = Xs + nbx * 16384;
-      uint8_t* Hs = Xs + (nbx + (MODE == kFwd ? 0 : nby)) * 16384;
-      const uint32_t row_lanes = (uint32_t)(warp & 3) << 21;  // 32 * quadrant in the lane field
-      const uint32_t d = tmem + g * tg + row_lanes;
-      const int row = (warp & 3) * 32 + lane, half = (warp >> 2) & 1;
-      auto prefetch = [&](int n) {
-        if (n >= nt) return;
-        const long long r = (first + g + n * step) * kTile + (tid & (kTile - 1));
+      if (n + 2 < nt) {
+        const long long r = first_row(n + 2) + (tid & (kTile - 1));
         if (tid < kTile)
           prefetch_row(p.x, r, p.f.M);
         else if (MODE != kFwd)
           prefetch_row(p.dy, r, p.f.M);
-      };
-      auto arrive = [&](uint32_t bar) {
-        fence_async_shared();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-      };
-      auto group_sync = [&]() {
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "n"(kGroupThreads) : "memory");
-      };
-      // the rows of step n; in weights mode the tile's old rows are free once out_done came
-      uint32_t ph_gu = 0, ph_out = 0;
-      auto wait_out = [&]() {
-        mbar_wait(out_done(g), ph_out, failed, status);
-        ph_out ^= 1;
-        fence_after();
-      };
-      auto load = [&](int n, bool wait) {
-        const long long r0 = (first + g + n * step) * kTile;
-        uint4 bx[4], by[4];
-        if (p.x.aligned) fetch_rows(p.x, 0, r0, p.f.M, tid, bx);
-        if (MODE != kFwd && p.dy.aligned) fetch_rows(p.dy, 0, r0, p.f.M, tid, by);
-        if (wait) wait_out();
-        auto rest = [&](const RowSrc& src, int blocks, uint4 (&v)[4], uint8_t* dst) {
-          if (src.aligned) {
-            store_rows(0, tid, v, dst);
-            if (blocks > 1) {
-              fetch_rows(src, 1, r0, p.f.M, tid, v);
-              store_rows(1, tid, v, dst);
-            }
-          } else {
-            for (int b = 0; b < blocks; ++b) gather_rows(src, b, r0, p.f.M, tid, dst);
+      }
+      uint4 bx[4], by[4];
+      if (p.x.aligned) fetch_rows(p.x, 0, r0, p.f.M, tid, bx);
+      if (MODE != kFwd && p.dy.aligned) fetch_rows(p.dy, 0, r0, p.f.M, tid, by);
+      auto rest = [&](const RowSrc& src, int blocks, uint4 (&v)[4], uint8_t* dst) {
+        if (src.aligned) {
+          store_rows(0, tid, v, dst);
+          if (blocks > 1) {
+            fetch_rows(src, 1, r0, p.f.M, tid, v);
+            store_rows(1, tid, v, dst);
           }
-        };
-        rest(p.x, nbx, bx, Xs);
-        if (MODE != kFwd) rest(p.dy, nby, by, Ys);
-        arrive(x_ready(g));
+        } else {
+          for (int b = 0; b < blocks; ++b) gather_rows(src, b, r0, p.f.M, tid, dst);
+        }
       };
-      // this thread: row `row` of the tile, units half * 32 .. + 32, taken kUnits at a time; the
-      // next units' accumulators are on their way while one set is worked on
-      constexpr int kUnits = MODE == kFwd ? 16 : 8;
-      constexpr int kSteps = 32 / kUnits;
-      auto get = [&](int q, uint32_t (&ra)[kUnits], uint32_t (&ru)[kUnits],
-                     uint32_t (&rd)[kUnits]) {
-        const uint32_t at = d + half * 32 + q * kUnits;
-        tmem_ld(at, ra);
-        if (GATED) tmem_ld(at + 64, ru);
-        if (MODE != kFwd) tmem_ld(at + 128, rd);
-      };
-      auto work = [&](int q, const uint32_t (&ra)[kUnits], const uint32_t (&ru)[kUnits],
-                      const uint32_t (&rd)[kUnits]) {
-        uint32_t h[kUnits / 2], da[kUnits / 2], du[kUnits / 2];
+      rest(p.x, nbx, bx, Xs);
+      if (MODE != kFwd) rest(p.dy, nby, by, Ys);
+      arrive(x_ready(n % p.nx));
+    };
+    // Output of tile n through shared memory to the row array. With a place of its own it is taken
+    // by the group of the next tile's first item; else by that of the tile's last item, through the
+    // place of that item's hidden operand (whose product is done when the output is complete).
+    auto output = [&](int n, int i) {
+      const int cols = MODE == kFwd ? p.f.O : p.f.D;
+      const uint32_t src = acc + (n % p.no) * acc_step + row_lanes + half * 32;
+      // (the phase before is over: this group has seen the end of an item behind tile n - no)
+      if (p.staged) {
+        if (i == total && total >= 2) wait(done(total & 1), (total - 2) >> 1);
+        wait(out_full(n % p.no), n / p.no);
+      } else {
+        wait(done(i & 1), i >> 1);
+      }
+      uint8_t* S = smem + h_off + p.nh * kHBytes + g * 16384;
+      if (!p.staged) S = smem + h_off + (i % p.nh) * kHBytes;
+      for (int b = 0; b * 64 < cols; ++b) {
+        if (b * 64 + half * 32 < cols) {
+          uint32_t v0[16], v1[16];
+          tmem_ld(src + b * 64, v0);
+          tmem_ld(src + b * 64 + 16, v1);  // (inside the accumulator's 32-column padding)
+          tmem_wait(v0);
+          tmem_wait(v1);
 #pragma unroll
-        for (int e = 0; e < kUnits; e += 4) {
-          float a[4], f[4], sl[4], vh[4], va[4], vu[4];
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = __uint_as_float(ra[e + i]);
-          act4<ACT, MODE != kFwd>(a, f, sl);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float u = GATED ? __uint_as_float(ru[e + i]) : 1.0f;
-            vh[i] = GATED ? f[i] * u : f[i];
-            if (MODE != kFwd) {
-              const float dh = __uint_as_float(rd[e + i]);
-              va[i] = GATED ? dh * u * sl[i] : dh * sl[i];
-              vu[i] = dh * f[i];
+            for (int k = 0; k < 8; k += 2) {
+              const int j = (e + k) & 15;
+              w[k / 2] = e < 16 ? Two<T>::pack(__uint_as_float(v0[j]), __uint_as_float(v0[j + 1]))
+                                : Two<T>::pack(__uint_as_float(v1[j]), __uint_as_float(v1[j + 1]));
             }
+            *reinterpret_cast<uint4*>(S + row * 128 + (((half * 4 + e / 8) ^ (row & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
+        }
+        if ((b + 1) * 64 >= cols) arrive(out_free(n % p.no));
+        group_sync();
+        write_rows(S, (uint8_t*)(MODE == kFwd ? p.f.y : p.f.dx),
+                   2 * (MODE == kFwd ? p.f.ldy : p.f.lddx), p.out_aligned, b * 64, cols,
+                   first_row(n), p.f.M, tid);
+        group_sync();
+      }
+    };
+    // this thread: row `row` of the tile, units half * 32 .. + 32, taken kUnits at a time; the
+    // next units' accumulators are on their way while one set is worked on
+    constexpr int kUnits = MODE == kFwd ? 16 : 8;
+    constexpr int kSteps = 32 / kUnits;
+    auto get = [&](uint32_t d, int q, uint32_t (&ra)[kUnits], uint32_t (&ru)[kUnits],
+                   uint32_t (&rd)[kUnits]) {
+      const uint32_t at = d + half * 32 + q * kUnits;
+      tmem_ld(at, ra);
+      if (GATED) tmem_ld(at + 64, ru);
+      if (MODE != kFwd) tmem_ld(at + WR, rd);
+    };
+    auto landed = [&](uint32_t (&ra)[kUnits], uint32_t (&ru)[kUnits], uint32_t (&rd)[kUnits]) {
+      tmem_wait(ra);
+      if (GATED) tmem_wait(ru);
+      if (MODE != kFwd) tmem_wait(rd);
+    };
+    auto work = [&](uint8_t* Hs, int q, const uint32_t (&ra)[kUnits], const uint32_t (&ru)[kUnits],
+                    const uint32_t (&rd)[kUnits]) {
+      uint32_t h[kUnits / 2], da[kUnits / 2], du[kUnits / 2];
 #pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            h[(e + i) / 2] = Two<T>::pack(vh[i], vh[i + 1]);
-            if (MODE != kFwd) {
-              da[(e + i) / 2] = Two<T>::pack(va[i], va[i + 1]);
-              du[(e + i) / 2] = Two<T>::pack(vu[i], vu[i + 1]);
-            }
+      for (int e = 0; e < kUnits; e += 4) {
+        float a[4], f[4], sl[4], vh[4], va[4], vu[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a[k] = __uint_as_float(ra[e + k]);
+        act4<ACT, MODE != kFwd>(a, f, sl);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float u = GATED ? __uint_as_float(ru[e + k]) : 1.0f;
+          vh[k] = GATED ? f[k] * u : f[k];
+          if (MODE != kFwd) {
+            const float dh = __uint_as_float(rd[e + k]);
+            va[k] = GATED ? dh * u * sl[k] : dh * sl[k];
+            vu[k] = dh * f[k];
           }
         }
 #pragma unroll
-        for (int e = 0; e < kUnits; e += 8) {
-          const int piece = half * 4 + (q * kUnits + e) / 8;
-          uint8_t* at = Hs + row * 128 + ((piece ^ (row & 7)) << 4);
-          auto put = [&](int block, const uint32_t* v) {
-            *reinterpret_cast<uint4*>(at + block * 16384) = make_uint4(v[0], v[1], v[2], v[3]);
-          };
-          if (MODE == kFwd) {
-            put(0, h + e / 2);
-          } else {
-            put(0, da + e / 2);
-            if (GATED) put(1, du + e / 2);
-            if (MODE == kDw) put(GATED ? 2 : 1, h + e / 2);
+        for (int k = 0; k < 4; k += 2) {
+          h[(e + k) / 2] = Two<T>::pack(vh[k], vh[k + 1]);
+          if (MODE != kFwd) {
+            da[(e + k) / 2] = Two<T>::pack(va[k], va[k + 1]);
+            du[(e + k) / 2] = Two<T>::pack(vu[k], vu[k + 1]);
           }
-        }
-      };
-      auto landed = [&](uint32_t (&ra)[kUnits], uint32_t (&ru)[kUnits], uint32_t (&rd)[kUnits]) {
-        tmem_wait(ra);
-        if (GATED) tmem_wait(ru);
-        if (MODE != kFwd) tmem_wait(rd);
-      };
-
-      prefetch(1);
-      load(0, false);
-      for (int n = 0; n < nt; ++n) {
-        prefetch(n + 2);
-        for (int c = 0; c < nch; ++c) {
-          mbar_wait(gu_full(g), ph_gu, failed, status);
-          ph_gu ^= 1;
-          fence_after();
-          uint32_t a0[kUnits], u0[kUnits], d0[kUnits], a1[kUnits], u1[kUnits], d1[kUnits];
-          get(0, a0, u0, d0);
-#pragma unroll
-          for (int q = 0; q < kSteps; q += 2) {
-            landed(a0, u0, d0);
-            get(q + 1, a1, u1, d1);
-            work(q, a0, u0, d0);
-            landed(a1, u1, d1);
-            if (q + 2 < kSteps) get(q + 2, a0, u0, d0);
-            work(q + 1, a1, u1, d1);
-          }
-          arrive(h_ready(g));
-        }
-        // the tile's first products are done, so its rows make room for the next tile's (weights:
-        // after the second product, which reads them too)
-        const bool more = n + 1 < nt;
-        if (more) load(n + 1, MODE == kDw);
-        if (MODE != kDw) {
-          wait_out();
-          // results to shared memory (the hidden operand's place, free now), then out
-          const int cols = MODE == kFwd ? p.f.O : p.f.D;
-          const uint32_t src = d + (MODE == kFwd ? 128 : 192) + half * 32;
-          for (int b = 0; b * 64 < cols; ++b) {
-            if (b * 64 + half * 32 < cols) {
-              uint32_t v0[16], v1[16];
-              tmem_ld(src + b * 64, v0);
-              tmem_ld(src + b * 64 + 16, v1);  // (inside the accumulator's 32-column padding)
-              tmem_wait(v0);
-              tmem_wait(v1);
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint32_t w[4];
-#pragma unroll
-                for (int k = 0; k < 8; k += 2) {
-                  const int i = (e + k) & 15;
-                  w[k / 2] = e < 16 ? Two<T>::pack(__uint_as_float(v0[i]), __uint_as_float(v0[i + 1]))
-                                    : Two<T>::pack(__uint_as_float(v1[i]), __uint_as_float(v1[i + 1]));
-                }
-                *reinterpret_cast<uint4*>(Hs + row * 128 +
-                                          (((half * 4 + e / 8) ^ (row & 7)) << 4)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            }
-            group_sync();
-            write_rows(Hs, (uint8_t*)(MODE == kFwd ? p.f.y : p.f.dx),
-                       2 * (MODE == kFwd ? p.f.ldy : p.f.lddx), p.out_aligned, b * 64, cols,
-                       (first + g + n * step) * kTile, p.f.M, tid);
-            group_sync();
-          }
-        } else if (!more) {
-          wait_out();
         }
       }
+#pragma unroll
+      for (int e = 0; e < kUnits; e += 8) {
+        const int piece = half * 4 + (q * kUnits + e) / 8;
+        uint8_t* at = Hs + row * 128 + ((piece ^ (row & 7)) << 4);
+        auto put = [&](int block, const uint32_t* v) {
+          *reinterpret_cast<uint4*>(at + block * 16384) = make_uint4(v[0], v[1], v[2], v[3]);
+        };
+        if (MODE == kFwd) {
+          put(0, h + e / 2);
+        } else {
+          put(0, da + e / 2);
+          if (GATED) put(1, du + e / 2);
+          if (MODE == kDw) put(GATED ? 2 : 1, h + e / 2);
+        }
+      }
+    };
+
+    for (int n = g; n < min(p.nx, nt); n += 2) load(n);
+    int c = g, n = 0;
+    for (int i = g; i < total; i += 2, c += 2) {
+      while (c >= nch) c -= nch, ++n;
+      wait(gu_full(i % gu_bars), i / gu_bars);
+      const uint32_t d = tmem + (i % p.ngu) * kGu + row_lanes;
+      uint8_t* Hs = smem + h_off + (i % p.nh) * kHBytes;
+      uint32_t a0[kUnits], u0[kUnits], d0[kUnits], a1[kUnits], u1[kUnits], d1[kUnits];
+      get(d, 0, a0, u0, d0);
+      // the hidden operand's place was item i - nh's
+      if (i >= p.nh) wait(done((i - p.nh) & 1), (i - p.nh) >> 1);
+#pragma unroll
+      for (int q = 0; q < kSteps; q += 2) {
+        landed(a0, u0, d0);
+        get(d, q + 1, a1, u1, d1);
+        work(Hs, q, a0, u0, d0);
+        landed(a1, u1, d1);
+        if (q + 2 < kSteps) get(d, q + 2, a0, u0, d0);
+        work(Hs, q + 1, a1, u1, d1);
+      }
+      // Waits for `done` stand where the next phase of the barrier cannot complete before them: for
+      // an earlier item before this one is handed over, for this one before the group's next.
+      if (MODE == kDw) {
+        // the rows of tile i - 1 (three buffers) or i (two) make room for tile i + 2, once their
+        // second product is done
+        if (p.nx == 3 && i > 0) wait(done((i - 1) & 1), (i - 1) >> 1);
+        arrive(h_ready(i & 1));
+        if (i + 2 < nt) {
+          if (p.nx == 2) wait(done(i & 1), i >> 1);
+          if (p.nx == 2 || i + 2 >= p.nx) load(i + 2);
+        }
+      } else {
+        arrive(h_ready(i & 1));
+        // the tile's first products are done: its rows make room
+        if (c == nch - 1 && n + p.nx < nt) load(n + p.nx);
+        if (p.staged ? c == 0 && n > 0 : c == nch - 1) output(p.staged ? n - 1 : n, i);
+      }
     }
+    if (MODE != kDw && p.staged && g == (total & 1)) output(nt - 1, total);
   }
 
-  if (MODE == kDw && warp < 8) {
+  if (MODE == kDw && warp < kGroupWarps) {
     // the CTA's sums: lanes are units (gate, up | up or gate, h), columns D or O
     const int row = (warp & 3) * 32 + lane, half = warp >> 2;
     const uint32_t row_lanes = (uint32_t)(warp & 3) << 21;
@@ -723,7 +724,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
     float* part = p.f.part + (size_t)me * ((GATED ? 2 : 1) * FD + (size_t)p.f.F * p.f.O);
     const int f = chunk0 * kChunk + (row & 63);
     if (nt > 0) {
-      mbar_wait(all_done, 0, failed, status);
+      mbar_drain(all_done, 0);
       fence_after();
     }
     for (int which = 0; which < 2; ++which) {
@@ -733,7 +734,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
                                  : (row >= 64 ? FD : 0) + (size_t)f * p.f.D);
       for (int e0 = half * 8; e0 < cols; e0 += 16) {
         uint32_t v[8];
-        tmem_ld((which ? acc_d : acc_gu) + row_lanes + e0, v);
+        tmem_ld(acc + which * acc_step + row_lanes + e0, v);
         tmem_wait(v);
         if (mine)
 #pragma unroll
@@ -744,9 +745,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
   }
   fence_before();
   __syncthreads();
-  if (warp == kMaxGroups * 8) {
+  if (warp == 2 * kGroupWarps) {
     // every MMA is done before TMEM is given back
-    if (nt > 0) mbar_wait(all_done, 0, failed, status);
+    if (nt > 0) mbar_drain(all_done, 0);
     fence_after();
     __syncwarp();
     tmem_free(tmem, kCols);
@@ -780,6 +781,46 @@ int stage_bytes(int D, int O, bool gated) {
   return (D + 63) / 64 * (gated ? 128 : 64) * 128 + pad16(O) * 128;
 }
 
+// What a CTA keeps in shared memory and TMEM. Two weight stages at least (a ring needs them, unless
+// there is one chunk), then as many row tiles and hidden operands as fit, a place for outputs, and
+// with the rest more weight stages. Weights mode wants three row tiles, so that a tile's loads wait
+// for nothing but the other group's products.
+struct Fit {
+  int nst, nx, nh, staged, ngu, no, smem;
+};
+
+Fit fit_of(int mode, bool gated, int dp, int op, int stage, int nch) {
+  static const int kOut[][3] = {{2, 2, 1}, {2, 2, 0}, {1, 2, 1}, {1, 2, 0}};  // nx, nh, staged
+  static const int kSum[][3] = {{3, 2, 0}, {2, 2, 0}, {2, 1, 0}, {0, 0, 0}};
+  Fit f = {};
+  const int gu = gu_cols(mode, gated);
+  if (mode == kDw) {
+    f.ngu = (512 - pad32(dp) - pad32(op)) / gu;
+  } else {
+    const int out = pad32(mode == kFwd ? op : dp);
+    f.no = (512 - 2 * out) / gu >= 2 ? 2 : 1;
+    f.ngu = (512 - f.no * out) / gu;
+    if (f.ngu < 2) return Fit{};  // (an output may wait for the item after its own)
+  }
+  if (f.ngu > kMaxGu) f.ngu = kMaxGu;
+  if (f.ngu < 1) return Fit{};
+  for (int k = 0; k < 4; ++k) {
+    const int* o = mode == kDw ? kSum[k] : kOut[k];
+    if (o[0] == 0) break;
+    const int used = o[0] * rows_bytes(mode, dp, op) + o[1] * hidden_bytes(mode, gated) +
+                     o[2] * 2 * 16384;  // (a place for each group)
+    const int nst = std::min({(kSmemLimit - used) / stage, nch, kMaxStages});
+    if (used > kSmemLimit || nst < std::min(nch, 2)) continue;
+    f.nx = o[0];
+    f.nh = o[1];
+    f.staged = o[2];
+    f.nst = nst;
+    f.smem = nst * stage + used + 1024;
+    return f;
+  }
+  return Fit{};
+}
+
 template <int MODE, typename T, int ACT, bool GATED>
 int launch(TcArgs p, cudaStream_t st) {
   const bool one = p.f.M <= 1;  // a single row's stride is never used
@@ -787,28 +828,22 @@ int launch(TcArgs p, cudaStream_t st) {
   if (MODE != kFwd) p.dy = row_src(p.f.dy, p.f.lddy, p.f.M, p.f.O);
   if (MODE == kFwd) p.out_aligned = aligned16(p.f.y, one ? 0 : p.f.ldy, p.f.O);
   if (MODE == kDx) p.out_aligned = aligned16(p.f.dx, one ? 0 : p.f.lddx, p.f.D);
-  const int nch = MODE == kDw ? 1 : p.nch, gb = smem_group(MODE, p.dp, p.op, GATED);
-  const int extra = MODE == kDw ? ((p.dp + 31) & ~31) + ((p.op + 31) & ~31) : 0;
-  // two groups where tensor memory and shared memory hold them with two weight stages
-  const int min_st = nch < 2 ? nch : 2;
-  p.ng = 2 * tmem_group(MODE, p.dp, p.op) + extra <= 512 &&
-                 2 * gb + min_st * p.stage_bytes <= kSmemLimit && p.tiles > 1
-             ? 2
-             : 1;
-  int nst = (kSmemLimit - p.ng * gb) / p.stage_bytes;
-  if (nst > kMaxStages) nst = kMaxStages;
-  if (nst > nch) nst = nch;
-  // (a ring needs two stages: the MMA thread asks for the next chunk before it frees this one)
-  if (nst < min_st || p.ng * tmem_group(MODE, p.dp, p.op) + extra > 512) return SPLAT_ERR_CAPACITY;
-  p.nst = nst;
-  const int smem = p.nst * p.stage_bytes + p.ng * gb + 1024;
-  long long grid = MODE == kDw ? (long long)p.nch * p.f.splits : (p.tiles + p.ng - 1) / p.ng;
-  if (MODE != kDw && grid > 148) grid = 148;
+  const int nch = MODE == kDw ? 1 : p.nch;
+  const Fit fit = fit_of(MODE, GATED, p.dp, p.op, p.stage_bytes, nch);
+  if (!fit.nst) return SPLAT_ERR_CAPACITY;
+  p.nst = fit.nst;
+  p.nx = fit.nx;
+  p.nh = fit.nh;
+  p.staged = fit.staged;
+  p.ngu = fit.ngu;
+  p.no = fit.no;
+  const long long grid =
+      MODE == kDw ? (long long)p.nch * p.f.splits : std::min(p.tiles, 148LL);
   auto kernel = k_ffn_tc<MODE, T, ACT, GATED>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, fit.smem) !=
       cudaSuccess)
     return SPLAT_ERR_CUDA;
-  kernel<<<(unsigned)grid, kTcThreads, smem, st>>>(p);
+  kernel<<<(unsigned)grid, kTcThreads, fit.smem, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? SPLAT_OK : SPLAT_ERR_CUDA;
 }
 

@@ -59,6 +59,14 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same for what must be over before a kernel goes on even after a failed wait: copies and MMAs
+// in flight, which end by themselves.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try(bar, parity) && clock64() - t0 < kWaitClocks) {
+  }
+}
+
 // contiguous copy global -> shared, completing on the barrier (16-byte aligned, multiple of 16)
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {

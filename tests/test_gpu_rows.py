@@ -189,6 +189,10 @@ FFNS = [  # M, D, F, O, gated, act, pad
     (1000, 65, 129, 66, False, "silu", 2), (1000, 8, 1024, 3, True, "silu", 0),
     (513, 128, 1024, 128, True, "silu", 0), (4097, 21, 40, 9, False, "gelu", 0),
     (20000, 30, 130, 62, True, "silu", 2), (40000, 57, 64, 64, True, "gelu", 0),
+    # several row tiles a CTA at every combination of widths up to and above 64
+    (40000, 128, 200, 128, True, "silu", 0), (40000, 100, 64, 20, False, "gelu", 0),
+    (40000, 40, 70, 128, True, "silu", 0), (60000, 128, 60, 40, True, "gelu", 0),
+    (40000, 33, 520, 33, False, "silu", 1), (30000, 128, 100, 128, False, "silu", 0),
 ]
 
 
