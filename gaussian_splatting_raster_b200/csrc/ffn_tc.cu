@@ -22,6 +22,8 @@
 // shared memory where they fit. Row tiles are read with plain loads, which take any row distance
 // and alignment (token rows have odd widths), straight into the swizzled layout, a tile or two
 // ahead.
+#include <cuda.h>
+
 #include <algorithm>
 
 #include "ffn.cuh"
@@ -37,7 +39,8 @@ enum Mode { kFwd, kDx, kDw };
 
 constexpr int kGroupThreads = 256;
 constexpr int kGroupWarps = kGroupThreads / 32;
-constexpr int kTcThreads = 2 * kGroupThreads + 64;  // + MMA warp + weight warp
+constexpr int kLoaders = 64;
+constexpr int kTcThreads = 2 * kGroupThreads + 64 + kLoaders;  // + both products, + row tiles
 constexpr int kMaxStages = 16;
 constexpr int kMaxGu = 3, kMaxRows = 3;  // accumulators of first products; row tiles
 constexpr int kTile = 128;
@@ -45,11 +48,11 @@ constexpr int kSmemLimit = 232448 - 2048;  // 227 KB less the alignment slack an
 
 __device__ unsigned int g_rows_status;
 
-// A row array as the loads see it: 16-byte pieces may be taken from [lo, hi) only.
+// A row array as the loads see it: words may be taken from [lo, hi) only.
 struct RowSrc {
-  const uint8_t *base, *lo, *hi;  // lo, hi: 16-byte aligned, inside the array
+  const uint8_t *base, *lo, *hi;  // lo, hi: 4-byte aligned, inside the array
   long long ld;                   // bytes
-  int cols, aligned;              // aligned: every row starts and ends at 16 bytes
+  int cols, tiled;                // tiled: read through the tensor map
 };
 
 struct TcArgs {
@@ -95,55 +98,89 @@ __device__ __forceinline__ float rcp_fast(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-__device__ __forceinline__ void rcp4(const float (&p)[4], float (&r)[4]) {
-  const float m01 = p[0] * p[1], m23 = p[2] * p[3];
-  const float i = rcp_fast(m01 * m23);
-  const float i01 = i * m23, i23 = i * m01;
-  r[0] = i01 * p[1];
-  r[1] = i01 * p[0];
-  r[2] = i23 * p[3];
-  r[3] = i23 * p[2];
+
+// two fp32 lanes of one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<unsigned long long*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ void rcp4(const float2 (&p)[2], float2 (&r)[2]) {
+  const float2 m = mul2(p[0], p[1]);  // p0 p2, p1 p3
+  const float i = rcp_fast(m.x * m.y);
+  const float2 w = make_float2(i * m.y, i * m.x);
+  r[0] = mul2(w, p[1]);
+  r[1] = mul2(w, p[0]);
 }
 
-// act and its slope for four values. MODE-independent; without SLOPE the slope is not formed.
+// act and its slope for four values (without SLOPE the slope is not formed).
 //   silu: s = 1 / (1 + 2^t), t = -a log2 e held at 31 so that four factors stay finite: s is then
-//         never below 2^-31, which differs from the true value by less than an fp32 step of 1/128.
+//         never below 2^-31, less than half an fp32 step of 1 away from the true value.
 //   gelu: Phi by Abramowitz and Stegun 7.1.26 (erfc at z = |a| / sqrt 2, absolute error 0.75e-7 in
 //         Phi), z held at 10 where Phi(-|a|) has long become zero; one power e^{-a^2/2} serves Phi
 //         and the density.
 // An argument that is no number gives no number: both are multiplied by a, or built from it.
 template <int ACT, bool SLOPE>
-__device__ __forceinline__ void act4(const float* a, float* f, float* slope) {
-  float p[4], r[4];
+__device__ __forceinline__ void act4(const float2 (&a)[2], float2 (&f)[2], float2 (&slope)[2]) {
+  float2 p[2], r[2];
   if (ACT == SPLAT_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      p[i] = 1.0f + ex2_fast(fminf(a[i] * -1.4426950408889634f, 31.0f));
+    for (int i = 0; i < 2; ++i) {
+      const float2 t = mul2(a[i], both(-1.4426950408889634f));
+      p[i] = add2(make_float2(ex2_fast(fminf(t.x, 31.0f)), ex2_fast(fminf(t.y, 31.0f))),
+                  both(1.0f));
+    }
     rcp4(p, r);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[i] = a[i] * r[i];
-      if (SLOPE) slope[i] = fmaf(f[i], 1.0f - r[i], r[i]);
+    for (int i = 0; i < 2; ++i) {
+      f[i] = mul2(a[i], r[i]);
+      if (SLOPE) slope[i] = fma2(f[i], fma2(r[i], both(-1.0f), both(1.0f)), r[i]);
     }
   } else {
-    float z[4];
+    float2 z[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      z[i] = fminf(fabsf(a[i]) * 0.70710678118654752f, 10.0f);
-      p[i] = fmaf(0.3275911f, z[i], 1.0f);
+    for (int i = 0; i < 2; ++i) {
+      z[i] = mul2(a[i], both(0.70710678118654752f));
+      z[i] = make_float2(fminf(fabsf(z[i].x), 10.0f), fminf(fabsf(z[i].y), 10.0f));
+      p[i] = fma2(both(0.3275911f), z[i], both(1.0f));
     }
     rcp4(p, r);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float e = ex2_fast(z[i] * z[i] * -1.4426950408889634f);
-      float q = fmaf(0.5307027145f, r[i], -0.7265760135f);  // half the published coefficients
-      q = fmaf(q, r[i], 0.7107068705f);
-      q = fmaf(q, r[i], -0.142248368f);
-      q = fmaf(q, r[i], 0.127414796f);
-      q = q * r[i] * e;
-      const float c = a[i] >= 0.0f ? 1.0f - q : q;
-      f[i] = a[i] * c;
-      if (SLOPE) slope[i] = fmaf(a[i] * 0.3989422804014327f, e, c);
+    for (int i = 0; i < 2; ++i) {
+      const float2 t = mul2(mul2(z[i], z[i]), both(-1.4426950408889634f));
+      const float2 e = make_float2(ex2_fast(t.x), ex2_fast(t.y));
+      // half the published coefficients
+      float2 q = fma2(both(0.5307027145f), r[i], both(-0.7265760135f));
+      q = fma2(q, r[i], both(0.7107068705f));
+      q = fma2(q, r[i], both(-0.142248368f));
+      q = fma2(q, r[i], both(0.127414796f));
+      q = mul2(mul2(q, r[i]), e);
+      const float2 c = make_float2(a[i].x >= 0.0f ? 1.0f - q.x : q.x,
+                                   a[i].y >= 0.0f ? 1.0f - q.y : q.y);
+      f[i] = mul2(a[i], c);
+      if (SLOPE) slope[i] = fma2(mul2(a[i], both(0.3989422804014327f)), e, c);
     }
   }
 }
@@ -194,91 +231,58 @@ k_pack(TcArgs p, uint8_t* __restrict__ img) {
 // row tiles
 // ---------------------------------------------------------------------------------------------
 
-// A group takes its tile of rows [r0, r0 + 128) with eight threads to a row: thread t has piece
-// t & 7 (16 bytes, 8 elements) of each 64-column block of rows t / 8 + 32 j. The swizzle and a
-// row's offset from 16-byte alignment are then the same for all four j. Rows >= M are zeros, and
-// so are elements behind a row's end up to the next multiple of 16 (the MMAs' step; nothing reads
-// what lies behind).
-
-// aligned rows: one 64-column block's loads, started and then stored
-__device__ __forceinline__ void fetch_rows(const RowSrc& s, int block, long long r0, long long M,
-                                           int tid, uint4 (&v)[4]) {
-  const int c = block * 8 + (tid & 7);
-  const long long r = r0 + (tid >> 3);
-  const uint8_t* p = s.base + r * s.ld + c * 16;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (c * 8 < s.cols && r + 32 * j < M)
-      v[j] = __ldg(reinterpret_cast<const uint4*>(p + 32 * j * s.ld));
-  }
-}
-
-__device__ __forceinline__ uint8_t* piece_at(uint8_t* dst, int block, int tid) {
-  return dst + block * 16384 + (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4);
-}
-
-__device__ __forceinline__ void store_rows(int block, int tid, const uint4 (&v)[4], uint8_t* dst) {
-  uint8_t* q = piece_at(dst, block, tid);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(q + j * 4096) = v[j];
-}
-
-// any other rows: the aligned 16-byte pieces around each piece (odd widths start anywhere), shifted
-// into place. Pieces that reach over the array's ends are gathered element by element.
+// Row tiles come by TMA where the rows allow it (start and distance multiples of 16 bytes): one
+// instruction a 64-column block, zeros behind the last row and column. Any other rows (odd widths
+// start anywhere) are taken by the loader warps, eight threads to a row: thread t has piece t & 7
+// (8 elements) of the block in rows t / 8 + 8 j, read as the five words around it and shifted by
+// half a word where the row starts on an odd element. Rows >= M are zeros, and so are elements
+// behind a row's end up to the block's.
 __device__ __forceinline__ void gather_rows(const RowSrc& s, int block, long long r0, long long M,
                                             int tid, uint8_t* dst) {
   const int c = block * 8 + (tid & 7);
   const long long r = r0 + (tid >> 3);
   const uint8_t* p = s.base + r * s.ld + c * 16;
   const int n = min(8, s.cols - c * 8);  // elements wanted
-  const uint32_t off = (uint32_t)(uintptr_t)p & 15u;
-  const bool two = (int)off + 2 * n > 16;
-  uint8_t* q = piece_at(dst, block, tid);
+  uint8_t* q = dst + block * 16384 + (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4);
+  constexpr int U = 4;
+  for (int j0 = 0; j0 < kTile / 8; j0 += U, p += 8 * U * s.ld, q += U * 1024) {
+    uint32_t w[U][5];
+    uint32_t sh[U];
 #pragma unroll
-  for (int j = 0; j < 4; ++j, p += 32 * s.ld) {
-    uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    if (n > 0 && r + 32 * j < M) {
-      const uint8_t* a = p - off;
-      if (a >= s.lo && a + (two ? 32 : 16) <= s.hi) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a));
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        if (two) {
-          const uint4 u = __ldg(reinterpret_cast<const uint4*>(a + 16));
-          w[4] = u.x, w[5] = u.y, w[6] = u.z, w[7] = u.w;
+    for (int j = 0; j < U; ++j) {
+      const uint8_t* e = p + 8 * j * s.ld;
+      const uint8_t* a = (const uint8_t*)((uintptr_t)e & ~(uintptr_t)3);
+      sh[j] = ((uint32_t)(uintptr_t)e & 2u) * 8u;
+      const int words = n > 0 && r + 8 * (j0 + j) < M ? (2 * n + (int)(sh[j] >> 3) + 3) >> 2 : 0;
+      const bool whole = a >= s.lo && a + 4 * words <= s.hi;
+#pragma unroll
+      for (int k = 0; k < 5; ++k) {
+        w[j][k] = 0u;
+        if (k < words) {
+          if (whole) {
+            w[j][k] = __ldg(reinterpret_cast<const uint32_t*>(a) + k);
+          } else {  // at the array's ends: element by element
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint8_t* x = a + 4 * k + 2 * h;
+              if (x >= e && x < e + 2 * n)
+                w[j][k] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(x)) << (16 * h);
+            }
+          }
         }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (2 * k >= (int)off && 2 * k < (int)off + 2 * n)
-            w[k >> 1] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(a + 2 * k))
-                         << ((k & 1) * 16);
       }
     }
-    if (off & 4u) {
 #pragma unroll
-      for (int k = 0; k < 7; ++k) w[k] = w[k + 1];
-    }
-    if (off & 8u) {
+    for (int j = 0; j < U; ++j) {
+      uint32_t v[4];
 #pragma unroll
-      for (int k = 0; k < 5; ++k) w[k] = w[k + 2];
+      for (int k = 0; k < 4; ++k) {
+        v[k] = __funnelshift_r(w[j][k], w[j][k + 1], sh[j]);
+        if (n < 8) v[k] = n >= 2 * k + 2 ? v[k] : n == 2 * k + 1 ? v[k] & 0xFFFFu : 0u;
+      }
+      *reinterpret_cast<uint4*>(q + j * 1024) = make_uint4(v[0], v[1], v[2], v[3]);
     }
-    const uint32_t sh = (off & 2u) * 8u;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      w[k] = __funnelshift_r(w[k], w[k + 1], sh);
-      if (n < 8) w[k] = n >= 2 * k + 2 ? w[k] : n == 2 * k + 1 ? w[k] & 0xFFFFu : 0u;
-    }
-    *reinterpret_cast<uint4*>(q + j * 4096) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-}
-
-// the rows' lines on their way into L2
-__device__ __forceinline__ void prefetch_row(const RowSrc& s, long long r, long long M) {
-  if (r >= M) return;
-  const uint8_t* p = s.base + r * s.ld;
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p + s.cols * 2 - 2));
 }
 
 // One 64-column block of results (columns col0 ..) from shared memory to a row array: aligned rows
@@ -326,9 +330,11 @@ __host__ __device__ constexpr int hidden_bytes(int mode, bool gated) {
 }
 
 template <int MODE, typename T, int ACT, bool GATED>
-__global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
+__global__ void __launch_bounds__(kTcThreads, 1)
+k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x_map,
+         const __grid_constant__ CUtensorMap dy_map) {
   extern __shared__ uint8_t raw[];
-  constexpr int kBars = 2 * kMaxStages + kMaxGu + kMaxRows + 2 + 2 + 2 + 2 + 1;
+  constexpr int kBars = 2 * kMaxStages + 2 * kMaxGu + 2 * kMaxRows + 2 + 2 + 2 + 2 + 1;
   __shared__ __align__(8) uint64_t s_bar[kBars];
   __shared__ uint32_t s_tmem;
   __shared__ int s_failed;
@@ -347,8 +353,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
   auto empty = [&](int k) { return bars + 8 * (kMaxStages + k); };    // ... are used
   constexpr int kB0 = 2 * kMaxStages;
   auto gu_full = [&](int k) { return bars + 8 * (kB0 + k); };         // a first product is done
-  auto x_ready = [&](int k) { return bars + 8 * (kB0 + kMaxGu + k); };  // a row tile is there
-  constexpr int kB1 = kB0 + kMaxGu + kMaxRows;
+  auto gu_free = [&](int k) { return bars + 8 * (kB0 + kMaxGu + k); };  // ... has been read
+  constexpr int kB2 = kB0 + 2 * kMaxGu;
+  auto x_ready = [&](int k) { return bars + 8 * (kB2 + k); };           // a row tile is there
+  auto x_free = [&](int k) { return bars + 8 * (kB2 + kMaxRows + k); };  // ... is used
+  constexpr int kB1 = kB2 + 2 * kMaxRows;
   auto h_ready = [&](int k) { return bars + 8 * (kB1 + k); };     // item's hidden operand, by parity
   auto done = [&](int k) { return bars + 8 * (kB1 + 2 + k); };    // item's second product, by parity
   auto out_full = [&](int k) { return bars + 8 * (kB1 + 4 + k); };  // a tile's output is complete
@@ -360,8 +369,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
   if (threadIdx.x == 0) {
     s_failed = 0;
     for (int k = 0; k < kBars; ++k) {
-      const bool by_warps = (k >= kB0 + kMaxGu && k < kB1 + 2) || k == kB1 + 6 || k == kB1 + 7;
-      mbar_init(bars + 8 * k, by_warps ? kGroupWarps : 1);
+      const bool by_group = (k >= kB0 + kMaxGu && k < kB2) || k == kB1 || k == kB1 + 1 ||
+                            k == kB1 + 6 || k == kB1 + 7;
+      const bool by_loaders = k >= kB2 && k < kB2 + kMaxRows;
+      mbar_init(bars + 8 * k, by_group ? kGroupWarps : by_loaders ? kLoaders / 32
+                                                                    : k == kB1 + 8 ? 2 : 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_shared();
@@ -388,108 +400,71 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
   // waiting group has seen) or one before it has the phase before on item i's.
   const int gu_bars = max(p.ngu, 2);
 
+  // descriptors count in 16 bytes: a step of 16 along K is 2 in a K-major tile (4 steps to a
+  // 64-column block), 128 in an MN-major one; weights' blocks have WR rows
+  constexpr uint32_t kBlk = 16384 >> 4, kWBlk = WR * 128 >> 4;
+  constexpr uint32_t kMn = (16384 >> 4) << 16, kWMn = (WR * 128 >> 4) << 16, kK = 1u << 16;
+  const uint32_t xs = xbytes >> 4, ss = p.stage_bytes >> 4;
+  const uint32_t y_off = nbx * kBlk, down_off = nbx * kWBlk;
+  // (whole warps ask the barriers, one lane issues)
+  auto is_there = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_test(bar, parity)) || *failed;
+  };
   if (warp == 2 * kGroupWarps) {
-    // ------------------------------------------------------------------------- MMA issue
-    // (the whole warp polls, one lane issues)
+    // ------------------------------------------------------------- first products, weight loads
     if (nt > 0) {
       const int kx = p.dp >> 4, ko = p.op >> 4;
       const uint32_t id_gu = idesc(BF, WR, false, false), id_dh = idesc(BF, 64, false, true);
-      const uint32_t id_out = MODE == kFwd  ? idesc(BF, p.op, false, false)
-                              : MODE == kDx ? idesc(BF, p.dp, false, true)
-                                            : idesc(BF, p.dp, true, true);
-      const uint32_t id_wy = idesc(BF, p.op, true, true);
-      // descriptors count in 16 bytes: a step of 16 along K is 2 in a K-major tile (4 steps to a
-      // 64-column block), 128 in an MN-major one; weights' blocks have WR rows
-      constexpr uint32_t kBlk = 16384 >> 4, kWBlk = WR * 128 >> 4;
-      const uint32_t xs = xbytes >> 4, ss = p.stage_bytes >> 4;
-      const uint32_t x_k = desc_lo(sbase + x_off, 16), h_k = desc_lo(sbase + h_off, 16);
-      const uint32_t w_k = desc_lo(sbase, 16);
-      constexpr uint32_t kMn = (16384 >> 4) << 16, kWMn = (WR * 128 >> 4) << 16, kK = 1u << 16;
-      const uint32_t y_off = nbx * kBlk, down_off = nbx * kWBlk;
-      // A|U (and dH) of a row tile and a weight stage
-      auto first_product = [&](int gu, int bar, int xb, int s) {
-        if (elect_one()) {
-          const uint32_t d = tmem + gu * kGu;
-          const uint32_t a = x_k + xb * xs, b = w_k + s * ss;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < kx)
-              mma(d, a + (k >> 2) * kBlk + (k & 3) * 2, b + (k >> 2) * kWBlk + (k & 3) * 2, id_gu,
-                  k > 0);
-          if (MODE != kFwd) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k < ko)
-                mma(d + WR, a + y_off + (k >> 2) * kBlk + (k & 3) * 2, b + down_off + k * 128,
-                    id_dh, k > 0);
-          }
-          commit(gu_full(bar));
-        }
-        __syncwarp();
-      };
-      auto second_product = [&](int i, int hb, int xb, int s, int o, bool add, bool last_chunk) {
-        if (elect_one()) {
-          const uint32_t h = h_k + hb * (kHBytes >> 4), w = w_k + s * ss;
-          if (MODE == kFwd) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma(acc + o * acc_step, h + k * 2, w + down_off + k * 2, id_out, add || k > 0);
-          } else if (MODE == kDx) {
-#pragma unroll
-            for (int k = 0; k < WR / 16; ++k)
-              mma(acc + o * acc_step, h + (k >> 2) * kBlk + (k & 3) * 2,
-                  w - kK + kWMn + k * 128, id_out, add || k > 0);
-          } else {
-            const uint32_t hm = h - kK + kMn, x = x_k - kK + kMn + xb * xs;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) mma(acc, hm + k * 128, x + k * 128, id_out, add || k > 0);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma(acc + acc_step, hm + (GATED ? kBlk : 0) + k * 128, x + y_off + k * 128, id_wy,
-                  add || k > 0);
-          }
-          commit(done(i & 1));
-          if (MODE != kDw && last_chunk) commit(out_full(o));
-          if (ring) commit(empty(s));
-          if (i == total - 1) commit(all_done);
-        }
-        __syncwarp();
-      };
-      auto is_there = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_try(bar, parity)) || *failed;
-      };
-      // next first product: item, chunk, buffer and parity of accumulator, rows, weights
+      const uint32_t x_k = desc_lo(sbase + x_off, 16), w_k = desc_lo(sbase, 16);
+      // next product: item, chunk, accumulator (and its barrier), rows, weights
       int i1 = 0, c1 = 0, gu = 0, gb = 0, x1 = 0, s1 = 0;
-      uint32_t px = 0, pw = 0;
+      uint32_t pg = 1, px = 0, pw = 0;  // (the first round of accumulators is free)
       bool fresh = true;  // the stage's weights are to be waited for
-      // next second product: item, chunk, hidden operand, rows, weights, output and its parity
-      int i2 = 0, c2 = 0, hb = 0, x2 = 0, s2 = 0, o2 = 0;
-      uint32_t po = 1;  // (the first round of outputs has nobody to wait for)
+      // next chunk's weights: number, chunk, stage
+      const int uses = ring ? total : nch;
+      int j = 0, cj = 0, sj = 0;
+      uint32_t pe = 1;
       long long since = clock64();
-      while (i2 < total) {
+      while (i1 < total) {
         bool moved = false;
-        if (i2 < i1 && is_there(h_ready(i2 & 1), (i2 >> 1) & 1) &&
-            (MODE == kDw || c2 > 0 || is_there(out_free(o2), po))) {
-          fence_after();
-          const bool last = c2 == nch - 1;
-          second_product(i2, hb, x2, s2, o2, MODE == kDw ? i2 > 0 : c2 > 0, last);
-          ++i2;
-          if (++hb == p.nh) hb = 0;
-          if (++s2 == p.nst) s2 = 0;
-          c2 = last ? 0 : c2 + 1;
-          if (last) {
-            if (++x2 == p.nx) x2 = 0;
-            if (++o2 == p.no) o2 = 0, po ^= 1;
+        // (after a failed wait a stage's last phase may still be open: nothing more is started)
+        if (j < uses && !*failed && is_there(empty(sj), pe) && !*failed) {
+          if (elect_one()) {
+            mbar_expect(full(sj), p.stage_bytes);
+            bulk_load(sbase + sj * p.stage_bytes,
+                      p.img + (size_t)(chunk0 + cj) * p.stage_bytes, p.stage_bytes, full(sj));
           }
+          __syncwarp();
+          ++j;
+          if (++cj == nch) cj = 0;
+          if (++sj == p.nst) sj = 0, pe ^= 1;
           moved = true;
         }
-        if (i1 < total && i1 < i2 + p.ngu && (c1 > 0 || is_there(x_ready(x1), px)) &&
+        if (is_there(gu_free(gu), pg) && (c1 > 0 || is_there(x_ready(x1), px)) &&
             (!fresh || is_there(full(s1), pw))) {
           fence_after();
-          first_product(gu, gb, x1, s1);
+          if (elect_one()) {
+            const uint32_t d = tmem + gu * kGu;
+            const uint32_t a = x_k + x1 * xs, b = w_k + s1 * ss;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k < kx)
+                mma(d, a + (k >> 2) * kBlk + (k & 3) * 2, b + (k >> 2) * kWBlk + (k & 3) * 2,
+                    id_gu, k > 0);
+            if (MODE != kFwd) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (k < ko)
+                  mma(d + WR, a + y_off + (k >> 2) * kBlk + (k & 3) * 2, b + down_off + k * 128,
+                      id_dh, k > 0);
+            }
+            commit(gu_full(gb));
+            if (MODE != kDw && c1 == nch - 1) commit(x_free(x1));
+          }
+          __syncwarp();
           ++i1;
+          if (++gu == p.ngu) gu = 0, pg ^= 1;
           if (++gb == gu_bars) gb = 0;
-          if (++gu == p.ngu) gu = 0;
           if (++s1 == p.nst) s1 = 0, pw ^= 1, fresh = ring;
           if (++c1 == nch) {
             c1 = 0;
@@ -504,24 +479,102 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
           atomicOr(status, 1u);
         }
       }
-    }
-  } else if (warp == 2 * kGroupWarps + 1) {
-    // ------------------------------------------------------------------------- weight loads
-    if (lane == 0 && nt > 0) {
-      const int uses = ring ? total : nch;
-      int j = 0;
-      for (; j < uses; ++j) {
-        const int s = j % p.nst;
-        if (j >= p.nst) mbar_wait(empty(s), (j / p.nst - 1) & 1, failed, status);
-        // (after a failed wait the stage's last phase may still be open: nothing more is started)
-        if (*failed) break;
-        mbar_expect(full(s), p.stage_bytes);
-        bulk_load(sbase + s * p.stage_bytes,
-                  p.img + (size_t)(chunk0 + j % nch) * p.stage_bytes, p.stage_bytes, full(s));
-      }
       // no copy may be in flight when the CTA ends, after a failed wait either
       for (int k = max(0, j - p.nst); k < j; ++k) mbar_drain(full(k % p.nst), (k / p.nst) & 1);
+      if (elect_one()) commit(all_done);
+      __syncwarp();
     }
+  } else if (warp == 2 * kGroupWarps + 1) {
+    // ------------------------------------------------------------------------- second products
+    if (nt > 0) {
+      const uint32_t id_out = MODE == kFwd  ? idesc(BF, p.op, false, false)
+                              : MODE == kDx ? idesc(BF, p.dp, false, true)
+                                            : idesc(BF, p.dp, true, true);
+      const uint32_t id_wy = idesc(BF, p.op, true, true);
+      const uint32_t h_k = desc_lo(sbase + h_off, 16), w_k = desc_lo(sbase, 16);
+      const uint32_t x_k = desc_lo(sbase + x_off, 16);
+      // chunk, hidden operand, rows, weights, output and its parity
+      int c2 = 0, hb = 0, x2 = 0, s2 = 0, o2 = 0;
+      uint32_t po = 1;  // (the first round of outputs has nobody to wait for)
+      for (int i = 0; i < total; ++i) {
+        const bool last = c2 == nch - 1;
+        mbar_wait(h_ready(i & 1), (i >> 1) & 1, failed, status);
+        if (MODE != kDw && c2 == 0) mbar_wait(out_free(o2), po, failed, status);
+        fence_after();
+        __syncwarp();
+        if (elect_one()) {
+          const uint32_t h = h_k + hb * (kHBytes >> 4), w = w_k + s2 * ss;
+          const bool add = MODE == kDw ? i > 0 : c2 > 0;
+          if (MODE == kFwd) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma(acc + o2 * acc_step, h + k * 2, w + down_off + k * 2, id_out, add || k > 0);
+          } else if (MODE == kDx) {
+#pragma unroll
+            for (int k = 0; k < WR / 16; ++k)
+              mma(acc + o2 * acc_step, h + (k >> 2) * kBlk + (k & 3) * 2,
+                  w - kK + kWMn + k * 128, id_out, add || k > 0);
+          } else {
+            const uint32_t hm = h - kK + kMn, x = x_k - kK + kMn + x2 * xs;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mma(acc, hm + k * 128, x + k * 128, id_out, add || k > 0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma(acc + acc_step, hm + (GATED ? kBlk : 0) + k * 128, x + y_off + k * 128, id_wy,
+                  add || k > 0);
+          }
+          commit(done(i & 1));
+          if (MODE == kDw) commit(x_free(x2));
+          if (MODE != kDw && last) commit(out_full(o2));
+          if (ring) commit(empty(s2));
+          if (i == total - 1) commit(all_done);
+        }
+        __syncwarp();
+        if (++hb == p.nh) hb = 0;
+        if (++s2 == p.nst) s2 = 0;
+        c2 = last ? 0 : c2 + 1;
+        if (last) {
+          if (++x2 == p.nx) x2 = 0;
+          if (++o2 == p.no) o2 = 0, po ^= 1;
+        }
+      }
+    }
+  } else if (warp >= 2 * kGroupWarps + 2) {
+    // ------------------------------------------------------------------------- row tiles
+    // x_ready counts an arrival of each loader warp, and the bytes of what comes by TMA
+    const int tid = threadIdx.x - (2 * kGroupThreads + 64);
+    const bool y_too = MODE != kFwd;
+    const uint32_t tma_bytes =
+        ((p.x.tiled ? nbx : 0) + (y_too && p.dy.tiled ? nby : 0)) * 16384;
+    int xb = 0, taken = 0;
+    uint32_t pf = 1;  // (the first round is free)
+    for (int n = 0; n < nt; ++n) {
+      mbar_wait(x_free(xb), pf, failed, status);
+      if (*failed) break;  // (the last round's phase may still be open)
+      const long long r0 = ((long long)me + (long long)n * ctas) * kTile;
+      uint8_t* Xs = smem + x_off + xb * xbytes;
+      uint8_t* Ys = Xs + nbx * 16384;
+      __syncwarp();
+      if (tid == 0 && tma_bytes) {
+        mbar_expect_more(x_ready(xb), tma_bytes);
+        if (p.x.tiled)
+          for (int b = 0; b < nbx; ++b)
+            tile_load(smem_addr(Xs) + b * 16384, &x_map, b * 64, (int)r0, x_ready(xb));
+        if (y_too && p.dy.tiled)
+          for (int b = 0; b < nby; ++b)
+            tile_load(smem_addr(Ys) + b * 16384, &dy_map, b * 64, (int)r0, x_ready(xb));
+      }
+      if (!p.x.tiled)
+        for (int b = 0; b < nbx; ++b) gather_rows(p.x, b, r0, p.f.M, tid, Xs);
+      if (y_too && !p.dy.tiled)
+        for (int b = 0; b < nby; ++b) gather_rows(p.dy, b, r0, p.f.M, tid, Ys);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x_ready(xb));
+      if (++xb == p.nx) xb = 0, pf ^= 1;
+      ++taken;
+    }
+    for (int n = max(0, taken - p.nx); n < taken; ++n) mbar_drain(x_ready(n % p.nx), (n / p.nx) & 1);
   } else if (nt > 0) {
     // ------------------------------------------------------------------------- row groups
     const int g = warp / kGroupWarps, tid = threadIdx.x & (kGroupThreads - 1);
@@ -541,45 +594,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
       asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "n"(kGroupThreads) : "memory");
     };
     auto first_row = [&](int n) { return ((long long)me + (long long)n * ctas) * kTile; };
-    // tile n into its buffer, which is free; the tile behind the next on its way to L2
-    auto load = [&](int n) {
-      const long long r0 = first_row(n);
-      uint8_t* Xs = smem + x_off + (n % p.nx) * xbytes;
-      uint8_t* Ys = Xs + nbx * 16384;
-      if (n + 2 < nt) {
-        const long long r = first_row(n + 2) + (tid & (kTile - 1));
-        if (tid < kTile)
-          prefetch_row(p.x, r, p.f.M);
-        else if (MODE != kFwd)
-          prefetch_row(p.dy, r, p.f.M);
-      }
-      uint4 bx[4], by[4];
-      if (p.x.aligned) fetch_rows(p.x, 0, r0, p.f.M, tid, bx);
-      if (MODE != kFwd && p.dy.aligned) fetch_rows(p.dy, 0, r0, p.f.M, tid, by);
-      auto rest = [&](const RowSrc& src, int blocks, uint4 (&v)[4], uint8_t* dst) {
-        if (src.aligned) {
-          store_rows(0, tid, v, dst);
-          if (blocks > 1) {
-            fetch_rows(src, 1, r0, p.f.M, tid, v);
-            store_rows(1, tid, v, dst);
-          }
-        } else {
-          for (int b = 0; b < blocks; ++b) gather_rows(src, b, r0, p.f.M, tid, dst);
-        }
-      };
-      rest(p.x, nbx, bx, Xs);
-      if (MODE != kFwd) rest(p.dy, nby, by, Ys);
-      arrive(x_ready(n % p.nx));
-    };
-    // Output of tile n through shared memory to the row array. With a place of its own it is taken
-    // by the group of the next tile's first item; else by that of the tile's last item, through the
-    // place of that item's hidden operand (whose product is done when the output is complete).
+    // Output of tile n through shared memory to the row array. With a place of their own the groups
+    // take them in turn, after their first item of the next tile; else the group of the tile's last
+    // item takes it, through the place of that item's hidden operand (whose product is done when the
+    // output is complete).
     auto output = [&](int n, int i) {
       const int cols = MODE == kFwd ? p.f.O : p.f.D;
       const uint32_t src = acc + (n % p.no) * acc_step + row_lanes + half * 32;
       // (the phase before is over: this group has seen the end of an item behind tile n - no)
       if (p.staged) {
-        if (i == total && total >= 2) wait(done(total & 1), (total - 2) >> 1);
+        if (i == total && total >= 2) {  // (the group's last item)
+          const int e = (total - 1 - g) / 2 * 2 + g;
+          wait(done(e & 1), e >> 1);
+        }
         wait(out_full(n % p.no), n / p.no);
       } else {
         wait(done(i & 1), i >> 1);
@@ -606,7 +633,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
                 make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-        if ((b + 1) * 64 >= cols) arrive(out_free(n % p.no));
+        if ((b + 1) * 64 >= cols) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(out_free(n % p.no));
+        }
         group_sync();
         write_rows(S, (uint8_t*)(MODE == kFwd ? p.f.y : p.f.dx),
                    2 * (MODE == kFwd ? p.f.ldy : p.f.lddx), p.out_aligned, b * 64, cols,
@@ -635,26 +666,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
       uint32_t h[kUnits / 2], da[kUnits / 2], du[kUnits / 2];
 #pragma unroll
       for (int e = 0; e < kUnits; e += 4) {
-        float a[4], f[4], sl[4], vh[4], va[4], vu[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) a[k] = __uint_as_float(ra[e + k]);
+        auto two = [&](const uint32_t (&r)[kUnits], int k) {
+          return make_float2(__uint_as_float(r[e + 2 * k]), __uint_as_float(r[e + 2 * k + 1]));
+        };
+        const float2 a[2] = {two(ra, 0), two(ra, 1)};
+        float2 f[2], sl[2];
         act4<ACT, MODE != kFwd>(a, f, sl);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float u = GATED ? __uint_as_float(ru[e + k]) : 1.0f;
-          vh[k] = GATED ? f[k] * u : f[k];
-          if (MODE != kFwd) {
-            const float dh = __uint_as_float(rd[e + k]);
-            va[k] = GATED ? dh * u * sl[k] : dh * sl[k];
-            vu[k] = dh * f[k];
+        for (int k = 0; k < 2; ++k) {
+          float2 u = make_float2(1.0f, 1.0f);
+          if (GATED) u = two(ru, k);
+          if (MODE != kDx) {
+            const float2 v = GATED ? mul2(f[k], u) : f[k];
+            h[e / 2 + k] = Two<T>::pack(v.x, v.y);
           }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          h[(e + k) / 2] = Two<T>::pack(vh[k], vh[k + 1]);
           if (MODE != kFwd) {
-            da[(e + k) / 2] = Two<T>::pack(va[k], va[k + 1]);
-            du[(e + k) / 2] = Two<T>::pack(vu[k], vu[k + 1]);
+            const float2 dh = two(rd, k);
+            const float2 va = mul2(GATED ? mul2(dh, u) : dh, sl[k]);
+            da[e / 2 + k] = Two<T>::pack(va.x, va.y);
+            if (GATED) {
+              const float2 vu = mul2(dh, f[k]);
+              du[e / 2 + k] = Two<T>::pack(vu.x, vu.y);
+            }
           }
         }
       }
@@ -675,7 +708,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
       }
     };
 
-    for (int n = g; n < min(p.nx, nt); n += 2) load(n);
     int c = g, n = 0;
     for (int i = g; i < total; i += 2, c += 2) {
       while (c >= nch) c -= nch, ++n;
@@ -684,7 +716,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
       uint8_t* Hs = smem + h_off + (i % p.nh) * kHBytes;
       uint32_t a0[kUnits], u0[kUnits], d0[kUnits], a1[kUnits], u1[kUnits], d1[kUnits];
       get(d, 0, a0, u0, d0);
-      // the hidden operand's place was item i - nh's
+      // the hidden operand's place was item i - nh's (asked before this item is handed over: the
+      // barrier's next phase cannot be complete yet)
       if (i >= p.nh) wait(done((i - p.nh) & 1), (i - p.nh) >> 1);
 #pragma unroll
       for (int q = 0; q < kSteps; q += 2) {
@@ -692,28 +725,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ffn_tc(TcArgs p) {
         get(d, q + 1, a1, u1, d1);
         work(Hs, q, a0, u0, d0);
         landed(a1, u1, d1);
-        if (q + 2 < kSteps) get(d, q + 2, a0, u0, d0);
+        if (q + 2 < kSteps) {
+          get(d, q + 2, a0, u0, d0);
+        } else {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(gu_free(i % p.ngu));
+        }
         work(Hs, q + 1, a1, u1, d1);
       }
-      // Waits for `done` stand where the next phase of the barrier cannot complete before them: for
-      // an earlier item before this one is handed over, for this one before the group's next.
-      if (MODE == kDw) {
-        // the rows of tile i - 1 (three buffers) or i (two) make room for tile i + 2, once their
-        // second product is done
-        if (p.nx == 3 && i > 0) wait(done((i - 1) & 1), (i - 1) >> 1);
-        arrive(h_ready(i & 1));
-        if (i + 2 < nt) {
-          if (p.nx == 2) wait(done(i & 1), i >> 1);
-          if (p.nx == 2 || i + 2 >= p.nx) load(i + 2);
+      arrive(h_ready(i & 1));
+      if (MODE != kDw) {
+        // (every group has one item of the first two of a tile; with one chunk, every other tile)
+        if (!p.staged) {
+          if (c == nch - 1) output(n, i);
+        } else if (c < 2 && n > 0 && (nch == 1 || ((n - 1) & 1) == g)) {
+          output(n - 1, i);
         }
-      } else {
-        arrive(h_ready(i & 1));
-        // the tile's first products are done: its rows make room
-        if (c == nch - 1 && n + p.nx < nt) load(n + p.nx);
-        if (p.staged ? c == 0 && n > 0 : c == nch - 1) output(p.staged ? n - 1 : n, i);
       }
     }
-    if (MODE != kDw && p.staged && g == (total & 1)) output(nt - 1, total);
+    if (MODE != kDw && p.staged && (nch == 1 ? g == (nt & 1) : g == ((nt - 1) & 1)))
+      output(nt - 1, total);
   }
 
   if (MODE == kDw && warp < kGroupWarps) {
@@ -762,16 +794,36 @@ bool aligned16(const void* p, long long ld, int cols) {
   return (((uintptr_t)p | (uintptr_t)(ld * 2) | (uintptr_t)(cols * 2)) & 15) == 0;
 }
 
-RowSrc row_src(const void* p, long long ld, long long rows, int cols) {
+RowSrc row_src(const void* p, long long ld, long long rows, int cols, CUtensorMap* map,
+               CUtensorMapDataType type) {
   RowSrc s = {};
   if (rows <= 0) return s;
   s.base = (const uint8_t*)p;
   s.ld = rows > 1 ? ld * 2 : 0;
   s.cols = cols;
-  s.aligned = aligned16(p, s.ld / 2, cols);
-  s.lo = (const uint8_t*)(((uintptr_t)p + 15) & ~(uintptr_t)15);
+  s.lo = (const uint8_t*)(((uintptr_t)p + 3) & ~(uintptr_t)3);
   s.hi = (const uint8_t*)(((uintptr_t)p + (uintptr_t)((rows - 1) * ld * 2 + cols * 2)) &
-                          ~(uintptr_t)15);
+                          ~(uintptr_t)3);
+  // a tensor map takes 16-byte aligned starts and (positive) distances
+  const long long step = rows > 1 ? ld * 2 : (cols * 2 + 15) & ~15;
+  if (((uintptr_t)p & 15) || (step & 15) || step < cols * 2) return s;
+  static const auto encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (decltype(&cuTensorMapEncodeTiled))f;
+  }();
+  if (!encode) return s;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)step};
+  const cuuint32_t box[2] = {64, kTile}, unit[2] = {1, 1};
+  s.tiled = encode(map, type, 2, const_cast<void*>(p), dims, strides, box, unit,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   return s;
 }
 
@@ -824,8 +876,11 @@ Fit fit_of(int mode, bool gated, int dp, int op, int stage, int nch) {
 template <int MODE, typename T, int ACT, bool GATED>
 int launch(TcArgs p, cudaStream_t st) {
   const bool one = p.f.M <= 1;  // a single row's stride is never used
-  p.x = row_src(p.f.x, p.f.ldx, p.f.M, p.f.D);
-  if (MODE != kFwd) p.dy = row_src(p.f.dy, p.f.lddy, p.f.M, p.f.O);
+  CUtensorMap x_map = {}, dy_map = {};
+  const auto type =
+      Two<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  p.x = row_src(p.f.x, p.f.ldx, p.f.M, p.f.D, &x_map, type);
+  if (MODE != kFwd) p.dy = row_src(p.f.dy, p.f.lddy, p.f.M, p.f.O, &dy_map, type);
   if (MODE == kFwd) p.out_aligned = aligned16(p.f.y, one ? 0 : p.f.ldy, p.f.O);
   if (MODE == kDx) p.out_aligned = aligned16(p.f.dx, one ? 0 : p.f.lddx, p.f.D);
   const int nch = MODE == kDw ? 1 : p.nch;
@@ -843,7 +898,7 @@ int launch(TcArgs p, cudaStream_t st) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, fit.smem) !=
       cudaSuccess)
     return SPLAT_ERR_CUDA;
-  kernel<<<(unsigned)grid, kTcThreads, fit.smem, st>>>(p);
+  kernel<<<(unsigned)grid, kTcThreads, fit.smem, st>>>(p, x_map, dy_map);
   return cudaGetLastError() == cudaSuccess ? SPLAT_OK : SPLAT_ERR_CUDA;
 }
 
