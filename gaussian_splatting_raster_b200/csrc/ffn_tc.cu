@@ -53,6 +53,7 @@ struct RowSrc {
   const uint8_t *base, *lo, *hi;  // lo, hi: 4-byte aligned, inside the array
   long long ld;                   // bytes
   int cols, tiled;                // tiled: read through the tensor map
+  int raw;                        // else bytes of a tile as it lies in memory, 0: not staged
 };
 
 struct TcArgs {
@@ -62,6 +63,7 @@ struct TcArgs {
   int nst, nx, nh;      // weight stages, row tiles and hidden operands in shared memory
   int ngu, no;          // accumulators of first products and of outputs in TMEM
   int staged;           // outputs have places of their own in shared memory
+  int raw_off;          // where tiles lie as in memory (x, then dy)
   int dp, op;           // D and O rounded up to 16
   RowSrc x, dy;
   int out_aligned;      // y's or dx's rows start and end at 16 bytes
@@ -233,18 +235,24 @@ k_pack(TcArgs p, uint8_t* __restrict__ img) {
 
 // Row tiles come by TMA where the rows allow it (start and distance multiples of 16 bytes): one
 // instruction a 64-column block, zeros behind the last row and column. Any other rows (odd widths
-// start anywhere) are taken by the loader warps, eight threads to a row: thread t has piece t & 7
-// (8 elements) of the block in rows t / 8 + 8 j, read as the five words around it and shifted by
-// half a word where the row starts on an odd element. Rows >= M are zeros, and so are elements
-// behind a row's end up to the block's.
-__device__ __forceinline__ void gather_rows(const RowSrc& s, int block, long long r0, long long M,
-                                            int tid, uint8_t* dst) {
-  const int c = block * 8 + (tid & 7);
-  const long long r = r0 + (tid >> 3);
-  const uint8_t* p = s.base + r * s.ld + c * 16;
+// start anywhere) come as they lie in memory, gaps between rows included, by one bulk copy into
+// shared memory, from where the loader warps put them into place; where there is no room for that,
+// and at the array's ends where a copy's 16 bytes would reach over them, the loader warps read the
+// rows from global memory.
+//
+// Eight threads to a row: thread t has piece t & 7 (8 elements) of the block in rows t / 8 + 8 j,
+// read as the five words around it and shifted by half a word where the row starts on an odd
+// element. Rows >= M are zeros, and so are elements behind a row's end up to the block's. `tile` is
+// the tile's first row, in shared (RAW) or global memory.
+template <bool RAW>
+__device__ __forceinline__ void place_rows(const RowSrc& s, const uint8_t* tile, int block,
+                                           long long rows, int tid, uint8_t* dst) {
+  const int c = block * 8 + (tid & 7), r = tid >> 3;
+  const uint8_t* p = tile + r * s.ld + c * 16;
   const int n = min(8, s.cols - c * 8);  // elements wanted
-  uint8_t* q = dst + block * 16384 + (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4);
+  uint8_t* q = dst + block * 16384 + r * 128 + (((tid & 7) ^ (r & 7)) << 4);
   constexpr int U = 4;
+#pragma unroll 1
   for (int j0 = 0; j0 < kTile / 8; j0 += U, p += 8 * U * s.ld, q += U * 1024) {
     uint32_t w[U][5];
     uint32_t sh[U];
@@ -253,14 +261,15 @@ __device__ __forceinline__ void gather_rows(const RowSrc& s, int block, long lon
       const uint8_t* e = p + 8 * j * s.ld;
       const uint8_t* a = (const uint8_t*)((uintptr_t)e & ~(uintptr_t)3);
       sh[j] = ((uint32_t)(uintptr_t)e & 2u) * 8u;
-      const int words = n > 0 && r + 8 * (j0 + j) < M ? (2 * n + (int)(sh[j] >> 3) + 3) >> 2 : 0;
-      const bool whole = a >= s.lo && a + 4 * words <= s.hi;
+      const int words = n > 0 && r + 8 * (j0 + j) < rows ? (2 * n + (int)(sh[j] >> 3) + 3) >> 2 : 0;
+      const bool whole = RAW || (a >= s.lo && a + 4 * words <= s.hi);
 #pragma unroll
       for (int k = 0; k < 5; ++k) {
         w[j][k] = 0u;
         if (k < words) {
           if (whole) {
-            w[j][k] = __ldg(reinterpret_cast<const uint32_t*>(a) + k);
+            w[j][k] = RAW ? reinterpret_cast<const uint32_t*>(a)[k]
+                          : __ldg(reinterpret_cast<const uint32_t*>(a) + k);
           } else {  // at the array's ends: element by element
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -283,6 +292,18 @@ __device__ __forceinline__ void gather_rows(const RowSrc& s, int block, long lon
       *reinterpret_cast<uint4*>(q + j * 1024) = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
+}
+
+// The bulk copy of the tile at row r0: start and bytes, 0 when it would reach over the array's ends.
+__device__ __forceinline__ uint32_t raw_span(const RowSrc& s, long long r0, long long M,
+                                             const uint8_t*& start) {
+  const uint8_t* p = s.base + r0 * s.ld;
+  start = (const uint8_t*)((uintptr_t)p & ~(uintptr_t)15);
+  const long long rows = min((long long)kTile, M - r0);
+  const long long last = (long long)(p - start) + (rows - 1) * s.ld + s.cols * 2;
+  const long long bytes = (last + 15) & ~15LL;
+  if (start < s.lo || start + bytes > s.hi) return 0;
+  return (uint32_t)bytes;
 }
 
 // One 64-column block of results (columns col0 ..) from shared memory to a row array: aligned rows
@@ -334,7 +355,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x_map,
          const __grid_constant__ CUtensorMap dy_map) {
   extern __shared__ uint8_t raw[];
-  constexpr int kBars = 2 * kMaxStages + 2 * kMaxGu + 2 * kMaxRows + 2 + 2 + 2 + 2 + 1;
+  constexpr int kBars = 2 * kMaxStages + 2 * kMaxGu + 2 * kMaxRows + 2 + 2 + 2 + 2 + 2;
   __shared__ __align__(8) uint64_t s_bar[kBars];
   __shared__ uint32_t s_tmem;
   __shared__ int s_failed;
@@ -362,7 +383,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
   auto done = [&](int k) { return bars + 8 * (kB1 + 2 + k); };    // item's second product, by parity
   auto out_full = [&](int k) { return bars + 8 * (kB1 + 4 + k); };  // a tile's output is complete
   auto out_free = [&](int k) { return bars + 8 * (kB1 + 6 + k); };  // ... has been read
-  const uint32_t all_done = bars + 8 * (kB1 + 8);
+  const uint32_t all_done = bars + 8 * (kB1 + 8), raw_full = bars + 8 * (kB1 + 9);
   volatile int* failed = &s_failed;
   unsigned int* status = &g_rows_status;
 
@@ -546,12 +567,26 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
     const bool y_too = MODE != kFwd;
     const uint32_t tma_bytes =
         ((p.x.tiled ? nbx : 0) + (y_too && p.dy.tiled ? nby : 0)) * 16384;
+    const uint32_t raw = sbase + p.raw_off;
+    // tile n's bulk copies on their way (both arrays' bytes on one barrier)
+    auto fetch = [&](int n) {
+      const long long r0 = ((long long)me + (long long)n * ctas) * kTile;
+      const uint8_t *xa, *ya;
+      const uint32_t xn = p.x.raw ? raw_span(p.x, r0, p.f.M, xa) : 0;
+      const uint32_t yn = y_too && p.dy.raw ? raw_span(p.dy, r0, p.f.M, ya) : 0;
+      mbar_expect(raw_full, xn + yn);
+      if (xn) bulk_load(raw, xa, xn, raw_full);
+      if (yn) bulk_load(raw + p.x.raw, ya, yn, raw_full);
+    };
+    const bool staged = p.x.raw || (y_too && p.dy.raw);
     int xb = 0, taken = 0;
     uint32_t pf = 1;  // (the first round is free)
+    if (staged && tid == 0) fetch(0);
     for (int n = 0; n < nt; ++n) {
       mbar_wait(x_free(xb), pf, failed, status);
       if (*failed) break;  // (the last round's phase may still be open)
       const long long r0 = ((long long)me + (long long)n * ctas) * kTile;
+      const long long rows = p.f.M - r0;
       uint8_t* Xs = smem + x_off + xb * xbytes;
       uint8_t* Ys = Xs + nbx * 16384;
       __syncwarp();
@@ -564,17 +599,32 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
           for (int b = 0; b < nby; ++b)
             tile_load(smem_addr(Ys) + b * 16384, &dy_map, b * 64, (int)r0, x_ready(xb));
       }
-      if (!p.x.tiled)
-        for (int b = 0; b < nbx; ++b) gather_rows(p.x, b, r0, p.f.M, tid, Xs);
-      if (y_too && !p.dy.tiled)
-        for (int b = 0; b < nby; ++b) gather_rows(p.dy, b, r0, p.f.M, tid, Ys);
+      if (staged) mbar_drain(raw_full, n & 1);
+      auto take = [&](const RowSrc& src, int blocks, const uint8_t* at, uint8_t* dst) {
+        const uint8_t* start;
+        if (src.raw && raw_span(src, r0, p.f.M, start)) {
+          at += src.base + r0 * src.ld - start;
+          for (int b = 0; b < blocks; ++b) place_rows<true>(src, at, b, rows, tid, dst);
+        } else {
+          for (int b = 0; b < blocks; ++b)
+            place_rows<false>(src, src.base + r0 * src.ld, b, rows, tid, dst);
+        }
+      };
+      if (!p.x.tiled) take(p.x, nbx, smem + p.raw_off, Xs);
+      if (y_too && !p.dy.tiled) take(p.dy, nby, smem + p.raw_off + p.x.raw, Ys);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(x_ready(xb));
+      if (staged && n + 1 < nt) {  // (the staged tile has been read by both warps)
+        asm volatile("bar.sync 3, %0;" ::"n"(kLoaders) : "memory");
+        if (tid == 0) fetch(n + 1);
+      }
       if (++xb == p.nx) xb = 0, pf ^= 1;
       ++taken;
     }
+    // no copy may be in flight when the CTA ends, after a failed wait either
     for (int n = max(0, taken - p.nx); n < taken; ++n) mbar_drain(x_ready(n % p.nx), (n / p.nx) & 1);
+    if (staged) mbar_drain(raw_full, min(taken, nt - 1) & 1);
   } else if (nt > 0) {
     // ------------------------------------------------------------------------- row groups
     const int g = warp / kGroupWarps, tid = threadIdx.x & (kGroupThreads - 1);
@@ -794,6 +844,12 @@ bool aligned16(const void* p, long long ld, int cols) {
   return (((uintptr_t)p | (uintptr_t)(ld * 2) | (uintptr_t)(cols * 2)) & 15) == 0;
 }
 
+// shared memory for a tile as it lies in memory; 0 when the gaps are most of it
+int tile_bytes(long long step, int cols) {
+  const long long b = (step * (kTile - 1) + cols * 2 + 31) & ~15LL;
+  return b <= 2LL * kTile * (cols * 2 + 16) ? (int)((b + 127) & ~127LL) : 0;
+}
+
 RowSrc row_src(const void* p, long long ld, long long rows, int cols, CUtensorMap* map,
                CUtensorMapDataType type) {
   RowSrc s = {};
@@ -806,6 +862,7 @@ RowSrc row_src(const void* p, long long ld, long long rows, int cols, CUtensorMa
                           ~(uintptr_t)3);
   // a tensor map takes 16-byte aligned starts and (positive) distances
   const long long step = rows > 1 ? ld * 2 : (cols * 2 + 15) & ~15;
+  s.raw = tile_bytes(step, cols);
   if (((uintptr_t)p & 15) || (step & 15) || step < cols * 2) return s;
   static const auto encode = [] {
     void* f = nullptr;
@@ -838,10 +895,10 @@ int stage_bytes(int D, int O, bool gated) {
 // with the rest more weight stages. Weights mode wants three row tiles, so that a tile's loads wait
 // for nothing but the other group's products.
 struct Fit {
-  int nst, nx, nh, staged, ngu, no, smem;
+  int nst, nx, nh, staged, ngu, no, raw_off, smem;
 };
 
-Fit fit_of(int mode, bool gated, int dp, int op, int stage, int nch) {
+Fit fit_of(int mode, bool gated, int dp, int op, int stage, int nch, int raw) {
   static const int kOut[][3] = {{2, 2, 1}, {2, 2, 0}, {1, 2, 1}, {1, 2, 0}};  // nx, nh, staged
   static const int kSum[][3] = {{3, 2, 0}, {2, 2, 0}, {2, 1, 0}, {0, 0, 0}};
   Fit f = {};
@@ -860,13 +917,14 @@ Fit fit_of(int mode, bool gated, int dp, int op, int stage, int nch) {
     const int* o = mode == kDw ? kSum[k] : kOut[k];
     if (o[0] == 0) break;
     const int used = o[0] * rows_bytes(mode, dp, op) + o[1] * hidden_bytes(mode, gated) +
-                     o[2] * 2 * 16384;  // (a place for each group)
+                     o[2] * 2 * 16384 + raw;  // (outputs: a place for each group)
     const int nst = std::min({(kSmemLimit - used) / stage, nch, kMaxStages});
     if (used > kSmemLimit || nst < std::min(nch, 2)) continue;
     f.nx = o[0];
     f.nh = o[1];
     f.staged = o[2];
     f.nst = nst;
+    f.raw_off = nst * stage + used - raw;
     f.smem = nst * stage + used + 1024;
     return f;
   }
@@ -884,8 +942,15 @@ int launch(TcArgs p, cudaStream_t st) {
   if (MODE == kFwd) p.out_aligned = aligned16(p.f.y, one ? 0 : p.f.ldy, p.f.O);
   if (MODE == kDx) p.out_aligned = aligned16(p.f.dx, one ? 0 : p.f.lddx, p.f.D);
   const int nch = MODE == kDw ? 1 : p.nch;
-  const Fit fit = fit_of(MODE, GATED, p.dp, p.op, p.stage_bytes, nch);
+  if (p.x.tiled) p.x.raw = 0;
+  if (p.dy.tiled) p.dy.raw = 0;
+  Fit fit = fit_of(MODE, GATED, p.dp, p.op, p.stage_bytes, nch, p.x.raw + p.dy.raw);
+  if (!fit.nst) {
+    p.x.raw = p.dy.raw = 0;
+    fit = fit_of(MODE, GATED, p.dp, p.op, p.stage_bytes, nch, 0);
+  }
   if (!fit.nst) return SPLAT_ERR_CAPACITY;
+  p.raw_off = fit.raw_off;
   p.nst = fit.nst;
   p.nx = fit.nx;
   p.nh = fit.nh;
@@ -916,7 +981,7 @@ int run(const FfnArgs& f, bool backward, uint8_t* img, cudaStream_t st) {
   k_pack<T, GATED><<<(pieces + 255) / 256, 256, 0, st>>>(p, img);
   int rc = SPLAT_OK;
   if (!backward) return launch<kFwd, T, ACT, GATED>(p, st);
-  if (f.dx) rc = launch<kDx, T, ACT, GATED>(p, st);
+  if (f.dx && f.M > 0) rc = launch<kDx, T, ACT, GATED>(p, st);
   if (rc == SPLAT_OK && (f.dwg || f.dwu || f.dwd)) rc = launch<kDw, T, ACT, GATED>(p, st);
   return rc;
 }
@@ -939,7 +1004,7 @@ size_t ffn_tc_image_bytes(int D, int F, int O, bool gated) {
 int ffn_tc_splits(long long M, int F) {
   const int chunks = (F + kChunk - 1) / kChunk;
   const long long tiles = (M + kTile - 1) / kTile, s = 148 / chunks;
-  return (int)(s < tiles ? (s < 1 ? 1 : s) : tiles);
+  return (int)std::max(1LL, std::min(s, tiles));
 }
 
 int ffn_tc_run(const FfnArgs& f, int dtype, int act, bool backward, void* img, cudaStream_t st) {

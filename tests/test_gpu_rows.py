@@ -326,10 +326,11 @@ def test_ffn_far_arguments(P, act, dt):
         R.close(dx, ref["dx"], "dx")
 
 
-def test_ffn_empty(P):
-    w = torch.ones(5, 3, device="cuda")
-    wd = torch.ones(2, 5, device="cuda")
-    x, y = torch.empty(0, 3, device="cuda"), torch.empty(0, 2, device="cuda")
+@pytest.mark.parametrize("dt", DTYPES, ids=str)
+def test_ffn_empty(P, dt):
+    w = torch.ones(5, 3, device="cuda", dtype=dt)
+    wd = torch.ones(2, 5, device="cuda", dtype=dt)
+    x, y = torch.empty(0, 3, device="cuda", dtype=dt), torch.empty(0, 2, device="cuda", dtype=dt)
     P.ffn(x, w, w, wd, y)
     g = [torch.full_like(w, 9), torch.full_like(w, 9), torch.full_like(wd, 9)]
     P.ffn_backward(y, x, w, w, wd, torch.empty_like(x), *g)
@@ -352,6 +353,44 @@ def test_ffn_broadcast_row(P, dt):
     P.ffn_backward(dy.cuda(), x[:1].cuda().expand(300, 24), *w, dx=dx, dw_up=dw)
     R.close(dx, ref["dx"])
     R.close(dw, ref["dw_up"])
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=str)
+@pytest.mark.parametrize("shift", [1, 3, 8])
+def test_ffn_rows_anywhere(P, dt, shift):
+    """Arrays that start at an odd element, at the first and last elements of their allocation, with
+    wide gaps between rows, and with rows that overlap one another (inputs)."""
+    M, D, F, O = 700, 29, 66, 31
+    x, wg, wu, wd, dy = _ffn_inputs(M, D, F, O, True, dt, 17)
+    w = [_cuda(t) for t in (wg, wu, wd)]
+    ref = R.ffn_ref(x, wg, wu, wd, "silu", dy)
+
+    def strided(t, ld):
+        flat = torch.full((shift + (M - 1) * ld + t.shape[1],), float("nan"), dtype=dt).cuda()
+        v = flat[shift:].as_strided((M, t.shape[1]), (ld, 1), shift)
+        v.copy_(t)
+        return v
+
+    for ldx, ldy in ((D, O), (D + 1, O + 3), (8 * D, 8 * O), (300, 301)):
+        xv, dyv = strided(x, ldx), strided(dy, ldy)
+        y = torch.empty(M, O, dtype=dt, device="cuda")
+        P.ffn(xv, *w, y)
+        R.close(y, ref["y"], "y")
+        dx, dw = torch.empty(M, D, dtype=dt, device="cuda"), torch.empty_like(w[2])
+        P.ffn_backward(dyv, xv, *w, dx=dx, dw_down=dw)
+        R.close(dx, ref["dx"], "dx")
+        R.close(dw, ref["dw_down"], "dw_down")
+    g = _gen(3)
+    flat = torch.randn(shift + (M - 1) * 5 + D, generator=g).to(dt)
+    xo = flat.as_strided((M, D), (5, 1), shift)
+    ref = R.ffn_ref(xo, wg, wu, wd, "gelu", dy)
+    xv = flat.cuda().as_strided((M, D), (5, 1), shift)
+    y = torch.empty(M, O, dtype=dt, device="cuda")
+    P.ffn(xv, *w, y, act="gelu")
+    R.close(y, ref["y"], "y")
+    dw = torch.empty_like(w[0])
+    P.ffn_backward(dy.cuda(), xv, *w, dw_gate=dw, act="gelu")
+    R.close(dw, ref["dw_gate"], "dw_gate")
 
 
 # -- streams, graphs, refusals --------------------------------------------------------------------
