@@ -427,80 +427,77 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
   constexpr uint32_t kMn = (16384 >> 4) << 16, kWMn = (WR * 128 >> 4) << 16, kK = 1u << 16;
   const uint32_t xs = xbytes >> 4, ss = p.stage_bytes >> 4;
   const uint32_t y_off = nbx * kBlk, down_off = nbx * kWBlk;
-  // (whole warps ask the barriers, one lane issues)
-  auto is_there = [&](uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_test(bar, parity)) || *failed;
-  };
   if (warp == 2 * kGroupWarps) {
     // ------------------------------------------------------------- first products, weight loads
     if (nt > 0) {
       const int kx = p.dp >> 4, ko = p.op >> 4;
       const uint32_t id_gu = idesc(BF, WR, false, false), id_dh = idesc(BF, 64, false, true);
       const uint32_t x_k = desc_lo(sbase + x_off, 16), w_k = desc_lo(sbase, 16);
-      // next product: item, chunk, accumulator (and its barrier), rows, weights
-      int i1 = 0, c1 = 0, gu = 0, gb = 0, x1 = 0, s1 = 0;
+      // (this loop is the longest chain of an item: about 100 instructions, a fifth of an SM's
+      // issue slots away; as a loop that asked its barriers in turn it took 1,000 cycles an item)
+      // product: chunk, accumulator (and its barrier), rows, weights
+      int c1 = 0, gu = 0, gb = 0, x1 = 0, s1 = 0;
       uint32_t pg = 1, px = 0, pw = 0;  // (the first round of accumulators is free)
-      bool fresh = true;  // the stage's weights are to be waited for
-      // next chunk's weights: number, chunk, stage
+      // the next chunk's weights: number, chunk, stage
       const int uses = ring ? total : nch;
       int j = 0, cj = 0, sj = 0;
       uint32_t pe = 1;
-      long long since = clock64();
-      while (i1 < total) {
-        bool moved = false;
+      auto load_weights = [&]() {
         // (after a failed wait a stage's last phase may still be open: nothing more is started)
-        if (j < uses && !*failed && is_there(empty(sj), pe) && !*failed) {
+        if (!*failed) {
           if (elect_one()) {
             mbar_expect(full(sj), p.stage_bytes);
             bulk_load(sbase + sj * p.stage_bytes,
                       p.img + (size_t)(chunk0 + cj) * p.stage_bytes, p.stage_bytes, full(sj));
           }
           __syncwarp();
-          ++j;
-          if (++cj == nch) cj = 0;
-          if (++sj == p.nst) sj = 0, pe ^= 1;
-          moved = true;
         }
-        if (is_there(gu_free(gu), pg) && (c1 > 0 || is_there(x_ready(x1), px)) &&
-            (!fresh || is_there(full(s1), pw))) {
-          fence_after();
-          if (elect_one()) {
-            const uint32_t d = tmem + gu * kGu;
-            const uint32_t a = x_k + x1 * xs, b = w_k + s1 * ss;
+        ++j;
+        if (++cj == nch) cj = 0;
+        if (++sj == p.nst) sj = 0, pe ^= 1;
+      };
+      while (j < p.nst) load_weights();
+      for (int i = 0; i < total; ++i) {
+        if (ring && j < uses) {
+          // the stage used longest ago, when its product is done; this item's weights for certain
+          const bool must = j <= i;
+          if (must) mbar_wait(empty(sj), pe, failed, status);
+          if (must || __all_sync(0xffffffffu, mbar_test(empty(sj), pe))) load_weights();
+        }
+        if (ring || i < nch) mbar_wait(full(s1), pw, failed, status);
+        if (c1 == 0) mbar_wait(x_ready(x1), px, failed, status);
+        mbar_wait(gu_free(gu), pg, failed, status);
+        fence_after();
+        __syncwarp();
+        if (elect_one()) {
+          const uint32_t d = tmem + gu * kGu;
+          const uint32_t a = x_k + x1 * xs, b = w_k + s1 * ss;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < kx)
+              mma(d, a + (k >> 2) * kBlk + (k & 3) * 2, b + (k >> 2) * kWBlk + (k & 3) * 2, id_gu,
+                  k > 0);
+          if (MODE != kFwd) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              if (k < kx)
-                mma(d, a + (k >> 2) * kBlk + (k & 3) * 2, b + (k >> 2) * kWBlk + (k & 3) * 2,
-                    id_gu, k > 0);
-            if (MODE != kFwd) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (k < ko)
-                  mma(d + WR, a + y_off + (k >> 2) * kBlk + (k & 3) * 2, b + down_off + k * 128,
-                      id_dh, k > 0);
-            }
-            commit(gu_full(gb));
-            if (MODE != kDw && c1 == nch - 1) commit(x_free(x1));
+              if (k < ko)
+                mma(d + WR, a + y_off + (k >> 2) * kBlk + (k & 3) * 2, b + down_off + k * 128,
+                    id_dh, k > 0);
           }
-          __syncwarp();
-          ++i1;
-          if (++gu == p.ngu) gu = 0, pg ^= 1;
-          if (++gb == gu_bars) gb = 0;
-          if (++s1 == p.nst) s1 = 0, pw ^= 1, fresh = ring;
-          if (++c1 == nch) {
-            c1 = 0;
-            if (++x1 == p.nx) x1 = 0, px ^= 1;
-          }
-          moved = true;
+          commit(gu_full(gb));
+          if (MODE != kDw && c1 == nch - 1) commit(x_free(x1));
         }
-        if (moved) {
-          since = clock64();
-        } else if (clock64() - since > kWaitClocks) {
-          *failed = 1;
-          atomicOr(status, 1u);
+        __syncwarp();
+        if (++gu == p.ngu) gu = 0, pg ^= 1;
+        if (++gb == gu_bars) gb = 0;
+        if (++s1 == p.nst) s1 = 0, pw ^= 1;
+        if (++c1 == nch) {
+          c1 = 0;
+          if (++x1 == p.nx) x1 = 0, px ^= 1;
         }
       }
-      // no copy may be in flight when the CTA ends, after a failed wait either
+      // no copy may be in flight when the CTA ends, after a failed wait either (the drain of a
+      // stage that was not started runs out, in that case)
       for (int k = max(0, j - p.nst); k < j; ++k) mbar_drain(full(k % p.nst), (k / p.nst) & 1);
       if (elect_one()) commit(all_done);
       __syncwarp();
