@@ -421,15 +421,25 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p) {
     }
 }
 
-// the splits' partial gradients summed in order
+// The splits' partial gradients: a CTA has 32 sums, each of its warps every eighth split of all of
+// them, the warps' sums added in order.
 template <typename T, bool GATED>
 __global__ void __launch_bounds__(kT) k_ffn_join(FfnArgs p) {
+  __shared__ float s_sum[kT / 32][32];
   const size_t FD = (size_t)p.F * p.D, n = (GATED ? 2 : 1) * FD + (size_t)p.O * p.F;
-  const size_t i = (size_t)blockIdx.x * kT + threadIdx.x;
-  if (i >= n) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t i = (size_t)blockIdx.x * 32 + lane;
   float s = 0.0f;
+  if (i < n) {
 #pragma unroll 4
-  for (int k = 0; k < p.splits; ++k) s += p.part[k * n + i];
+    for (int k = warp; k < p.splits; k += kT / 32) s += p.part[k * n + i];
+  }
+  s_sum[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || i >= n) return;
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kT / 32; ++w) s += s_sum[w][lane];
   const size_t down = i - (GATED ? 2 : 1) * FD;  // of dWd^T, when i is past the others
   if (GATED && i < FD) {
     if (p.dwg) ((T*)p.dwg)[i] = from_f<T>(s);
@@ -489,7 +499,7 @@ int run_forward(const FfnArgs& p, cudaStream_t st) {
 
 template <typename T, bool GATED> int run_join(const FfnArgs& p, cudaStream_t st) {
   const size_t n = ((GATED ? 2 : 1) * (size_t)p.D + p.O) * p.F;
-  k_ffn_join<T, GATED><<<(unsigned)((n + kT - 1) / kT), kT, 0, st>>>(p);
+  k_ffn_join<T, GATED><<<(unsigned)((n + 31) / 32), kT, 0, st>>>(p);
   return last_error();
 }
 

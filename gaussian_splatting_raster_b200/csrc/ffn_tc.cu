@@ -242,19 +242,68 @@ k_pack(TcArgs p, uint8_t* __restrict__ img) {
 //
 // Eight threads to a row: thread t has piece t & 7 (8 elements) of the block in rows t / 8 + 8 j,
 // read as the five words around it and shifted by half a word where the row starts on an odd
-// element. Rows >= M are zeros, and so are elements behind a row's end up to the block's. `tile` is
-// the tile's first row, in shared (RAW) or global memory.
-template <bool RAW>
-__device__ __forceinline__ void place_rows(const RowSrc& s, const uint8_t* tile, int block,
+// element. Rows >= M are zeros, and so are elements behind a row's end up to the block's.
+struct Piece {
+  uint32_t w[5];
+};
+
+// words to the piece's place: `keep` has the bits of its elements
+__device__ __forceinline__ void put_piece(uint8_t* q, const Piece& v, uint32_t sh,
+                                          const uint4& keep) {
+  *reinterpret_cast<uint4*>(q) =
+      make_uint4(__funnelshift_r(v.w[0], v.w[1], sh) & keep.x,
+                 __funnelshift_r(v.w[1], v.w[2], sh) & keep.y,
+                 __funnelshift_r(v.w[2], v.w[3], sh) & keep.z,
+                 __funnelshift_r(v.w[3], v.w[4], sh) & keep.w);
+}
+
+__device__ __forceinline__ uint4 keep_bits(int n) {  // of the first n of 8 elements
+  uint32_t m[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    m[k] = n >= 2 * k + 2 ? 0xFFFFFFFFu : n == 2 * k + 1 ? 0xFFFFu : 0u;
+  return make_uint4(m[0], m[1], m[2], m[3]);
+}
+
+// from the staged tile at `at` (whose buffer has room for the words behind its last row)
+__device__ __forceinline__ void place_staged(uint32_t at, int ld, int cols, int block,
+                                             long long rows, int tid, uint8_t* dst) {
+  const int c = block * 8 + (tid & 7), r = tid >> 3;
+  const uint4 keep = keep_bits(cols - c * 8), none = make_uint4(0u, 0u, 0u, 0u);
+  // (pieces behind the row's end read what is there, within the buffer, and keep nothing)
+  uint32_t p = at + r * ld + (c * 8 < cols ? c * 16 : 0);
+  uint8_t* q = dst + block * 16384 + r * 128 + (((tid & 7) ^ (r & 7)) << 4);
+  constexpr int U = 8;
+#pragma unroll
+  for (int j0 = 0; j0 < kTile / 8; j0 += U) {
+    Piece v[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const uint32_t a = (p + j * 8 * ld) & ~3u;
+#pragma unroll
+      for (int k = 0; k < 5; ++k)
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[j].w[k]) : "r"(a + 4 * k));
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      put_piece(q + (j0 + j) * 1024, v[j], ((p + j * 8 * ld) & 2u) * 8u,
+                r + 8 * (j0 + j) < rows ? keep : none);
+    p += 8 * U * ld;
+  }
+}
+
+// from global memory; at the array's ends element by element
+__device__ __forceinline__ void place_rows(const RowSrc& s, long long r0, int block,
                                            long long rows, int tid, uint8_t* dst) {
   const int c = block * 8 + (tid & 7), r = tid >> 3;
-  const uint8_t* p = tile + r * s.ld + c * 16;
   const int n = min(8, s.cols - c * 8);  // elements wanted
+  const uint4 keep = keep_bits(n);
+  const uint8_t* p = s.base + (r0 + r) * s.ld + c * 16;
   uint8_t* q = dst + block * 16384 + r * 128 + (((tid & 7) ^ (r & 7)) << 4);
   constexpr int U = 4;
 #pragma unroll 1
   for (int j0 = 0; j0 < kTile / 8; j0 += U, p += 8 * U * s.ld, q += U * 1024) {
-    uint32_t w[U][5];
+    Piece v[U];
     uint32_t sh[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
@@ -262,35 +311,26 @@ __device__ __forceinline__ void place_rows(const RowSrc& s, const uint8_t* tile,
       const uint8_t* a = (const uint8_t*)((uintptr_t)e & ~(uintptr_t)3);
       sh[j] = ((uint32_t)(uintptr_t)e & 2u) * 8u;
       const int words = n > 0 && r + 8 * (j0 + j) < rows ? (2 * n + (int)(sh[j] >> 3) + 3) >> 2 : 0;
-      const bool whole = RAW || (a >= s.lo && a + 4 * words <= s.hi);
+      const bool whole = a >= s.lo && a + 4 * words <= s.hi;
 #pragma unroll
       for (int k = 0; k < 5; ++k) {
-        w[j][k] = 0u;
+        v[j].w[k] = 0u;
         if (k < words) {
           if (whole) {
-            w[j][k] = RAW ? reinterpret_cast<const uint32_t*>(a)[k]
-                          : __ldg(reinterpret_cast<const uint32_t*>(a) + k);
-          } else {  // at the array's ends: element by element
+            v[j].w[k] = __ldg(reinterpret_cast<const uint32_t*>(a) + k);
+          } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint8_t* x = a + 4 * k + 2 * h;
               if (x >= e && x < e + 2 * n)
-                w[j][k] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(x)) << (16 * h);
+                v[j].w[k] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(x)) << (16 * h);
             }
           }
         }
       }
     }
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      uint32_t v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[k] = __funnelshift_r(w[j][k], w[j][k + 1], sh[j]);
-        if (n < 8) v[k] = n >= 2 * k + 2 ? v[k] : n == 2 * k + 1 ? v[k] & 0xFFFFu : 0u;
-      }
-      *reinterpret_cast<uint4*>(q + j * 1024) = make_uint4(v[0], v[1], v[2], v[3]);
-    }
+    for (int j = 0; j < U; ++j) put_piece(q + j * 1024, v[j], sh[j], keep);
   }
 }
 
@@ -597,18 +637,18 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
             tile_load(smem_addr(Ys) + b * 16384, &dy_map, b * 64, (int)r0, x_ready(xb));
       }
       if (staged) mbar_drain(raw_full, n & 1);
-      auto take = [&](const RowSrc& src, int blocks, const uint8_t* at, uint8_t* dst) {
+      auto take = [&](const RowSrc& src, int blocks, uint32_t at, uint8_t* dst) {
         const uint8_t* start;
         if (src.raw && raw_span(src, r0, p.f.M, start)) {
-          at += src.base + r0 * src.ld - start;
-          for (int b = 0; b < blocks; ++b) place_rows<true>(src, at, b, rows, tid, dst);
-        } else {
+          at += (uint32_t)(src.base + r0 * src.ld - start);
           for (int b = 0; b < blocks; ++b)
-            place_rows<false>(src, src.base + r0 * src.ld, b, rows, tid, dst);
+            place_staged(at, (int)src.ld, src.cols, b, rows, tid, dst);
+        } else {
+          for (int b = 0; b < blocks; ++b) place_rows(src, r0, b, rows, tid, dst);
         }
       };
-      if (!p.x.tiled) take(p.x, nbx, smem + p.raw_off, Xs);
-      if (y_too && !p.dy.tiled) take(p.dy, nby, smem + p.raw_off + p.x.raw, Ys);
+      if (!p.x.tiled) take(p.x, nbx, raw, Xs);
+      if (y_too && !p.dy.tiled) take(p.dy, nby, raw + p.x.raw, Ys);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(x_ready(xb));
@@ -843,7 +883,8 @@ bool aligned16(const void* p, long long ld, int cols) {
 
 // shared memory for a tile as it lies in memory; 0 when the gaps are most of it
 int tile_bytes(long long step, int cols) {
-  const long long b = (step * (kTile - 1) + cols * 2 + 31) & ~15LL;
+  // (place_staged reads up to 20 bytes from a row's last piece)
+  const long long b = (step * (kTile - 1) + cols * 2 + 31 + 16) & ~15LL;
   return b <= 2LL * kTile * (cols * 2 + 16) ? (int)((b + 127) & ~127LL) : 0;
 }
 
