@@ -12,55 +12,106 @@ namespace {
 
 constexpr int kT = 256;  // 16 x 16 threads: thread (tx, ty) has rows ty * RT .., units tx * 4 ..
 
-// rows [r0, r0 + R) of src (cols columns) transposed into dst[k * ld + r]; rows >= M are zero
-template <typename T, int R>
-__device__ __forceinline__ void stage_rows(const T* src, long long lds, long long r0, int M,
-                                           int cols, float* dst, int ld) {
-  for (int i = threadIdx.x; i < R * cols; i += kT) {
-    const int r = i / cols, k = i - r * cols;
-    dst[k * ld + r] = r0 + r < M ? to_f<T>(src[(r0 + r) * lds + k]) : 0.0f;
+// ---------------------------------------------------------------------------------------------
+// packed weights and staging
+// ---------------------------------------------------------------------------------------------
+// Per chunk of 64 units: [Wg | Wu]^T as D rows of kGuLd (64 gate, 64 up units), Wd^T as 64 rows of
+// kODown, and Wd as O rows of kLd (64 units): zeros beyond F and O. A chunk is then copied to
+// shared memory in 16-byte pieces, asynchronously, while the one before is worked on.
+constexpr int kGuLd = 2 * kChunk + 4;
+constexpr int kLd = kChunk + 4;
+__host__ __device__ constexpr int down_ld(int O) { return (O <= 64 ? 64 : 128) + 4; }
+__host__ __device__ constexpr int fwd_floats(int D, int O) {
+  return D * kGuLd + kChunk * down_ld(O);
+}
+__host__ __device__ constexpr int bwd_floats(int D, int O) { return D * kGuLd + O * kLd; }
+
+__global__ void __launch_bounds__(kT) k_pack32(FfnArgs p, bool backward, float* __restrict__ img) {
+  const int per = backward ? bwd_floats(p.D, p.O) : fwd_floats(p.D, p.O);
+  const int c = blockIdx.y, f0 = c * kChunk;
+  const float *wg = (const float*)p.wg, *wu = (const float*)p.wu, *wd = (const float*)p.wd;
+  for (int i = blockIdx.x * kT + threadIdx.x; i < per; i += gridDim.x * kT) {
+    float v = 0.0f;
+    if (i < p.D * kGuLd) {
+      const int k = i / kGuLd, j = i - k * kGuLd;
+      const float* w = wg && j < kChunk ? wg : wu;
+      const int u = wg && j >= kChunk ? j - kChunk : j;
+      if (u < kChunk && f0 + u < p.F) v = w[(size_t)(f0 + u) * p.D + k];
+    } else if (backward) {
+      const int o = (i - p.D * kGuLd) / kLd, u = (i - p.D * kGuLd) - o * kLd;
+      if (u < kChunk && f0 + u < p.F) v = wd[(size_t)o * p.F + f0 + u];
+    } else {
+      const int ld = down_ld(p.O), u = (i - p.D * kGuLd) / ld, o = (i - p.D * kGuLd) - u * ld;
+      if (o < p.O && f0 + u < p.F) v = wd[(size_t)o * p.F + f0 + u];
+    }
+    img[(size_t)c * per + i] = v;
   }
 }
 
-// units [f0, f0 + 64) of w [F, D] transposed into dst[k * ld + j]; units >= F are zero
-template <typename T>
-__device__ __forceinline__ void stage_units(const T* w, int F, int D, int f0, float* dst, int ld) {
-  for (int i = threadIdx.x; i < kChunk * D; i += kT) {
-    const int j = i / D, k = i - j * D;
-    dst[k * ld + j] = f0 + j < F ? to_f<T>(w[(size_t)(f0 + j) * D + k]) : 0.0f;
+__device__ __forceinline__ void copy_chunk(float* dst, const float* src, int floats) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  for (int i = threadIdx.x; i < floats / 4; i += kT)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i * 16), "l"(src + i * 4)
+                 : "memory");
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// all copies but the newest `left` (0 or 1) are there
+__device__ __forceinline__ void chunks_left(int left) {
+  if (left)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// rows [r0, r0 + R) of src transposed into dst[k * (R + 4) + r]; rows >= M are zero
+template <int R>
+__device__ __forceinline__ void stage_rows(const float* src, long long lds, long long r0, int M,
+                                           int cols, float* dst) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 2
+  for (int r = threadIdx.x >> 5; r < R; r += kT / 32) {
+    const bool in = r0 + r < M;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int k = lane + 32 * q;
+      if (k < cols) dst[k * (R + 4) + r] = in ? src[(r0 + r) * lds + k] : 0.0f;
+    }
   }
 }
 
-// units [f0, f0 + 64) of wd [O, F]: dst[o * ldo + j * ldj]
-template <typename T>
-__device__ __forceinline__ void stage_down(const T* wd, int F, int O, int f0, float* dst, int ldo,
-                                           int ldj) {
-  for (int i = threadIdx.x; i < kChunk * O; i += kT) {
-    const int o = i / kChunk, j = i % kChunk;
-    dst[o * ldo + j * ldj] = f0 + j < F ? to_f<T>(wd[(size_t)o * F + f0 + j]) : 0.0f;
-  }
-}
-
-// acc[i][j] += sum_k rowsT[k][ty RT + i] w[k][tx 4 + j]
+// acc[i][j] += sum_k rowsT[k][ty RT + i] w[k][tx 4 + j], two units an instruction
 template <int RT>
 __device__ __forceinline__ void product(const float* rowsT, int ldr, const float* w, int ldw,
-                                        int K, float (&acc)[RT][4]) {
+                                        int K, float2 (&acc)[RT][2]) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const float* xp = rowsT + ty * RT;
+  const float* wp = w + tx * 4;
 #pragma unroll 4
-  for (int k = 0; k < K; ++k) {
-    float xr[RT], wv[4];
+  for (int k = 0; k < K; ++k, xp += ldr, wp += ldw) {
+    float xr[RT];
+    if constexpr (RT == 2) {
+      *reinterpret_cast<float2*>(xr) = *reinterpret_cast<const float2*>(xp);
+    } else {
 #pragma unroll
-    for (int i = 0; i < RT; i += 4)
-      *reinterpret_cast<float4*>(xr + i) =
-          *reinterpret_cast<const float4*>(rowsT + k * ldr + ty * RT + i);
-    *reinterpret_cast<float4*>(wv) = *reinterpret_cast<const float4*>(w + k * ldw + tx * 4);
+      for (int i = 0; i < RT; i += 4)
+        *reinterpret_cast<float4*>(xr + i) = *reinterpret_cast<const float4*>(xp + i);
+    }
+    const float4 wv = *reinterpret_cast<const float4*>(wp);
+    const float2 w0 = make_float2(wv.x, wv.y), w1 = make_float2(wv.z, wv.w);
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xr[i], wv[j], acc[i][j]);
+    for (int i = 0; i < RT; ++i) {
+      const float2 x2 = make_float2(xr[i], xr[i]);
+      acc[i][0] = __ffma2_rn(x2, w0, acc[i][0]);
+      acc[i][1] = __ffma2_rn(x2, w1, acc[i][1]);
+    }
   }
 }
 
+template <int N>
+__device__ __forceinline__ void clear(float2 (&a)[N][2]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i][0] = a[i][1] = make_float2(0.0f, 0.0f);
+}
 template <int N, int M>
 __device__ __forceinline__ void clear(float (&a)[N][M]) {
 #pragma unroll
@@ -68,64 +119,76 @@ __device__ __forceinline__ void clear(float (&a)[N][M]) {
 #pragma unroll
     for (int j = 0; j < M; ++j) a[i][j] = 0.0f;
 }
-
-constexpr int kFwdRows = 128;
-constexpr int kFwdLd = kFwdRows + 4;
-constexpr int kGuLd = 2 * kChunk + 4;
-constexpr int kLd = 64 + 4;
-
-int fwd_smem(int D, int O) {
-  const int Op = O <= 64 ? 64 : 128;
-  return 4 * (D * kFwdLd + D * kGuLd + kChunk * (Op + 4) + kChunk * kFwdLd);
+__device__ __forceinline__ float pick(const float2 (&a)[2], int j) {
+  return j == 0 ? a[0].x : j == 1 ? a[0].y : j == 2 ? a[1].x : a[1].y;
+}
+// the thread's R / 16 rows of one unit
+template <int RT>
+__device__ __forceinline__ void put_rows(float* dst, const float* v) {
+  if constexpr (RT == 2) {
+    *reinterpret_cast<float2*>(dst) = make_float2(v[0], v[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < RT; i += 4)
+      *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  }
 }
 
-template <typename T, int ACT, bool GATED, int NO>  // NO: 64-wide pieces of O
-__global__ void __launch_bounds__(kT, 1) k_ffn(FfnArgs p) {
+// ---------------------------------------------------------------------------------------------
+// forward, R rows a CTA
+// ---------------------------------------------------------------------------------------------
+int fwd_smem(int R, int D, int O, int bufs) {
+  return 4 * (D * (R + 4) + bufs * fwd_floats(D, O) + kChunk * (R + 4));
+}
+
+template <int ACT, bool GATED, int NO, int R>  // NO: 64-wide pieces of O
+__global__ void __launch_bounds__(kT, 1) k_ffn(FfnArgs p, const float* __restrict__ img,
+                                               int bufs) {
   extern __shared__ __align__(16) float sm[];
-  constexpr int RT = kFwdRows / 16, ldo = NO * 64 + 4;
-  float* Xs = sm;                          // [D][132]
-  float* Ws = Xs + p.D * kFwdLd;           // [D][132]: 64 gate units, 64 up units
-  float* Ds = Ws + p.D * kGuLd;            // [64][ldo]
-  float* Hs = Ds + kChunk * ldo;           // [64][132]
+  constexpr int RT = R / 16, ldr = R + 4, ldo = NO * 64 + 4;
+  float* Xs = sm;                     // [D][ldr]
+  float* Hs = Xs + p.D * ldr;         // [64][ldr]
+  float* Ws = Hs + kChunk * ldr;      // [bufs] of a chunk
+  const int per = fwd_floats(p.D, p.O);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const long long r0 = (long long)blockIdx.x * kFwdRows;
-  const T *x = (const T*)p.x, *wg = (const T*)p.wg, *wu = (const T*)p.wu, *wd = (const T*)p.wd;
-  stage_rows<T, kFwdRows>(x, p.ldx, r0, p.M, p.D, Xs, kFwdLd);
-  for (int i = threadIdx.x; i < kChunk * ldo; i += kT) Ds[i] = 0.0f;  // columns >= O stay zero
-  float yv[NO][RT][4];
+  const long long r0 = (long long)blockIdx.x * R;
+  const int nch = (p.F + kChunk - 1) / kChunk;
+  copy_chunk(Ws, img, per);
+  stage_rows<R>((const float*)p.x, p.ldx, r0, p.M, p.D, Xs);
+  float2 yv[NO][RT][2];
 #pragma unroll
   for (int n = 0; n < NO; ++n) clear(yv[n]);
-  for (int f0 = 0; f0 < p.F; f0 += kChunk) {
+  for (int c = 0; c < nch; ++c) {
+    float* W = Ws + (bufs > 1 ? (c & 1) * per : 0);
+    const bool ahead = bufs > 1 && c + 1 < nch;
+    if (ahead) copy_chunk(Ws + ((c + 1) & 1) * per, img + (size_t)(c + 1) * per, per);
+    chunks_left(ahead);
     __syncthreads();
-    if (GATED) stage_units(wg, p.F, p.D, f0, Ws, kGuLd);
-    stage_units(wu, p.F, p.D, f0, Ws + (GATED ? kChunk : 0), kGuLd);
-    stage_down(wd, p.F, p.O, f0, Ds, 1, ldo);
-    __syncthreads();
-    float a[RT][4], u[RT][4];
+    float2 a[RT][2], u[RT][2];
     clear(a);
-    product<RT>(Xs, kFwdLd, Ws, kGuLd, p.D, a);
+    product<RT>(Xs, ldr, W, kGuLd, p.D, a);
     if (GATED) {
       clear(u);
-      product<RT>(Xs, kFwdLd, Ws + kChunk, kGuLd, p.D, u);
+      product<RT>(Xs, ldr, W + kChunk, kGuLd, p.D, u);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j) {
+      float h[RT];
 #pragma unroll
-      for (int i = 0; i < RT; i += 4) {
-        float h[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          h[q] = act_of<ACT>(a[i + q][j]);
-          if (GATED) h[q] *= u[i + q][j];
-        }
-        *reinterpret_cast<float4*>(Hs + (tx * 4 + j) * kFwdLd + ty * RT + i) =
-            *reinterpret_cast<float4*>(h);
+      for (int i = 0; i < RT; ++i) {
+        h[i] = act_of<ACT>(pick(a[i], j));
+        if (GATED) h[i] *= pick(u[i], j);
       }
+      put_rows<RT>(Hs + (tx * 4 + j) * ldr + ty * RT, h);
+    }
     __syncthreads();
 #pragma unroll
-    for (int n = 0; n < NO; ++n) product<RT>(Hs, kFwdLd, Ds + n * 64, ldo, kChunk, yv[n]);
+    for (int n = 0; n < NO; ++n)
+      product<RT>(Hs, ldr, W + p.D * kGuLd + n * 64, ldo, kChunk, yv[n]);
+    __syncthreads();
+    if (bufs == 1 && c + 1 < nch) copy_chunk(Ws, img + (size_t)(c + 1) * per, per);
   }
-  T* y = (T*)p.y;
+  float* y = (float*)p.y;
 #pragma unroll
   for (int n = 0; n < NO; ++n)
 #pragma unroll
@@ -134,7 +197,7 @@ __global__ void __launch_bounds__(kT, 1) k_ffn(FfnArgs p) {
       for (int j = 0; j < 4; ++j) {
         const int o = n * 64 + tx * 4 + j;
         const long long r = r0 + ty * RT + i;
-        if (o < p.O && r < p.M) y[r * p.ldy + o] = from_f<T>(yv[n][i][j]);
+        if (o < p.O && r < p.M) y[r * p.ldy + o] = pick(yv[n][i], j);
       }
 }
 
@@ -242,165 +305,184 @@ k_ffn_few(FfnArgs p) {
   }
 }
 
-// a, u, dh of one 64-row tile and chunk, turned into da, du (and h) in place
-template <int ACT, bool GATED>
-__device__ __forceinline__ void hidden_grads(const float* Xs, const float* Ys, const float* Ws,
-                                             const float* Ds, int D, int O, float (&da)[4][4],
-                                             float (&du)[4][4], float (&h)[4][4]) {
-  float a[4][4], u[4][4], dh[4][4];
+// ---------------------------------------------------------------------------------------------
+// gradients, R rows a tile
+// ---------------------------------------------------------------------------------------------
+
+// a, u, dh of one tile and chunk, turned into da, du (and h)
+template <int ACT, bool GATED, int RT>
+__device__ __forceinline__ void hidden_grads(const float* Xs, const float* Ys, int ldr,
+                                             const float* W, int D, int O, float (&da)[RT][4],
+                                             float (&du)[RT][4], float (&h)[RT][4]) {
+  float2 a[RT][2], u[RT][2], dh[RT][2];
   clear(a);
   clear(dh);
-  product<4>(Xs, kLd, Ws, kGuLd, D, a);
+  product<RT>(Xs, ldr, W, kGuLd, D, a);
   if (GATED) {
     clear(u);
-    product<4>(Xs, kLd, Ws + kChunk, kGuLd, D, u);
+    product<RT>(Xs, ldr, W + kChunk, kGuLd, D, u);
   }
-  product<4>(Ys, kLd, Ds, kLd, O, dh);
+  product<RT>(Ys, ldr, W + D * kGuLd, kLd, O, dh);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float s;
-      const float f = act_and_slope<ACT>(a[i][j], s);
-      h[i][j] = GATED ? f * u[i][j] : f;
-      da[i][j] = GATED ? dh[i][j] * u[i][j] * s : dh[i][j] * s;
-      du[i][j] = GATED ? dh[i][j] * f : 0.0f;
+      const float f = act_and_slope<ACT>(pick(a[i], j), s), g = pick(dh[i], j);
+      const float v = GATED ? pick(u[i], j) : 1.0f;
+      h[i][j] = GATED ? f * v : f;
+      da[i][j] = GATED ? g * v * s : g * s;
+      du[i][j] = GATED ? g * f : 0.0f;
     }
 }
 
-int dx_smem(int D, int O) { return 4 * (D * kLd + O * kLd + D * kGuLd + O * kLd + 2 * 64 * kLd); }
-int dw_smem(int D, int O) { return 4 * (D * kLd + O * kLd + D * kGuLd + O * kLd + 3 * 64 * kLd); }
+int dx_smem(int R, int D, int O, int bufs) {
+  return 4 * ((D + O) * (R + 4) + 2 * kChunk * (R + 4) + bufs * bwd_floats(D, O));
+}
+int dw_smem(int R, int D, int O) {
+  return 4 * ((D + O) * (R + 4) + 3 * R * kLd + bwd_floats(D, O));
+}
 
-// dx of one 64-row tile: all chunks in turn
-template <typename T, int ACT, bool GATED>
-__global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p) {
+// dx of one tile: all chunks in turn
+template <int ACT, bool GATED, int R>
+__global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __restrict__ img,
+                                                  int bufs) {
   extern __shared__ __align__(16) float sm[];
-  float* Xs = sm;                    // [D][68]
-  float* Ys = Xs + p.D * kLd;        // [O][68]
-  float* Ws = Ys + p.O * kLd;        // [D][132]
-  float* Ds = Ws + p.D * kGuLd;      // [O][68]
-  float* As = Ds + p.O * kLd;        // [64 units][68 rows] da, then du
-  float* Us = As + kChunk * kLd;
+  constexpr int RT = R / 16, ldr = R + 4;
+  float* Xs = sm;                    // [D][ldr]
+  float* Ys = Xs + p.D * ldr;        // [O][ldr]
+  float* As = Ys + p.O * ldr;        // [64 units][ldr] da, then du
+  float* Us = As + kChunk * ldr;
+  float* Ws = Us + kChunk * ldr;     // [bufs] of a chunk
+  const int per = bwd_floats(p.D, p.O), nch = (p.F + kChunk - 1) / kChunk;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const long long r0 = (long long)blockIdx.x * 64;
-  const T *wg = (const T*)p.wg, *wu = (const T*)p.wu, *wd = (const T*)p.wd;
-  stage_rows<T, 64>((const T*)p.x, p.ldx, r0, p.M, p.D, Xs, kLd);
-  stage_rows<T, 64>((const T*)p.dy, p.lddy, r0, p.M, p.O, Ys, kLd);
-  float acc[8][4];  // columns tx + 16 c, rows ty * 4 + i
+  const long long r0 = (long long)blockIdx.x * R;
+  copy_chunk(Ws, img, per);
+  stage_rows<R>((const float*)p.x, p.ldx, r0, p.M, p.D, Xs);
+  stage_rows<R>((const float*)p.dy, p.lddy, r0, p.M, p.O, Ys);
+  float acc[8][RT];  // columns tx + 16 c, rows ty * RT + i
   clear(acc);
-  for (int f0 = 0; f0 < p.F; f0 += kChunk) {
+  for (int ch = 0; ch < nch; ++ch) {
+    float* W = Ws + (bufs > 1 ? (ch & 1) * per : 0);
+    const bool ahead = bufs > 1 && ch + 1 < nch;
+    if (ahead) copy_chunk(Ws + ((ch + 1) & 1) * per, img + (size_t)(ch + 1) * per, per);
+    chunks_left(ahead);
     __syncthreads();
-    if (GATED) stage_units(wg, p.F, p.D, f0, Ws, kGuLd);
-    stage_units(wu, p.F, p.D, f0, Ws + (GATED ? kChunk : 0), kGuLd);
-    stage_down(wd, p.F, p.O, f0, Ds, kLd, 1);
-    __syncthreads();
-    float da[4][4], du[4][4], h[4][4];
-    hidden_grads<ACT, GATED>(Xs, Ys, Ws, Ds, p.D, p.O, da, du, h);
+    float da[RT][4], du[RT][4], h[RT][4];
+    hidden_grads<ACT, GATED, RT>(Xs, Ys, ldr, W, p.D, p.O, da, du, h);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      *reinterpret_cast<float4*>(As + (tx * 4 + j) * kLd + ty * 4) =
-          make_float4(da[0][j], da[1][j], da[2][j], da[3][j]);
-      if (GATED)
-        *reinterpret_cast<float4*>(Us + (tx * 4 + j) * kLd + ty * 4) =
-            make_float4(du[0][j], du[1][j], du[2][j], du[3][j]);
+      float v[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) v[i] = da[i][j];
+      put_rows<RT>(As + (tx * 4 + j) * ldr + ty * RT, v);
+      if (GATED) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) v[i] = du[i][j];
+        put_rows<RT>(Us + (tx * 4 + j) * ldr + ty * RT, v);
+      }
     }
     __syncthreads();
+#pragma unroll 2
     for (int f = 0; f < kChunk; ++f) {
-      float av[4], uv[4];
-      *reinterpret_cast<float4*>(av) = *reinterpret_cast<const float4*>(As + f * kLd + ty * 4);
-      if (GATED)
-        *reinterpret_cast<float4*>(uv) = *reinterpret_cast<const float4*>(Us + f * kLd + ty * 4);
+      float av[RT], uv[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        av[i] = As[f * ldr + ty * RT + i];
+        if (GATED) uv[i] = Us[f * ldr + ty * RT + i];
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const int d = tx + 16 * c;
-        if (d >= p.D) break;
-        const float g = Ws[d * kGuLd + f], v = GATED ? Ws[d * kGuLd + kChunk + f] : 0.0f;
+        if (16 * c >= p.D) break;
+        const int d = min(tx + 16 * c, p.D - 1);
+        const float g = W[d * kGuLd + f], v = GATED ? W[d * kGuLd + kChunk + f] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RT; ++i) {
           acc[c][i] = fmaf(av[i], g, acc[c][i]);
           if (GATED) acc[c][i] = fmaf(uv[i], v, acc[c][i]);
         }
       }
     }
+    __syncthreads();
+    if (bufs == 1 && ch + 1 < nch) copy_chunk(Ws, img + (size_t)(ch + 1) * per, per);
   }
-  T* dx = (T*)p.dx;
+  float* dx = (float*)p.dx;
 #pragma unroll
   for (int c = 0; c < 8; ++c)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RT; ++i) {
       const int d = tx + 16 * c;
-      const long long r = r0 + ty * 4 + i;
-      if (d < p.D && r < p.M) dx[r * p.lddx + d] = from_f<T>(acc[c][i]);
+      const long long r = r0 + ty * RT + i;
+      if (d < p.D && r < p.M) dx[r * p.lddx + d] = acc[c][i];
     }
 }
 
 // partial weight gradients of chunk blockIdx.x over the row tiles blockIdx.y, + splits, ...
-template <typename T, int ACT, bool GATED>
-__global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p) {
+template <int ACT, bool GATED, int R>
+__global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p, const float* __restrict__ img) {
   extern __shared__ __align__(16) float sm[];
+  constexpr int RT = R / 16, ldr = R + 4;
   float* Xs = sm;
-  float* Ys = Xs + p.D * kLd;
-  float* Ws = Ys + p.O * kLd;
-  float* Ds = Ws + p.D * kGuLd;
-  float* As = Ds + p.O * kLd;        // [64 rows][68 units] da, du, h
-  float* Us = As + 64 * kLd;
-  float* Hs = Us + 64 * kLd;
+  float* Ys = Xs + p.D * ldr;
+  float* As = Ys + p.O * ldr;        // [R rows][68 units] da, du, h
+  float* Us = As + R * kLd;
+  float* Hs = Us + R * kLd;
+  float* W = Hs + R * kLd;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int f0 = blockIdx.x * kChunk;
-  const T *wg = (const T*)p.wg, *wu = (const T*)p.wu, *wd = (const T*)p.wd;
-  if (GATED) stage_units(wg, p.F, p.D, f0, Ws, kGuLd);
-  stage_units(wu, p.F, p.D, f0, Ws + (GATED ? kChunk : 0), kGuLd);
-  stage_down(wd, p.F, p.O, f0, Ds, kLd, 1);
-  float ga[8][4], gu[8][4], gd[8][4];  // rows (of D or O) ty + 16 c, units tx * 4 + j
+  const int f0 = blockIdx.x * kChunk, per = bwd_floats(p.D, p.O);
+  copy_chunk(W, img + (size_t)blockIdx.x * per, per);
+  chunks_left(0);
+  float2 ga[8][2], gu[8][2], gd[8][2];  // rows (of D or O) ty + 16 c, units tx * 4 + j
   clear(ga);
   clear(gu);
   clear(gd);
-  const int tiles = (int)(((long long)p.M + 63) / 64);
+  const int tiles = (int)(((long long)p.M + R - 1) / R);
   for (int t = blockIdx.y; t < tiles; t += p.splits) {
     __syncthreads();
-    stage_rows<T, 64>((const T*)p.x, p.ldx, (long long)t * 64, p.M, p.D, Xs, kLd);
-    stage_rows<T, 64>((const T*)p.dy, p.lddy, (long long)t * 64, p.M, p.O, Ys, kLd);
+    stage_rows<R>((const float*)p.x, p.ldx, (long long)t * R, p.M, p.D, Xs);
+    stage_rows<R>((const float*)p.dy, p.lddy, (long long)t * R, p.M, p.O, Ys);
     __syncthreads();
-    float da[4][4], du[4][4], h[4][4];
-    hidden_grads<ACT, GATED>(Xs, Ys, Ws, Ds, p.D, p.O, da, du, h);
+    float da[RT][4], du[RT][4], h[RT][4];
+    hidden_grads<ACT, GATED, RT>(Xs, Ys, ldr, W, p.D, p.O, da, du, h);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = (ty * 4 + i) * kLd + tx * 4;
-      *reinterpret_cast<float4*>(As + at) = *reinterpret_cast<float4*>(da[i]);
-      if (GATED) *reinterpret_cast<float4*>(Us + at) = *reinterpret_cast<float4*>(du[i]);
-      *reinterpret_cast<float4*>(Hs + at) = *reinterpret_cast<float4*>(h[i]);
+    for (int i = 0; i < RT; ++i) {
+      const int at = (ty * RT + i) * kLd + tx * 4;
+      *reinterpret_cast<float4*>(As + at) = make_float4(da[i][0], da[i][1], da[i][2], da[i][3]);
+      if (GATED)
+        *reinterpret_cast<float4*>(Us + at) = make_float4(du[i][0], du[i][1], du[i][2], du[i][3]);
+      *reinterpret_cast<float4*>(Hs + at) = make_float4(h[i][0], h[i][1], h[i][2], h[i][3]);
     }
     __syncthreads();
-    for (int r = 0; r < 64; r += 4) {
-      float av[4][4], uv[4][4], hv[4][4];
+    for (int r = 0; r < R; r += 2) {
+      float4 av[2], uv[2], hv[2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 2; ++q) {
         const int at = (r + q) * kLd + tx * 4;
-        *reinterpret_cast<float4*>(av[q]) = *reinterpret_cast<const float4*>(As + at);
-        if (GATED) *reinterpret_cast<float4*>(uv[q]) = *reinterpret_cast<const float4*>(Us + at);
-        *reinterpret_cast<float4*>(hv[q]) = *reinterpret_cast<const float4*>(Hs + at);
+        av[q] = *reinterpret_cast<const float4*>(As + at);
+        if (GATED) uv[q] = *reinterpret_cast<const float4*>(Us + at);
+        hv[q] = *reinterpret_cast<const float4*>(Hs + at);
       }
+      auto add = [](float2 (&g)[2], float x, const float4& v) {
+        const float2 x2 = make_float2(x, x);
+        g[0] = __ffma2_rn(x2, make_float2(v.x, v.y), g[0]);
+        g[1] = __ffma2_rn(x2, make_float2(v.z, v.w), g[1]);
+      };
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const int k = ty + 16 * c;
         if (k < p.D) {
-          float xv[4];
-          *reinterpret_cast<float4*>(xv) = *reinterpret_cast<const float4*>(Xs + k * kLd + r);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              ga[c][j] = fmaf(xv[q], av[q][j], ga[c][j]);
-              if (GATED) gu[c][j] = fmaf(xv[q], uv[q][j], gu[c][j]);
-            }
+          const float2 x = *reinterpret_cast<const float2*>(Xs + k * ldr + r);
+          add(ga[c], x.x, av[0]);
+          add(ga[c], x.y, av[1]);
+          if (GATED) {
+            add(gu[c], x.x, uv[0]);
+            add(gu[c], x.y, uv[1]);
+          }
         }
         if (k < p.O) {
-          float yv[4];
-          *reinterpret_cast<float4*>(yv) = *reinterpret_cast<const float4*>(Ys + k * kLd + r);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) gd[c][j] = fmaf(yv[q], hv[q][j], gd[c][j]);
+          const float2 y = *reinterpret_cast<const float2*>(Ys + k * ldr + r);
+          add(gd[c], y.x, hv[0]);
+          add(gd[c], y.y, hv[1]);
         }
       }
     }
@@ -414,10 +496,10 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p) {
       const int k = ty + 16 * c, f = f0 + tx * 4 + j;
       if (f >= p.F) continue;
       if (k < p.D) {
-        part[(size_t)f * p.D + k] = ga[c][j];
-        if (GATED) part[FD + (size_t)f * p.D + k] = gu[c][j];
+        part[(size_t)f * p.D + k] = pick(ga[c], j);
+        if (GATED) part[FD + (size_t)f * p.D + k] = pick(gu[c], j);
       }
-      if (k < p.O) part[(GATED ? 2 : 1) * FD + (size_t)f * p.O + k] = gd[c][j];
+      if (k < p.O) part[(GATED ? 2 : 1) * FD + (size_t)f * p.O + k] = pick(gd[c], j);
     }
 }
 
@@ -460,16 +542,56 @@ bool allow_smem(K kernel, int bytes) {
          cudaSuccess;
 }
 
+// rows of a gradient tile: 32 while 64 would leave SMs without one
+int grad_rows(long long M) { return M <= 64 * 148 ? 32 : 64; }
+
 // row splits of the weight gradients: enough CTAs for the machine, and at most 8,192 rows a split
 // (an fp32 sum of n products is off by about sqrt(n) 2^-25 of its size)
 int dw_splits(long long M, int F) {
-  const int chunks = (F + kChunk - 1) / kChunk;
-  const long long tiles = (M + 63) / 64;
+  const int chunks = (F + kChunk - 1) / kChunk, R = grad_rows(M);
+  const long long tiles = (M + R - 1) / R;
   long long s = (148 + chunks - 1) / chunks;
-  if (s < (tiles + 127) / 128) s = (tiles + 127) / 128;
+  if (s < (M + 8191) / 8192) s = (M + 8191) / 8192;
   if (s > tiles) s = tiles;
   if (s > 65535) s = 65535;  // the grid's limit
   return (int)(s < 1 ? 1 : s);
+}
+
+size_t pack32_bytes(int D, int F, int O, bool backward) {
+  const size_t n = (size_t)((F + kChunk - 1) / kChunk) *
+                   (backward ? bwd_floats(D, O) : fwd_floats(D, O)) * 4;
+  return (n + 255) & ~(size_t)255;
+}
+
+void pack32(const FfnArgs& p, bool backward, float* img, cudaStream_t st) {
+  const int per = backward ? bwd_floats(p.D, p.O) : fwd_floats(p.D, p.O);
+  k_pack32<<<dim3((per + kT - 1) / kT, (p.F + kChunk - 1) / kChunk), kT, 0, st>>>(p, backward,
+                                                                                  img);
+}
+
+constexpr int kSmemMax = 232448 - 1024;
+
+template <int ACT, bool GATED, int NO, int R>
+int launch_fwd(const FfnArgs& p, const float* img, cudaStream_t st) {
+  const int bufs = fwd_smem(R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
+  const int smem = fwd_smem(R, p.D, p.O, bufs);
+  if (!allow_smem(k_ffn<ACT, GATED, NO, R>, smem)) return SPLAT_ERR_CUDA;
+  k_ffn<ACT, GATED, NO, R>
+      <<<(unsigned)(((long long)p.M + R - 1) / R), kT, smem, st>>>(p, img, bufs);
+  return last_error();
+}
+
+// Rows of a CTA: 128 feed the lanes best (a thread's 8 x 4 sums take 3 shared loads a step, 2 x 4
+// take 3 as well), 32 where 128 would leave most SMs without a tile.
+template <int ACT, bool GATED>
+int run_forward(const FfnArgs& p, float* img, cudaStream_t st) {
+  pack32(p, false, img, st);
+  const bool small = p.M <= 64 * 148;
+  if (p.O <= 64)
+    return small ? launch_fwd<ACT, GATED, 1, 32>(p, img, st)
+                 : launch_fwd<ACT, GATED, 1, 128>(p, img, st);
+  return small ? launch_fwd<ACT, GATED, 2, 32>(p, img, st)
+               : launch_fwd<ACT, GATED, 2, 128>(p, img, st);
 }
 
 template <typename T, int ACT, bool GATED>
@@ -483,41 +605,36 @@ int run_few(const FfnArgs& p, cudaStream_t st) {
   return last_error();
 }
 
-template <typename T, int ACT, bool GATED>
-int run_forward(const FfnArgs& p, cudaStream_t st) {
-  const int smem = fwd_smem(p.D, p.O);
-  const unsigned grid = (unsigned)(((long long)p.M + kFwdRows - 1) / kFwdRows);
-  if (p.O <= 64) {
-    if (!allow_smem(k_ffn<T, ACT, GATED, 1>, smem)) return SPLAT_ERR_CUDA;
-    k_ffn<T, ACT, GATED, 1><<<grid, kT, smem, st>>>(p);
-  } else {
-    if (!allow_smem(k_ffn<T, ACT, GATED, 2>, smem)) return SPLAT_ERR_CUDA;
-    k_ffn<T, ACT, GATED, 2><<<grid, kT, smem, st>>>(p);
-  }
-  return last_error();
-}
-
 template <typename T, bool GATED> int run_join(const FfnArgs& p, cudaStream_t st) {
   const size_t n = ((GATED ? 2 : 1) * (size_t)p.D + p.O) * p.F;
   k_ffn_join<T, GATED><<<(unsigned)((n + 31) / 32), kT, 0, st>>>(p);
   return last_error();
 }
 
-template <typename T, int ACT, bool GATED>
-int run_backward(const FfnArgs& p, cudaStream_t st) {
+template <int ACT, bool GATED, int R>
+int launch_bwd(const FfnArgs& p, const float* img, cudaStream_t st) {
   if (p.dx && p.M > 0) {
-    const int smem = dx_smem(p.D, p.O);
-    if (!allow_smem(k_ffn_dx<T, ACT, GATED>, smem)) return SPLAT_ERR_CUDA;
-    k_ffn_dx<T, ACT, GATED><<<(unsigned)(((long long)p.M + 63) / 64), kT, smem, st>>>(p);
+    const int bufs = dx_smem(R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
+    const int smem = dx_smem(R, p.D, p.O, bufs);
+    if (!allow_smem(k_ffn_dx<ACT, GATED, R>, smem)) return SPLAT_ERR_CUDA;
+    k_ffn_dx<ACT, GATED, R>
+        <<<(unsigned)(((long long)p.M + R - 1) / R), kT, smem, st>>>(p, img, bufs);
   }
   if (p.dwg || p.dwu || p.dwd) {
-    const int smem = dw_smem(p.D, p.O);
-    if (!allow_smem(k_ffn_dw<T, ACT, GATED>, smem)) return SPLAT_ERR_CUDA;
+    const int smem = dw_smem(R, p.D, p.O);
+    if (!allow_smem(k_ffn_dw<ACT, GATED, R>, smem)) return SPLAT_ERR_CUDA;
     const dim3 grid((p.F + kChunk - 1) / kChunk, p.splits);
-    k_ffn_dw<T, ACT, GATED><<<grid, kT, smem, st>>>(p);
-    return run_join<T, GATED>(p, st);
+    k_ffn_dw<ACT, GATED, R><<<grid, kT, smem, st>>>(p, img);
+    return run_join<float, GATED>(p, st);
   }
   return last_error();
+}
+
+template <int ACT, bool GATED>
+int run_backward(const FfnArgs& p, float* img, cudaStream_t st) {
+  pack32(p, true, img, st);
+  return grad_rows(p.M) == 32 ? launch_bwd<ACT, GATED, 32>(p, img, st)
+                              : launch_bwd<ACT, GATED, 64>(p, img, st);
 }
 
 // A few rows by the clusters; otherwise fp32 on the fp32 lanes, bf16 and fp16 on the tensor cores.
@@ -525,9 +642,10 @@ template <typename T, int ACT, bool GATED>
 int run(FfnArgs& p, int dtype, bool backward, void* scratch, cudaStream_t st) {
   if (!backward && p.M <= kFewRows) return run_few<T, ACT, GATED>(p, st);
   if constexpr (sizeof(T) == 4) {
-    p.part = (float*)scratch;
+    p.part = (float*)((char*)scratch + pack32_bytes(p.D, p.F, p.O, backward));
     p.splits = dw_splits(p.M, p.F);
-    return backward ? run_backward<T, ACT, GATED>(p, st) : run_forward<T, ACT, GATED>(p, st);
+    return backward ? run_backward<ACT, GATED>(p, (float*)scratch, st)
+                    : run_forward<ACT, GATED>(p, (float*)scratch, st);
   } else {
     p.part = (float*)((char*)scratch + ffn_tc_image_bytes(p.D, p.F, p.O, GATED));
     p.splits = ffn_tc_splits(p.M, p.F);
@@ -572,7 +690,8 @@ long long splat_ffn_scratch(int M, int D, int F, int O, int dtype, int gated, in
   if (check_sizes(M, D, F, O, dtype, SPLAT_ACT_SILU) != SPLAT_OK) return 0;
   if (!backward && M <= kFewRows) return 0;
   const bool tc = dtype != SPLAT_F32;
-  long long n = tc ? (long long)ffn_tc_image_bytes(D, F, O, gated != 0) : 0;
+  long long n = tc ? (long long)ffn_tc_image_bytes(D, F, O, gated != 0)
+                   : (long long)pack32_bytes(D, F, O, backward != 0);
   if (backward)
     n += (long long)F * ((gated ? 2 : 1) * D + O) * 4 *
          (tc ? ffn_tc_splits(M, F) : dw_splits(M, F));
