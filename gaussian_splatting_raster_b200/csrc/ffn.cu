@@ -15,16 +15,20 @@ constexpr int kT = 256;  // 16 x 16 threads: thread (tx, ty) has rows ty * RT ..
 // ---------------------------------------------------------------------------------------------
 // packed weights and staging
 // ---------------------------------------------------------------------------------------------
-// Per chunk of 64 units: [Wg | Wu]^T as D rows of kGuLd (64 gate, 64 up units), Wd^T as 64 rows of
-// kODown, and Wd as O rows of kLd (64 units): zeros beyond F and O. A chunk is then copied to
-// shared memory in 16-byte pieces, asynchronously, while the one before is worked on.
+// Per chunk of 64 units: [Wg | Wu]^T as D rows of kGuLd (64 gate, 64 up units); then, forward, Wd^T
+// as 64 rows of down_ld(O), or, for the gradients, Wd as O rows of kLd (64 units) and [Wg; Wu] as
+// 128 rows of down_ld(D): zeros beyond F, D and O. A chunk is then copied to shared memory in
+// 16-byte pieces, asynchronously, while the one before is worked on (where two fit).
 constexpr int kGuLd = 2 * kChunk + 4;
 constexpr int kLd = kChunk + 4;
 __host__ __device__ constexpr int down_ld(int O) { return (O <= 64 ? 64 : 128) + 4; }
 __host__ __device__ constexpr int fwd_floats(int D, int O) {
   return D * kGuLd + kChunk * down_ld(O);
 }
-__host__ __device__ constexpr int bwd_floats(int D, int O) { return D * kGuLd + O * kLd; }
+__host__ __device__ constexpr int dw_floats(int D, int O) { return D * kGuLd + O * kLd; }
+__host__ __device__ constexpr int bwd_floats(int D, int O) {
+  return dw_floats(D, O) + 2 * kChunk * down_ld(D);
+}
 
 __global__ void __launch_bounds__(kT) k_pack32(FfnArgs p, bool backward, float* __restrict__ img) {
   const int per = backward ? bwd_floats(p.D, p.O) : fwd_floats(p.D, p.O);
@@ -37,6 +41,11 @@ __global__ void __launch_bounds__(kT) k_pack32(FfnArgs p, bool backward, float* 
       const float* w = wg && j < kChunk ? wg : wu;
       const int u = wg && j >= kChunk ? j - kChunk : j;
       if (u < kChunk && f0 + u < p.F) v = w[(size_t)(f0 + u) * p.D + k];
+    } else if (backward && i >= dw_floats(p.D, p.O)) {
+      const int ld = down_ld(p.D), q = i - dw_floats(p.D, p.O), j = q / ld, k = q - j * ld;
+      const float* w = wg && j < kChunk ? wg : wu;
+      const int u = wg && j >= kChunk ? j - kChunk : j;
+      if (u < kChunk && f0 + u < p.F && k < p.D) v = w[(size_t)(f0 + u) * p.D + k];
     } else if (backward) {
       const int o = (i - p.D * kGuLd) / kLd, u = (i - p.D * kGuLd) - o * kLd;
       if (u < kChunk && f0 + u < p.F) v = wd[(size_t)o * p.F + f0 + u];
@@ -79,6 +88,27 @@ __device__ __forceinline__ void stage_rows(const float* src, long long lds, long
   }
 }
 
+// the same as asynchronous copies
+template <int R>
+__device__ __forceinline__ void copy_rows(const float* src, long long lds, long long r0, int M,
+                                          int cols, float* dst) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  for (int r = threadIdx.x >> 5; r < R; r += kT / 32) {
+    const bool in = r0 + r < M;
+    const float* row = src + (in ? r0 + r : 0) * lds;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int k = lane + 32 * q;
+      if (k < cols)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                         d + 4 * (k * (R + 4) + r)),
+                     "l"(row + k), "r"(in ? 4 : 0)
+                     : "memory");
+    }
+  }
+}
+
 // acc[i][j] += sum_k rowsT[k][ty RT + i] w[k][tx 4 + j], two units an instruction
 template <int RT>
 __device__ __forceinline__ void product(const float* rowsT, int ldr, const float* w, int ldw,
@@ -103,6 +133,36 @@ __device__ __forceinline__ void product(const float* rowsT, int ldr, const float
       const float2 x2 = make_float2(xr[i], xr[i]);
       acc[i][0] = __ffma2_rn(x2, w0, acc[i][0]);
       acc[i][1] = __ffma2_rn(x2, w1, acc[i][1]);
+    }
+  }
+}
+
+// the same with two sets of units, kChunk apart
+template <int RT>
+__device__ __forceinline__ void product_pair(const float* rowsT, int ldr, const float* w, int ldw,
+                                             int K, float2 (&a)[RT][2], float2 (&b)[RT][2]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const float* xp = rowsT + ty * RT;
+  const float* wp = w + tx * 4;
+#pragma unroll 2
+  for (int k = 0; k < K; ++k, xp += ldr, wp += ldw) {
+    float xr[RT];
+    if constexpr (RT == 2) {
+      *reinterpret_cast<float2*>(xr) = *reinterpret_cast<const float2*>(xp);
+    } else {
+#pragma unroll
+      for (int i = 0; i < RT; i += 4)
+        *reinterpret_cast<float4*>(xr + i) = *reinterpret_cast<const float4*>(xp + i);
+    }
+    const float4 wv = *reinterpret_cast<const float4*>(wp);
+    const float4 vv = *reinterpret_cast<const float4*>(wp + kChunk);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const float2 x2 = make_float2(xr[i], xr[i]);
+      a[i][0] = __ffma2_rn(x2, make_float2(wv.x, wv.y), a[i][0]);
+      a[i][1] = __ffma2_rn(x2, make_float2(wv.z, wv.w), a[i][1]);
+      b[i][0] = __ffma2_rn(x2, make_float2(vv.x, vv.y), b[i][0]);
+      b[i][1] = __ffma2_rn(x2, make_float2(vv.z, vv.w), b[i][1]);
     }
   }
 }
@@ -166,10 +226,11 @@ __global__ void __launch_bounds__(kT, 1) k_ffn(FfnArgs p, const float* __restric
     __syncthreads();
     float2 a[RT][2], u[RT][2];
     clear(a);
-    product<RT>(Xs, ldr, W, kGuLd, p.D, a);
     if (GATED) {
       clear(u);
-      product<RT>(Xs, ldr, W + kChunk, kGuLd, p.D, u);
+      product_pair<RT>(Xs, ldr, W, kGuLd, p.D, a, u);
+    } else {
+      product<RT>(Xs, ldr, W, kGuLd, p.D, a);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -317,10 +378,11 @@ __device__ __forceinline__ void hidden_grads(const float* Xs, const float* Ys, i
   float2 a[RT][2], u[RT][2], dh[RT][2];
   clear(a);
   clear(dh);
-  product<RT>(Xs, ldr, W, kGuLd, D, a);
   if (GATED) {
     clear(u);
-    product<RT>(Xs, ldr, W + kChunk, kGuLd, D, u);
+    product_pair<RT>(Xs, ldr, W, kGuLd, D, a, u);
+  } else {
+    product<RT>(Xs, ldr, W, kGuLd, D, a);
   }
   product<RT>(Ys, ldr, W + D * kGuLd, kLd, O, dh);
 #pragma unroll
@@ -340,11 +402,11 @@ int dx_smem(int R, int D, int O, int bufs) {
   return 4 * ((D + O) * (R + 4) + 2 * kChunk * (R + 4) + bufs * bwd_floats(D, O));
 }
 int dw_smem(int R, int D, int O) {
-  return 4 * ((D + O) * (R + 4) + 3 * R * kLd + bwd_floats(D, O));
+  return 4 * (2 * (D + O) * (R + 4) + 3 * R * kLd + dw_floats(D, O));
 }
 
 // dx of one tile: all chunks in turn
-template <int ACT, bool GATED, int R>
+template <int ACT, bool GATED, int ND, int R>  // ND: 64-wide pieces of D
 __global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __restrict__ img,
                                                   int bufs) {
   extern __shared__ __align__(16) float sm[];
@@ -360,8 +422,9 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __rest
   copy_chunk(Ws, img, per);
   stage_rows<R>((const float*)p.x, p.ldx, r0, p.M, p.D, Xs);
   stage_rows<R>((const float*)p.dy, p.lddy, r0, p.M, p.O, Ys);
-  float acc[8][RT];  // columns tx + 16 c, rows ty * RT + i
-  clear(acc);
+  float2 acc[ND][RT][2];
+#pragma unroll
+  for (int n = 0; n < ND; ++n) clear(acc[n]);
   for (int ch = 0; ch < nch; ++ch) {
     float* W = Ws + (bufs > 1 ? (ch & 1) * per : 0);
     const bool ahead = bufs > 1 && ch + 1 < nch;
@@ -383,38 +446,27 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __rest
       }
     }
     __syncthreads();
-#pragma unroll 2
-    for (int f = 0; f < kChunk; ++f) {
-      float av[RT], uv[RT];
+    const float* N = W + dw_floats(p.D, p.O);
+    constexpr int ldd = ND * 64 + 4;
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        av[i] = As[f * ldr + ty * RT + i];
-        if (GATED) uv[i] = Us[f * ldr + ty * RT + i];
-      }
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        if (16 * c >= p.D) break;
-        const int d = min(tx + 16 * c, p.D - 1);
-        const float g = W[d * kGuLd + f], v = GATED ? W[d * kGuLd + kChunk + f] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          acc[c][i] = fmaf(av[i], g, acc[c][i]);
-          if (GATED) acc[c][i] = fmaf(uv[i], v, acc[c][i]);
-        }
-      }
+    for (int n = 0; n < ND; ++n) {
+      product<RT>(As, ldr, N + n * 64, ldd, kChunk, acc[n]);
+      if (GATED) product<RT>(Us, ldr, N + kChunk * ldd + n * 64, ldd, kChunk, acc[n]);
     }
     __syncthreads();
     if (bufs == 1 && ch + 1 < nch) copy_chunk(Ws, img + (size_t)(ch + 1) * per, per);
   }
   float* dx = (float*)p.dx;
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
+  for (int n = 0; n < ND; ++n)
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int d = tx + 16 * c;
-      const long long r = r0 + ty * RT + i;
-      if (d < p.D && r < p.M) dx[r * p.lddx + d] = acc[c][i];
-    }
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int d = n * 64 + tx * 4 + j;
+        const long long r = r0 + ty * RT + i;
+        if (d < p.D && r < p.M) dx[r * p.lddx + d] = pick(acc[n][i], j);
+      }
 }
 
 // partial weight gradients of chunk blockIdx.x over the row tiles blockIdx.y, + splits, ...
@@ -422,26 +474,35 @@ template <int ACT, bool GATED, int R>
 __global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p, const float* __restrict__ img) {
   extern __shared__ __align__(16) float sm[];
   constexpr int RT = R / 16, ldr = R + 4;
-  float* Xs = sm;
-  float* Ys = Xs + p.D * ldr;
-  float* As = Ys + p.O * ldr;        // [R rows][68 units] da, du, h
+  float* rows = sm;                  // two tiles' X [D][ldr] and dY [O][ldr]
+  const int both = (p.D + p.O) * ldr;
+  float* As = rows + 2 * both;       // [R rows][68 units] da, du, h
   float* Us = As + R * kLd;
   float* Hs = Us + R * kLd;
   float* W = Hs + R * kLd;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int f0 = blockIdx.x * kChunk, per = bwd_floats(p.D, p.O);
-  copy_chunk(W, img + (size_t)blockIdx.x * per, per);
-  chunks_left(0);
+  copy_chunk(W, img + (size_t)blockIdx.x * per, dw_floats(p.D, p.O));
   float2 ga[8][2], gu[8][2], gd[8][2];  // rows (of D or O) ty + 16 c, units tx * 4 + j
   clear(ga);
   clear(gu);
   clear(gd);
   const int tiles = (int)(((long long)p.M + R - 1) / R);
-  for (int t = blockIdx.y; t < tiles; t += p.splits) {
+  auto fetch = [&](int t, int b) {
+    float* X = rows + b * both;
+    copy_rows<R>((const float*)p.x, p.ldx, (long long)t * R, p.M, p.D, X);
+    copy_rows<R>((const float*)p.dy, p.lddy, (long long)t * R, p.M, p.O, X + p.D * ldr);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if ((int)blockIdx.y < tiles) fetch(blockIdx.y, 0);
+  int b = 0;
+  for (int t = blockIdx.y; t < tiles; t += p.splits, b ^= 1) {
+    const bool ahead = t + p.splits < tiles;
+    if (ahead) fetch(t + p.splits, b ^ 1);
+    chunks_left(ahead);
     __syncthreads();
-    stage_rows<R>((const float*)p.x, p.ldx, (long long)t * R, p.M, p.D, Xs);
-    stage_rows<R>((const float*)p.dy, p.lddy, (long long)t * R, p.M, p.O, Ys);
-    __syncthreads();
+    const float* Xs = rows + b * both;
+    const float* Ys = Xs + p.D * ldr;
     float da[RT][4], du[RT][4], h[RT][4];
     hidden_grads<ACT, GATED, RT>(Xs, Ys, ldr, W, p.D, p.O, da, du, h);
 #pragma unroll
@@ -486,6 +547,7 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p, const float* __rest
         }
       }
     }
+    __syncthreads();  // the tile's place is the one after next's
   }
   const size_t FD = (size_t)p.F * p.D;
   float* part = p.part + blockIdx.y * ((GATED ? 2 : 1) * FD + (size_t)p.O * p.F);
@@ -542,13 +604,20 @@ bool allow_smem(K kernel, int bytes) {
          cudaSuccess;
 }
 
-// rows of a gradient tile: 32 while 64 would leave SMs without one
-int grad_rows(long long M) { return M <= 64 * 148 ? 32 : 64; }
+constexpr int kSmemMax = 232448 - 1024;
+
+// rows of a gradient tile: 64 where they fit and leave no SM without a tile, else 32
+int dw_rows(long long M, int D, int O) {
+  return M > 64 * 148 && dw_smem(64, D, O) <= kSmemMax ? 64 : 32;
+}
+int dx_rows(long long M, int D, int O) {
+  return M > 64 * 148 && dx_smem(64, D, O, 1) <= kSmemMax ? 64 : 32;
+}
 
 // row splits of the weight gradients: enough CTAs for the machine, and at most 8,192 rows a split
 // (an fp32 sum of n products is off by about sqrt(n) 2^-25 of its size)
-int dw_splits(long long M, int F) {
-  const int chunks = (F + kChunk - 1) / kChunk, R = grad_rows(M);
+int dw_splits(long long M, int D, int F, int O) {
+  const int chunks = (F + kChunk - 1) / kChunk, R = dw_rows(M, D, O);
   const long long tiles = (M + R - 1) / R;
   long long s = (148 + chunks - 1) / chunks;
   if (s < (M + 8191) / 8192) s = (M + 8191) / 8192;
@@ -568,8 +637,6 @@ void pack32(const FfnArgs& p, bool backward, float* img, cudaStream_t st) {
   k_pack32<<<dim3((per + kT - 1) / kT, (p.F + kChunk - 1) / kChunk), kT, 0, st>>>(p, backward,
                                                                                   img);
 }
-
-constexpr int kSmemMax = 232448 - 1024;
 
 template <int ACT, bool GATED, int NO, int R>
 int launch_fwd(const FfnArgs& p, const float* img, cudaStream_t st) {
@@ -611,30 +678,39 @@ template <typename T, bool GATED> int run_join(const FfnArgs& p, cudaStream_t st
   return last_error();
 }
 
-template <int ACT, bool GATED, int R>
-int launch_bwd(const FfnArgs& p, const float* img, cudaStream_t st) {
-  if (p.dx && p.M > 0) {
-    const int bufs = dx_smem(R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
-    const int smem = dx_smem(R, p.D, p.O, bufs);
-    if (!allow_smem(k_ffn_dx<ACT, GATED, R>, smem)) return SPLAT_ERR_CUDA;
-    k_ffn_dx<ACT, GATED, R>
-        <<<(unsigned)(((long long)p.M + R - 1) / R), kT, smem, st>>>(p, img, bufs);
-  }
-  if (p.dwg || p.dwu || p.dwd) {
-    const int smem = dw_smem(R, p.D, p.O);
-    if (!allow_smem(k_ffn_dw<ACT, GATED, R>, smem)) return SPLAT_ERR_CUDA;
-    const dim3 grid((p.F + kChunk - 1) / kChunk, p.splits);
-    k_ffn_dw<ACT, GATED, R><<<grid, kT, smem, st>>>(p, img);
-    return run_join<float, GATED>(p, st);
-  }
+template <int ACT, bool GATED, int ND, int R>
+int launch_dx(const FfnArgs& p, const float* img, cudaStream_t st) {
+  const int bufs = dx_smem(R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
+  const int smem = dx_smem(R, p.D, p.O, bufs);
+  if (!allow_smem(k_ffn_dx<ACT, GATED, ND, R>, smem)) return SPLAT_ERR_CUDA;
+  k_ffn_dx<ACT, GATED, ND, R>
+      <<<(unsigned)(((long long)p.M + R - 1) / R), kT, smem, st>>>(p, img, bufs);
   return last_error();
+}
+
+template <int ACT, bool GATED, int R>
+int launch_dw(const FfnArgs& p, const float* img, cudaStream_t st) {
+  const int smem = dw_smem(R, p.D, p.O);
+  if (!allow_smem(k_ffn_dw<ACT, GATED, R>, smem)) return SPLAT_ERR_CUDA;
+  const dim3 grid((p.F + kChunk - 1) / kChunk, p.splits);
+  k_ffn_dw<ACT, GATED, R><<<grid, kT, smem, st>>>(p, img);
+  return run_join<float, GATED>(p, st);
 }
 
 template <int ACT, bool GATED>
 int run_backward(const FfnArgs& p, float* img, cudaStream_t st) {
   pack32(p, true, img, st);
-  return grad_rows(p.M) == 32 ? launch_bwd<ACT, GATED, 32>(p, img, st)
-                              : launch_bwd<ACT, GATED, 64>(p, img, st);
+  int rc = SPLAT_OK;
+  if (p.dx && p.M > 0) {
+    const bool big = dx_rows(p.M, p.D, p.O) == 64;
+    if (p.D <= 64)
+      rc = big ? launch_dx<ACT, GATED, 1, 64>(p, img, st) : launch_dx<ACT, GATED, 1, 32>(p, img, st);
+    else
+      rc = big ? launch_dx<ACT, GATED, 2, 64>(p, img, st) : launch_dx<ACT, GATED, 2, 32>(p, img, st);
+  }
+  if (rc != SPLAT_OK || !(p.dwg || p.dwu || p.dwd)) return rc;
+  return dw_rows(p.M, p.D, p.O) == 64 ? launch_dw<ACT, GATED, 64>(p, img, st)
+                                      : launch_dw<ACT, GATED, 32>(p, img, st);
 }
 
 // A few rows by the clusters; otherwise fp32 on the fp32 lanes, bf16 and fp16 on the tensor cores.
@@ -643,7 +719,7 @@ int run(FfnArgs& p, int dtype, bool backward, void* scratch, cudaStream_t st) {
   if (!backward && p.M <= kFewRows) return run_few<T, ACT, GATED>(p, st);
   if constexpr (sizeof(T) == 4) {
     p.part = (float*)((char*)scratch + pack32_bytes(p.D, p.F, p.O, backward));
-    p.splits = dw_splits(p.M, p.F);
+    p.splits = dw_splits(p.M, p.D, p.F, p.O);
     return backward ? run_backward<ACT, GATED>(p, (float*)scratch, st)
                     : run_forward<ACT, GATED>(p, (float*)scratch, st);
   } else {
@@ -694,7 +770,7 @@ long long splat_ffn_scratch(int M, int D, int F, int O, int dtype, int gated, in
                    : (long long)pack32_bytes(D, F, O, backward != 0);
   if (backward)
     n += (long long)F * ((gated ? 2 : 1) * D + O) * 4 *
-         (tc ? ffn_tc_splits(M, F) : dw_splits(M, F));
+         (tc ? ffn_tc_splits(M, F) : dw_splits(M, D, F, O));
   return (n + 255) & ~255LL;
 }
 
