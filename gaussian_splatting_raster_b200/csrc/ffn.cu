@@ -10,47 +10,57 @@ namespace splat {
 namespace rows {
 namespace {
 
-constexpr int kT = 256;  // 16 x 16 threads: thread (tx, ty) has rows ty * RT .., units tx * 4 ..
+constexpr int kT = 256;
+// UC units are taken at a time: 64 (16 x 16 threads), or 16 (4 x 64) or 4 (1 x 256) for a few hidden
+// units. Thread (tx, ty) has rows ty * RT .. and units (or output columns) tx * 4 .. of every UC.
 
 // ---------------------------------------------------------------------------------------------
 // packed weights and staging
 // ---------------------------------------------------------------------------------------------
-// Per chunk of 64 units: [Wg | Wu]^T as D rows of kGuLd (64 gate, 64 up units); then, forward, Wd^T
-// as 64 rows of down_ld(O), or, for the gradients, Wd as O rows of kLd (64 units) and [Wg; Wu] as
-// 128 rows of down_ld(D): zeros beyond F, D and O. A chunk is then copied to shared memory in
+// Per chunk of UC units: [Wg | Wu]^T as D rows of gu_ld (UC gate, UC up units); then, forward, Wd^T
+// as UC rows of down_ld(O), or, for the gradients, Wd as O rows of h_ld (UC units) and [Wg; Wu] as
+// 2 UC rows of down_ld(D): zeros beyond F, D and O. A chunk is then copied to shared memory in
 // 16-byte pieces, asynchronously, while the one before is worked on (where two fit).
-constexpr int kGuLd = 2 * kChunk + 4;
-constexpr int kLd = kChunk + 4;
+__host__ __device__ constexpr int gu_ld(int UC) { return 2 * UC + 4; }
+__host__ __device__ constexpr int h_ld(int UC) { return UC + 4; }
 __host__ __device__ constexpr int down_ld(int O) { return (O <= 64 ? 64 : 128) + 4; }
-__host__ __device__ constexpr int fwd_floats(int D, int O) {
-  return D * kGuLd + kChunk * down_ld(O);
+__host__ __device__ constexpr int fwd_floats(int UC, int D, int O) {
+  return D * gu_ld(UC) + UC * down_ld(O);
 }
-__host__ __device__ constexpr int dw_floats(int D, int O) { return D * kGuLd + O * kLd; }
-__host__ __device__ constexpr int bwd_floats(int D, int O) {
-  return dw_floats(D, O) + 2 * kChunk * down_ld(D);
+__host__ __device__ constexpr int dw_floats(int UC, int D, int O) {
+  return D * gu_ld(UC) + O * h_ld(UC);
+}
+__host__ __device__ constexpr int bwd_floats(int UC, int D, int O) {
+  return dw_floats(UC, D, O) + 2 * UC * down_ld(D);
 }
 
-__global__ void __launch_bounds__(kT) k_pack32(FfnArgs p, bool backward, float* __restrict__ img) {
-  const int per = backward ? bwd_floats(p.D, p.O) : fwd_floats(p.D, p.O);
-  const int c = blockIdx.y, f0 = c * kChunk;
+__global__ void __launch_bounds__(kT)
+k_pack32(FfnArgs p, int UC, bool backward, float* __restrict__ img) {
+  const int per = backward ? bwd_floats(UC, p.D, p.O) : fwd_floats(UC, p.D, p.O);
+  const int c = blockIdx.y, f0 = c * UC;
   const float *wg = (const float*)p.wg, *wu = (const float*)p.wu, *wd = (const float*)p.wd;
+  // unit j of a chunk's gate and up units: its weights (NULL beyond F)
+  auto unit = [&](int j) -> const float* {
+    const int u = wg && j >= UC ? j - UC : j;
+    if (u >= UC || f0 + u >= p.F) return nullptr;
+    return (wg && j < UC ? wg : wu) + (size_t)(f0 + u) * p.D;
+  };
   for (int i = blockIdx.x * kT + threadIdx.x; i < per; i += gridDim.x * kT) {
     float v = 0.0f;
-    if (i < p.D * kGuLd) {
-      const int k = i / kGuLd, j = i - k * kGuLd;
-      const float* w = wg && j < kChunk ? wg : wu;
-      const int u = wg && j >= kChunk ? j - kChunk : j;
-      if (u < kChunk && f0 + u < p.F) v = w[(size_t)(f0 + u) * p.D + k];
-    } else if (backward && i >= dw_floats(p.D, p.O)) {
-      const int ld = down_ld(p.D), q = i - dw_floats(p.D, p.O), j = q / ld, k = q - j * ld;
-      const float* w = wg && j < kChunk ? wg : wu;
-      const int u = wg && j >= kChunk ? j - kChunk : j;
-      if (u < kChunk && f0 + u < p.F && k < p.D) v = w[(size_t)(f0 + u) * p.D + k];
+    const int q = i - p.D * gu_ld(UC);
+    if (q < 0) {
+      const int k = i / gu_ld(UC);
+      const float* w = unit(i - k * gu_ld(UC));
+      if (w) v = w[k];
+    } else if (backward && i >= dw_floats(UC, p.D, p.O)) {
+      const int ld = down_ld(p.D), r = i - dw_floats(UC, p.D, p.O), k = r % ld;
+      const float* w = unit(r / ld);
+      if (w && k < p.D) v = w[k];
     } else if (backward) {
-      const int o = (i - p.D * kGuLd) / kLd, u = (i - p.D * kGuLd) - o * kLd;
-      if (u < kChunk && f0 + u < p.F) v = wd[(size_t)o * p.F + f0 + u];
+      const int o = q / h_ld(UC), u = q - o * h_ld(UC);
+      if (u < UC && f0 + u < p.F) v = wd[(size_t)o * p.F + f0 + u];
     } else {
-      const int ld = down_ld(p.O), u = (i - p.D * kGuLd) / ld, o = (i - p.D * kGuLd) - u * ld;
+      const int ld = down_ld(p.O), u = q / ld, o = q - u * ld;
       if (o < p.O && f0 + u < p.F) v = wd[(size_t)o * p.F + f0 + u];
     }
     img[(size_t)c * per + i] = v;
@@ -72,23 +82,8 @@ __device__ __forceinline__ void chunks_left(int left) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// rows [r0, r0 + R) of src transposed into dst[k * (R + 4) + r]; rows >= M are zero
-template <int R>
-__device__ __forceinline__ void stage_rows(const float* src, long long lds, long long r0, int M,
-                                           int cols, float* dst) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll 2
-  for (int r = threadIdx.x >> 5; r < R; r += kT / 32) {
-    const bool in = r0 + r < M;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int k = lane + 32 * q;
-      if (k < cols) dst[k * (R + 4) + r] = in ? src[(r0 + r) * lds + k] : 0.0f;
-    }
-  }
-}
-
-// the same as asynchronous copies
+// rows [r0, r0 + R) of src transposed into dst[k * (R + 4) + r] by asynchronous copies; rows >= M are
+// zero
 template <int R>
 __device__ __forceinline__ void copy_rows(const float* src, long long lds, long long r0, int M,
                                           int cols, float* dst) {
@@ -110,16 +105,18 @@ __device__ __forceinline__ void copy_rows(const float* src, long long lds, long 
 }
 
 // acc[i][j] += sum_k rowsT[k][ty RT + i] w[k][tx 4 + j], two units an instruction
-template <int RT>
+template <int RT, int UC>
 __device__ __forceinline__ void product(const float* rowsT, int ldr, const float* w, int ldw,
                                         int K, float2 (&acc)[RT][2]) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = threadIdx.x % (UC / 4), ty = threadIdx.x / (UC / 4);
   const float* xp = rowsT + ty * RT;
   const float* wp = w + tx * 4;
-#pragma unroll 4
+#pragma unroll(RT <= 2 ? 8 : 4)
   for (int k = 0; k < K; ++k, xp += ldr, wp += ldw) {
     float xr[RT];
-    if constexpr (RT == 2) {
+    if constexpr (RT == 1) {
+      xr[0] = *xp;
+    } else if constexpr (RT == 2) {
       *reinterpret_cast<float2*>(xr) = *reinterpret_cast<const float2*>(xp);
     } else {
 #pragma unroll
@@ -137,17 +134,19 @@ __device__ __forceinline__ void product(const float* rowsT, int ldr, const float
   }
 }
 
-// the same with two sets of units, kChunk apart
-template <int RT>
+// the same with two sets of units, UC apart
+template <int RT, int UC>
 __device__ __forceinline__ void product_pair(const float* rowsT, int ldr, const float* w, int ldw,
                                              int K, float2 (&a)[RT][2], float2 (&b)[RT][2]) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = threadIdx.x % (UC / 4), ty = threadIdx.x / (UC / 4);
   const float* xp = rowsT + ty * RT;
   const float* wp = w + tx * 4;
-#pragma unroll 2
+#pragma unroll(RT <= 2 ? 8 : 2)
   for (int k = 0; k < K; ++k, xp += ldr, wp += ldw) {
     float xr[RT];
-    if constexpr (RT == 2) {
+    if constexpr (RT == 1) {
+      xr[0] = *xp;
+    } else if constexpr (RT == 2) {
       *reinterpret_cast<float2*>(xr) = *reinterpret_cast<const float2*>(xp);
     } else {
 #pragma unroll
@@ -155,7 +154,7 @@ __device__ __forceinline__ void product_pair(const float* rowsT, int ldr, const 
         *reinterpret_cast<float4*>(xr + i) = *reinterpret_cast<const float4*>(xp + i);
     }
     const float4 wv = *reinterpret_cast<const float4*>(wp);
-    const float4 vv = *reinterpret_cast<const float4*>(wp + kChunk);
+    const float4 vv = *reinterpret_cast<const float4*>(wp + UC);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const float2 x2 = make_float2(xr[i], xr[i]);
@@ -182,10 +181,12 @@ __device__ __forceinline__ void clear(float (&a)[N][M]) {
 __device__ __forceinline__ float pick(const float2 (&a)[2], int j) {
   return j == 0 ? a[0].x : j == 1 ? a[0].y : j == 2 ? a[1].x : a[1].y;
 }
-// the thread's R / 16 rows of one unit
+// the thread's RT rows of one unit
 template <int RT>
 __device__ __forceinline__ void put_rows(float* dst, const float* v) {
-  if constexpr (RT == 2) {
+  if constexpr (RT == 1) {
+    *dst = v[0];
+  } else if constexpr (RT == 2) {
     *reinterpret_cast<float2*>(dst) = make_float2(v[0], v[1]);
   } else {
 #pragma unroll
@@ -194,30 +195,61 @@ __device__ __forceinline__ void put_rows(float* dst, const float* v) {
   }
 }
 
+// Results (a thread's RT rows of 4 columns in each of N pieces of UC) to a row array. Where one
+// thread has whole rows of 32 columns or more (UC = 4) they go through shared memory (all of it is
+// free; `floats` of it) and out by whole warps: 560,000 rows of 61 took 202 us instead of 263 (of 3
+// columns, 153 instead of 89).
+template <int N, int RT, int UC, int R>
+__device__ __forceinline__ void write_rows(const float2 (&v)[N][RT][2], float* sm, int floats,
+                                           float* dst, long long ld, int cols, long long r0,
+                                           int M) {
+  constexpr int ldr = R + 1;
+  const int tx = threadIdx.x % (UC / 4), ty = threadIdx.x / (UC / 4);
+  const bool through = UC == 4 && cols >= 32 && cols * ldr <= floats;
+  if (through) __syncthreads();
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = n * UC + tx * 4 + j, r = ty * RT + i;
+        if (c >= cols) continue;
+        if (through)
+          sm[c * ldr + r] = pick(v[n][i], j);
+        else if (r0 + r < M)
+          dst[(r0 + r) * ld + c] = pick(v[n][i], j);
+      }
+  if (!through) return;
+  __syncthreads();
+  for (int r = threadIdx.x >> 5; r < R && r0 + r < M; r += kT / 32)
+    for (int c = threadIdx.x & 31; c < cols; c += 32) dst[(r0 + r) * ld + c] = sm[c * ldr + r];
+}
+
 // ---------------------------------------------------------------------------------------------
 // forward, R rows a CTA
 // ---------------------------------------------------------------------------------------------
-int fwd_smem(int R, int D, int O, int bufs) {
-  return 4 * (D * (R + 4) + bufs * fwd_floats(D, O) + kChunk * (R + 4));
+int fwd_smem(int UC, int R, int D, int O, int bufs) {
+  return 4 * (D * (R + 4) + bufs * fwd_floats(UC, D, O) + UC * (R + 4));
 }
 
-template <int ACT, bool GATED, int NO, int R>  // NO: 64-wide pieces of O
+template <int ACT, bool GATED, int NO, int UC, int R>  // NO: 64-wide pieces of O
 __global__ void __launch_bounds__(kT, 1) k_ffn(FfnArgs p, const float* __restrict__ img,
                                                int bufs) {
   extern __shared__ __align__(16) float sm[];
-  constexpr int RT = R / 16, ldr = R + 4, ldo = NO * 64 + 4;
+  constexpr int RT = R * UC / 1024, ldr = R + 4, ldo = NO * 64 + 4, P = 64 / UC;
   float* Xs = sm;                     // [D][ldr]
-  float* Hs = Xs + p.D * ldr;         // [64][ldr]
-  float* Ws = Hs + kChunk * ldr;      // [bufs] of a chunk
-  const int per = fwd_floats(p.D, p.O);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  float* Hs = Xs + p.D * ldr;         // [UC][ldr]
+  float* Ws = Hs + UC * ldr;          // [bufs] of a chunk
+  const int per = fwd_floats(UC, p.D, p.O);
+  const int tx = threadIdx.x % (UC / 4), ty = threadIdx.x / (UC / 4);
   const long long r0 = (long long)blockIdx.x * R;
-  const int nch = (p.F + kChunk - 1) / kChunk;
+  const int nch = (p.F + UC - 1) / UC;
+  copy_rows<R>((const float*)p.x, p.ldx, r0, p.M, p.D, Xs);
   copy_chunk(Ws, img, per);
-  stage_rows<R>((const float*)p.x, p.ldx, r0, p.M, p.D, Xs);
-  float2 yv[NO][RT][2];
+  float2 yv[NO * P][RT][2];
 #pragma unroll
-  for (int n = 0; n < NO; ++n) clear(yv[n]);
+  for (int n = 0; n < NO * P; ++n) clear(yv[n]);
   for (int c = 0; c < nch; ++c) {
     float* W = Ws + (bufs > 1 ? (c & 1) * per : 0);
     const bool ahead = bufs > 1 && c + 1 < nch;
@@ -228,9 +260,9 @@ __global__ void __launch_bounds__(kT, 1) k_ffn(FfnArgs p, const float* __restric
     clear(a);
     if (GATED) {
       clear(u);
-      product_pair<RT>(Xs, ldr, W, kGuLd, p.D, a, u);
+      product_pair<RT, UC>(Xs, ldr, W, gu_ld(UC), p.D, a, u);
     } else {
-      product<RT>(Xs, ldr, W, kGuLd, p.D, a);
+      product<RT, UC>(Xs, ldr, W, gu_ld(UC), p.D, a);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -244,22 +276,14 @@ __global__ void __launch_bounds__(kT, 1) k_ffn(FfnArgs p, const float* __restric
     }
     __syncthreads();
 #pragma unroll
-    for (int n = 0; n < NO; ++n)
-      product<RT>(Hs, ldr, W + p.D * kGuLd + n * 64, ldo, kChunk, yv[n]);
+    for (int n = 0; n < NO * P; ++n)
+      if (n * UC < p.O)
+        product<RT, UC>(Hs, ldr, W + p.D * gu_ld(UC) + n * UC, ldo, UC, yv[n]);
     __syncthreads();
     if (bufs == 1 && c + 1 < nch) copy_chunk(Ws, img + (size_t)(c + 1) * per, per);
   }
-  float* y = (float*)p.y;
-#pragma unroll
-  for (int n = 0; n < NO; ++n)
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int o = n * 64 + tx * 4 + j;
-        const long long r = r0 + ty * RT + i;
-        if (o < p.O && r < p.M) y[r * p.ldy + o] = pick(yv[n][i], j);
-      }
+  write_rows<NO * P, RT, UC, R>(yv, sm, p.D * ldr + UC * ldr + bufs * per, (float*)p.y, p.ldy, p.O,
+                                r0, p.M);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -371,7 +395,7 @@ k_ffn_few(FfnArgs p) {
 // ---------------------------------------------------------------------------------------------
 
 // a, u, dh of one tile and chunk, turned into da, du (and h)
-template <int ACT, bool GATED, int RT>
+template <int ACT, bool GATED, int RT, int UC>
 __device__ __forceinline__ void hidden_grads(const float* Xs, const float* Ys, int ldr,
                                              const float* W, int D, int O, float (&da)[RT][4],
                                              float (&du)[RT][4], float (&h)[RT][4]) {
@@ -380,11 +404,11 @@ __device__ __forceinline__ void hidden_grads(const float* Xs, const float* Ys, i
   clear(dh);
   if (GATED) {
     clear(u);
-    product_pair<RT>(Xs, ldr, W, kGuLd, D, a, u);
+    product_pair<RT, UC>(Xs, ldr, W, gu_ld(UC), D, a, u);
   } else {
-    product<RT>(Xs, ldr, W, kGuLd, D, a);
+    product<RT, UC>(Xs, ldr, W, gu_ld(UC), D, a);
   }
-  product<RT>(Ys, ldr, W + D * kGuLd, kLd, O, dh);
+  product<RT, UC>(Ys, ldr, W + D * gu_ld(UC), h_ld(UC), O, dh);
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -398,33 +422,33 @@ __device__ __forceinline__ void hidden_grads(const float* Xs, const float* Ys, i
     }
 }
 
-int dx_smem(int R, int D, int O, int bufs) {
-  return 4 * ((D + O) * (R + 4) + 2 * kChunk * (R + 4) + bufs * bwd_floats(D, O));
+int dx_smem(int UC, int R, int D, int O, int bufs) {
+  return 4 * ((D + O) * (R + 4) + 2 * UC * (R + 4) + bufs * bwd_floats(UC, D, O));
 }
-int dw_smem(int R, int D, int O) {
-  return 4 * (2 * (D + O) * (R + 4) + 3 * R * kLd + dw_floats(D, O));
+int dw_smem(int UC, int R, int D, int O, int bufs) {
+  return 4 * (bufs * (D + O) * (R + 4) + 3 * R * h_ld(UC) + dw_floats(UC, D, O));
 }
 
 // dx of one tile: all chunks in turn
-template <int ACT, bool GATED, int ND, int R>  // ND: 64-wide pieces of D
+template <int ACT, bool GATED, int ND, int UC, int R>  // ND: 64-wide pieces of D
 __global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __restrict__ img,
                                                   int bufs) {
   extern __shared__ __align__(16) float sm[];
-  constexpr int RT = R / 16, ldr = R + 4;
+  constexpr int RT = R * UC / 1024, ldr = R + 4, P = 64 / UC;
   float* Xs = sm;                    // [D][ldr]
   float* Ys = Xs + p.D * ldr;        // [O][ldr]
-  float* As = Ys + p.O * ldr;        // [64 units][ldr] da, then du
-  float* Us = As + kChunk * ldr;
-  float* Ws = Us + kChunk * ldr;     // [bufs] of a chunk
-  const int per = bwd_floats(p.D, p.O), nch = (p.F + kChunk - 1) / kChunk;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  float* As = Ys + p.O * ldr;        // [UC units][ldr] da, then du
+  float* Us = As + UC * ldr;
+  float* Ws = Us + UC * ldr;         // [bufs] of a chunk
+  const int per = bwd_floats(UC, p.D, p.O), nch = (p.F + UC - 1) / UC;
+  const int tx = threadIdx.x % (UC / 4), ty = threadIdx.x / (UC / 4);
   const long long r0 = (long long)blockIdx.x * R;
+  copy_rows<R>((const float*)p.x, p.ldx, r0, p.M, p.D, Xs);
+  copy_rows<R>((const float*)p.dy, p.lddy, r0, p.M, p.O, Ys);
   copy_chunk(Ws, img, per);
-  stage_rows<R>((const float*)p.x, p.ldx, r0, p.M, p.D, Xs);
-  stage_rows<R>((const float*)p.dy, p.lddy, r0, p.M, p.O, Ys);
-  float2 acc[ND][RT][2];
+  float2 acc[ND * P][RT][2];
 #pragma unroll
-  for (int n = 0; n < ND; ++n) clear(acc[n]);
+  for (int n = 0; n < ND * P; ++n) clear(acc[n]);
   for (int ch = 0; ch < nch; ++ch) {
     float* W = Ws + (bufs > 1 ? (ch & 1) * per : 0);
     const bool ahead = bufs > 1 && ch + 1 < nch;
@@ -432,7 +456,7 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __rest
     chunks_left(ahead);
     __syncthreads();
     float da[RT][4], du[RT][4], h[RT][4];
-    hidden_grads<ACT, GATED, RT>(Xs, Ys, ldr, W, p.D, p.O, da, du, h);
+    hidden_grads<ACT, GATED, RT, UC>(Xs, Ys, ldr, W, p.D, p.O, da, du, h);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float v[RT];
@@ -446,44 +470,38 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __rest
       }
     }
     __syncthreads();
-    const float* N = W + dw_floats(p.D, p.O);
+    const float* N = W + dw_floats(UC, p.D, p.O);
     constexpr int ldd = ND * 64 + 4;
 #pragma unroll
-    for (int n = 0; n < ND; ++n) {
-      product<RT>(As, ldr, N + n * 64, ldd, kChunk, acc[n]);
-      if (GATED) product<RT>(Us, ldr, N + kChunk * ldd + n * 64, ldd, kChunk, acc[n]);
-    }
+    for (int n = 0; n < ND * P; ++n)
+      if (n * UC < p.D) {
+        product<RT, UC>(As, ldr, N + n * UC, ldd, UC, acc[n]);
+        if (GATED) product<RT, UC>(Us, ldr, N + UC * ldd + n * UC, ldd, UC, acc[n]);
+      }
     __syncthreads();
     if (bufs == 1 && ch + 1 < nch) copy_chunk(Ws, img + (size_t)(ch + 1) * per, per);
   }
-  float* dx = (float*)p.dx;
-#pragma unroll
-  for (int n = 0; n < ND; ++n)
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int d = n * 64 + tx * 4 + j;
-        const long long r = r0 + ty * RT + i;
-        if (d < p.D && r < p.M) dx[r * p.lddx + d] = pick(acc[n][i], j);
-      }
+  write_rows<ND * P, RT, UC, R>(acc, sm, (p.D + p.O) * ldr + 2 * UC * ldr + bufs * per,
+                                (float*)p.dx, p.lddx, p.D, r0, p.M);
 }
 
 // partial weight gradients of chunk blockIdx.x over the row tiles blockIdx.y, + splits, ...
-template <int ACT, bool GATED, int R>
-__global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p, const float* __restrict__ img) {
+template <int ACT, bool GATED, int UC, int R>
+__global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p, const float* __restrict__ img,
+                                                  int bufs) {
   extern __shared__ __align__(16) float sm[];
-  constexpr int RT = R / 16, ldr = R + 4;
-  float* rows = sm;                  // two tiles' X [D][ldr] and dY [O][ldr]
+  constexpr int RT = R * UC / 1024, ldr = R + 4, kLd = h_ld(UC);
+  constexpr int TY = 1024 / UC, C = TY < kMaxWidth ? kMaxWidth / TY : 1;  // rows of D or O a thread has: ty + TY c
+  float* rows = sm;                  // [bufs] of X [D][ldr] and dY [O][ldr]
   const int both = (p.D + p.O) * ldr;
-  float* As = rows + 2 * both;       // [R rows][68 units] da, du, h
+  float* As = rows + bufs * both;       // [R rows][kLd units] da, du, h
   float* Us = As + R * kLd;
   float* Hs = Us + R * kLd;
   float* W = Hs + R * kLd;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int f0 = blockIdx.x * kChunk, per = bwd_floats(p.D, p.O);
-  copy_chunk(W, img + (size_t)blockIdx.x * per, dw_floats(p.D, p.O));
-  float2 ga[8][2], gu[8][2], gd[8][2];  // rows (of D or O) ty + 16 c, units tx * 4 + j
+  const int tx = threadIdx.x % (UC / 4), ty = threadIdx.x / (UC / 4);
+  const int f0 = blockIdx.x * UC, per = bwd_floats(UC, p.D, p.O);
+  copy_chunk(W, img + (size_t)blockIdx.x * per, dw_floats(UC, p.D, p.O));
+  float2 ga[C][2], gu[C][2], gd[C][2];
   clear(ga);
   clear(gu);
   clear(gd);
@@ -496,15 +514,15 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p, const float* __rest
   };
   if ((int)blockIdx.y < tiles) fetch(blockIdx.y, 0);
   int b = 0;
-  for (int t = blockIdx.y; t < tiles; t += p.splits, b ^= 1) {
-    const bool ahead = t + p.splits < tiles;
+  for (int t = blockIdx.y; t < tiles; t += p.splits, b ^= bufs - 1) {
+    const bool more = t + p.splits < tiles, ahead = more && bufs > 1;
     if (ahead) fetch(t + p.splits, b ^ 1);
     chunks_left(ahead);
     __syncthreads();
     const float* Xs = rows + b * both;
     const float* Ys = Xs + p.D * ldr;
     float da[RT][4], du[RT][4], h[RT][4];
-    hidden_grads<ACT, GATED, RT>(Xs, Ys, ldr, W, p.D, p.O, da, du, h);
+    hidden_grads<ACT, GATED, RT, UC>(Xs, Ys, ldr, W, p.D, p.O, da, du, h);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int at = (ty * RT + i) * kLd + tx * 4;
@@ -529,8 +547,8 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p, const float* __rest
         g[1] = __ffma2_rn(x2, make_float2(v.z, v.w), g[1]);
       };
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int k = ty + 16 * c;
+      for (int c = 0; c < C; ++c) {
+        const int k = ty + TY * c;
         if (k < p.D) {
           const float2 x = *reinterpret_cast<const float2*>(Xs + k * ldr + r);
           add(ga[c], x.x, av[0]);
@@ -547,15 +565,16 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p, const float* __rest
         }
       }
     }
-    __syncthreads();  // the tile's place is the one after next's
+    __syncthreads();  // the tile's place is free
+    if (more && bufs == 1) fetch(t + p.splits, 0);
   }
   const size_t FD = (size_t)p.F * p.D;
   float* part = p.part + blockIdx.y * ((GATED ? 2 : 1) * FD + (size_t)p.O * p.F);
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
+  for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int k = ty + 16 * c, f = f0 + tx * 4 + j;
+      const int k = ty + TY * c, f = f0 + tx * 4 + j;
       if (f >= p.F) continue;
       if (k < p.D) {
         part[(size_t)f * p.D + k] = pick(ga[c], j);
@@ -606,18 +625,30 @@ bool allow_smem(K kernel, int bytes) {
 
 constexpr int kSmemMax = 232448 - 1024;
 
-// rows of a gradient tile: 64 where they fit and leave no SM without a tile, else 32
-int dw_rows(long long M, int D, int O) {
-  return M > 64 * 148 && dw_smem(64, D, O) <= kSmemMax ? 64 : 32;
+// Units taken at a time: 16 or 4 for a few hidden units, whose chunk of 64 would be mostly zeros (4
+// where its 256-row tiles fit).
+int chunk_of(int D, int F, int O) { return F > 32 ? 64 : F > 4 || D + O > 180 ? 16 : 4; }
+
+// Rows of a tile: `most` where that leaves no SM without a tile and fits, else less. More rows a
+// thread take fewer shared loads a product; more tiles fill the machine.
+bool many(long long M) { return M > 64 * 148; }
+bool few(long long M) { return M <= 16 * 148; }
+int dx_rows(int UC, long long M, int D, int O) {
+  if (UC == 4) return 256;
+  if (UC == 16) return many(M) && dx_smem(16, 128, D, O, 1) <= kSmemMax ? 128 : 64;
+  if (few(M)) return 16;
+  return many(M) && dx_smem(64, 64, D, O, 1) <= kSmemMax ? 64 : 32;
 }
-int dx_rows(long long M, int D, int O) {
-  return M > 64 * 148 && dx_smem(64, D, O, 1) <= kSmemMax ? 64 : 32;
+int dw_rows(int UC, long long M, int D, int O) {
+  if (UC == 4) return 256;
+  const int most = UC == 64 ? 64 : 128;
+  return many(M) && dw_smem(UC, most, D, O, 2) <= kSmemMax ? most : most / 2;
 }
 
 // row splits of the weight gradients: enough CTAs for the machine, and at most 8,192 rows a split
 // (an fp32 sum of n products is off by about sqrt(n) 2^-25 of its size)
 int dw_splits(long long M, int D, int F, int O) {
-  const int chunks = (F + kChunk - 1) / kChunk, R = dw_rows(M, D, O);
+  const int UC = chunk_of(D, F, O), chunks = (F + UC - 1) / UC, R = dw_rows(UC, M, D, O);
   const long long tiles = (M + R - 1) / R;
   long long s = (148 + chunks - 1) / chunks;
   if (s < (M + 8191) / 8192) s = (M + 8191) / 8192;
@@ -627,38 +658,39 @@ int dw_splits(long long M, int D, int F, int O) {
 }
 
 size_t pack32_bytes(int D, int F, int O, bool backward) {
-  const size_t n = (size_t)((F + kChunk - 1) / kChunk) *
-                   (backward ? bwd_floats(D, O) : fwd_floats(D, O)) * 4;
+  const int UC = chunk_of(D, F, O);
+  const size_t n = (size_t)((F + UC - 1) / UC) *
+                   (backward ? bwd_floats(UC, D, O) : fwd_floats(UC, D, O)) * 4;
   return (n + 255) & ~(size_t)255;
 }
 
 void pack32(const FfnArgs& p, bool backward, float* img, cudaStream_t st) {
-  const int per = backward ? bwd_floats(p.D, p.O) : fwd_floats(p.D, p.O);
-  k_pack32<<<dim3((per + kT - 1) / kT, (p.F + kChunk - 1) / kChunk), kT, 0, st>>>(p, backward,
-                                                                                  img);
+  const int UC = chunk_of(p.D, p.F, p.O);
+  const int per = backward ? bwd_floats(UC, p.D, p.O) : fwd_floats(UC, p.D, p.O);
+  k_pack32<<<dim3((per + kT - 1) / kT, (p.F + UC - 1) / UC), kT, 0, st>>>(p, UC, backward, img);
 }
 
-template <int ACT, bool GATED, int NO, int R>
+template <int ACT, bool GATED, int NO, int UC, int R>
 int launch_fwd(const FfnArgs& p, const float* img, cudaStream_t st) {
-  const int bufs = fwd_smem(R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
-  const int smem = fwd_smem(R, p.D, p.O, bufs);
-  if (!allow_smem(k_ffn<ACT, GATED, NO, R>, smem)) return SPLAT_ERR_CUDA;
-  k_ffn<ACT, GATED, NO, R>
+  const int bufs = p.F > UC && fwd_smem(UC, R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
+  const int smem = fwd_smem(UC, R, p.D, p.O, bufs);
+  if (!allow_smem(k_ffn<ACT, GATED, NO, UC, R>, smem)) return SPLAT_ERR_CUDA;
+  k_ffn<ACT, GATED, NO, UC, R>
       <<<(unsigned)(((long long)p.M + R - 1) / R), kT, smem, st>>>(p, img, bufs);
   return last_error();
 }
 
-// Rows of a CTA: 128 feed the lanes best (a thread's 8 x 4 sums take 3 shared loads a step, 2 x 4
-// take 3 as well), 32 where 128 would leave most SMs without a tile.
-template <int ACT, bool GATED>
+template <int ACT, bool GATED, int NO>
 int run_forward(const FfnArgs& p, float* img, cudaStream_t st) {
   pack32(p, false, img, st);
-  const bool small = p.M <= 64 * 148;
-  if (p.O <= 64)
-    return small ? launch_fwd<ACT, GATED, 1, 32>(p, img, st)
-                 : launch_fwd<ACT, GATED, 1, 128>(p, img, st);
-  return small ? launch_fwd<ACT, GATED, 2, 32>(p, img, st)
-               : launch_fwd<ACT, GATED, 2, 128>(p, img, st);
+  const int UC = chunk_of(p.D, p.F, p.O);
+  if (UC == 4) return launch_fwd<ACT, GATED, NO, 4, 256>(p, img, st);
+  if (UC == 16)
+    return many(p.M) ? launch_fwd<ACT, GATED, NO, 16, 128>(p, img, st)
+                     : launch_fwd<ACT, GATED, NO, 16, 64>(p, img, st);
+  return many(p.M)  ? launch_fwd<ACT, GATED, NO, 64, 128>(p, img, st)
+         : few(p.M) ? launch_fwd<ACT, GATED, NO, 64, 16>(p, img, st)
+                    : launch_fwd<ACT, GATED, NO, 64, 32>(p, img, st);
 }
 
 template <typename T, int ACT, bool GATED>
@@ -678,39 +710,52 @@ template <typename T, bool GATED> int run_join(const FfnArgs& p, cudaStream_t st
   return last_error();
 }
 
-template <int ACT, bool GATED, int ND, int R>
+template <int ACT, bool GATED, int ND, int UC, int R>
 int launch_dx(const FfnArgs& p, const float* img, cudaStream_t st) {
-  const int bufs = dx_smem(R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
-  const int smem = dx_smem(R, p.D, p.O, bufs);
-  if (!allow_smem(k_ffn_dx<ACT, GATED, ND, R>, smem)) return SPLAT_ERR_CUDA;
-  k_ffn_dx<ACT, GATED, ND, R>
+  const int bufs = p.F > UC && dx_smem(UC, R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
+  const int smem = dx_smem(UC, R, p.D, p.O, bufs);
+  if (!allow_smem(k_ffn_dx<ACT, GATED, ND, UC, R>, smem)) return SPLAT_ERR_CUDA;
+  k_ffn_dx<ACT, GATED, ND, UC, R>
       <<<(unsigned)(((long long)p.M + R - 1) / R), kT, smem, st>>>(p, img, bufs);
   return last_error();
 }
 
-template <int ACT, bool GATED, int R>
+template <int ACT, bool GATED, int UC, int R>
 int launch_dw(const FfnArgs& p, const float* img, cudaStream_t st) {
-  const int smem = dw_smem(R, p.D, p.O);
-  if (!allow_smem(k_ffn_dw<ACT, GATED, R>, smem)) return SPLAT_ERR_CUDA;
-  const dim3 grid((p.F + kChunk - 1) / kChunk, p.splits);
-  k_ffn_dw<ACT, GATED, R><<<grid, kT, smem, st>>>(p, img);
+  const int bufs = dw_smem(UC, R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
+  const int smem = dw_smem(UC, R, p.D, p.O, bufs);
+  if (!allow_smem(k_ffn_dw<ACT, GATED, UC, R>, smem)) return SPLAT_ERR_CUDA;
+  const dim3 grid((p.F + UC - 1) / UC, p.splits);
+  k_ffn_dw<ACT, GATED, UC, R><<<grid, kT, smem, st>>>(p, img, bufs);
   return run_join<float, GATED>(p, st);
+}
+
+template <int ACT, bool GATED, int ND>
+int run_dx(const FfnArgs& p, const float* img, cudaStream_t st) {
+  const int UC = chunk_of(p.D, p.F, p.O), R = dx_rows(UC, p.M, p.D, p.O);
+  if (UC == 4) return launch_dx<ACT, GATED, ND, 4, 256>(p, img, st);
+  if (UC == 16)
+    return R == 128 ? launch_dx<ACT, GATED, ND, 16, 128>(p, img, st)
+                    : launch_dx<ACT, GATED, ND, 16, 64>(p, img, st);
+  return R == 64   ? launch_dx<ACT, GATED, ND, 64, 64>(p, img, st)
+         : R == 32 ? launch_dx<ACT, GATED, ND, 64, 32>(p, img, st)
+                   : launch_dx<ACT, GATED, ND, 64, 16>(p, img, st);
 }
 
 template <int ACT, bool GATED>
 int run_backward(const FfnArgs& p, float* img, cudaStream_t st) {
   pack32(p, true, img, st);
   int rc = SPLAT_OK;
-  if (p.dx && p.M > 0) {
-    const bool big = dx_rows(p.M, p.D, p.O) == 64;
-    if (p.D <= 64)
-      rc = big ? launch_dx<ACT, GATED, 1, 64>(p, img, st) : launch_dx<ACT, GATED, 1, 32>(p, img, st);
-    else
-      rc = big ? launch_dx<ACT, GATED, 2, 64>(p, img, st) : launch_dx<ACT, GATED, 2, 32>(p, img, st);
-  }
+  if (p.dx && p.M > 0)
+    rc = p.D <= 64 ? run_dx<ACT, GATED, 1>(p, img, st) : run_dx<ACT, GATED, 2>(p, img, st);
   if (rc != SPLAT_OK || !(p.dwg || p.dwu || p.dwd)) return rc;
-  return dw_rows(p.M, p.D, p.O) == 64 ? launch_dw<ACT, GATED, 64>(p, img, st)
-                                      : launch_dw<ACT, GATED, 32>(p, img, st);
+  const int UC = chunk_of(p.D, p.F, p.O), R = dw_rows(UC, p.M, p.D, p.O);
+  if (UC == 4) return launch_dw<ACT, GATED, 4, 256>(p, img, st);
+  if (UC == 16)
+    return R == 128 ? launch_dw<ACT, GATED, 16, 128>(p, img, st)
+                    : launch_dw<ACT, GATED, 16, 64>(p, img, st);
+  return R == 64 ? launch_dw<ACT, GATED, 64, 64>(p, img, st)
+                 : launch_dw<ACT, GATED, 64, 32>(p, img, st);
 }
 
 // A few rows by the clusters; otherwise fp32 on the fp32 lanes, bf16 and fp16 on the tensor cores.
@@ -720,8 +765,9 @@ int run(FfnArgs& p, int dtype, bool backward, void* scratch, cudaStream_t st) {
   if constexpr (sizeof(T) == 4) {
     p.part = (float*)((char*)scratch + pack32_bytes(p.D, p.F, p.O, backward));
     p.splits = dw_splits(p.M, p.D, p.F, p.O);
-    return backward ? run_backward<ACT, GATED>(p, (float*)scratch, st)
-                    : run_forward<ACT, GATED>(p, (float*)scratch, st);
+    if (backward) return run_backward<ACT, GATED>(p, (float*)scratch, st);
+    return p.O <= 64 ? run_forward<ACT, GATED, 1>(p, (float*)scratch, st)
+                     : run_forward<ACT, GATED, 2>(p, (float*)scratch, st);
   } else {
     p.part = (float*)((char*)scratch + ffn_tc_image_bytes(p.D, p.F, p.O, GATED));
     p.splits = ffn_tc_splits(p.M, p.F);

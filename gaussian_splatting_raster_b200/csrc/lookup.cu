@@ -216,6 +216,38 @@ __device__ __forceinline__ int cta_exclusive(int v, int* wsum) {
 // all CTAs up to and including it (at most 2^31 - 1).
 enum : unsigned { kAll = 1u << 31 };
 
+// A few items: CTA 0 sorts them in shared memory (bitonic, on id and row together, so the order is
+// stable), the others clear the runs' bounds.
+constexpr int kFewItems = 2048;
+
+__global__ void __launch_bounds__(kSortThreads) k_sort_few(SortArgs a, int n) {
+  __shared__ unsigned long long s[kFewItems];
+  if (blockIdx.x > 0) {
+    for (unsigned i = (blockIdx.x - 1) * kSortThreads + threadIdx.x; i < a.N;
+         i += (gridDim.x - 1) * kSortThreads)
+      a.bounds[i] = make_uint2(0u, 0u);
+    return;
+  }
+  if (threadIdx.x == 0) *a.unsorted = 1;
+  for (int i = threadIdx.x; i < n; i += kSortThreads)
+    s[i] = i < (int)a.M ? ((unsigned long long)key_of(a.ids[i], a.N) << 32) | (unsigned)i : ~0ULL;
+  for (int k = 2; k <= n; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      __syncthreads();
+      for (int t = threadIdx.x; t < n / 2; t += kSortThreads) {
+        const int i = 2 * t - (t & (j - 1));  // the lower of the pair
+        const unsigned long long lo = s[i], hi = s[i + j];
+        if ((lo > hi) == ((i & k) == 0)) {
+          s[i] = hi;
+          s[i + j] = lo;
+        }
+      }
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < (int)a.M; i += kSortThreads)
+    a.out[i] = make_uint2((uint32_t)(s[i] >> 32), (uint32_t)s[i]);
+}
+
 // items of a thread and tile: ITEMS, each warp's contiguous, a lane's 32 apart
 template <int ITEMS>
 __global__ void __launch_bounds__(kSortThreads, 2) k_sort_pass(SortArgs a) {
@@ -739,22 +771,30 @@ int run_backward(const T* dout, long long ldd, const int* ids, long long M, int 
   q.nblk = p.nblk;
   q.share = p.share;
   uint2* buf[2] = {(uint2*)(scratch + p.pairs0), (uint2*)(scratch + p.pairs1)};
-  const long long words = (long long)(p.clear / 16);
-  k_clear<<<(unsigned)std::min((words + kThreads - 1) / kThreads, 148LL * 8), kThreads, 0, st>>>(
-      (uint4*)scratch, words);
-  const long long want = (std::max(M, (long long)N) + kThreads * 16 - 1) / (kThreads * 16);
-  k_survey<<<(unsigned)std::min(want, 148LL * 4), kThreads, 0, st>>>(q);
-  const int smem = std::max(kSortWarps * p.nd * 4, kSortThreads * p.items * 8) + p.nd * 8 +
-                   kSortWarps * p.nd * 2;
-  auto pass = p.items == 16 ? k_sort_pass<16> : k_sort_pass<4>;
-  if (cudaFuncSetAttribute(pass, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess)
-    return last_error();
-  for (int i = 0; i < p.passes; ++i) {
-    q.pass = i;
-    q.in = buf[(i & 1) ^ 1];
-    q.out = buf[i & 1];
-    pass<<<p.nblk, kSortThreads, smem, st>>>(q);
+  if (M <= kFewItems) {
+    int n = 2;
+    while (n < M) n <<= 1;
+    q.out = buf[(p.passes - 1) & 1];
+    const int clear = std::min((N + kSortThreads - 1) / kSortThreads, 296);
+    k_sort_few<<<1 + clear, kSortThreads, 0, st>>>(q, n);
+  } else {
+    const long long words = (long long)(p.clear / 16);
+    k_clear<<<(unsigned)std::min((words + kThreads - 1) / kThreads, 148LL * 8), kThreads, 0, st>>>(
+        (uint4*)scratch, words);
+    const long long want = (std::max(M, (long long)N) + kThreads * 16 - 1) / (kThreads * 16);
+    k_survey<<<(unsigned)std::min(want, 148LL * 4), kThreads, 0, st>>>(q);
+    const int smem = std::max(kSortWarps * p.nd * 4, kSortThreads * p.items * 8) + p.nd * 8 +
+                     kSortWarps * p.nd * 2;
+    auto pass = p.items == 16 ? k_sort_pass<16> : k_sort_pass<4>;
+    if (cudaFuncSetAttribute(pass, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+        cudaSuccess)
+      return last_error();
+    for (int i = 0; i < p.passes; ++i) {
+      q.pass = i;
+      q.in = buf[(i & 1) ^ 1];
+      q.out = buf[i & 1];
+      pass<<<p.nblk, kSortThreads, smem, st>>>(q);
+    }
   }
   RunArgs a;
   a.ids = ids;

@@ -75,7 +75,8 @@ LOOKUPS = [  # N, M, C, ids, pad, lead
     (1023, 3000, 16, "reverse", 0, 0), (1024, 3000, 19, "uniform", 5, 0),
     (70000, 20000, 8, "uniform", 0, 0), (1, 70000, 4, "uniform", 0, 0),
     (12, 40, 1025, "uniform", 0, 0), (4, 9, 8192, "uniform", 0, 0), (300, 9000, 128, "skewed", 1, 1),
-    (2, 33000, 2, "uniform", 0, 0),
+    (2, 33000, 2, "uniform", 0, 0), (40, 2048, 8, "uniform", 0, 0), (40, 2049, 8, "skewed", 0, 0),
+    (500000, 2047, 3, "outside", 0, 0), (3, 1025, 60, "skewed", 4, 0),
 ]
 
 
@@ -193,6 +194,10 @@ FFNS = [  # M, D, F, O, gated, act, pad
     (40000, 128, 200, 128, True, "silu", 0), (40000, 100, 64, 20, False, "gelu", 0),
     (40000, 40, 70, 128, True, "silu", 0), (60000, 128, 60, 40, True, "gelu", 0),
     (40000, 33, 520, 33, False, "silu", 1), (30000, 128, 100, 128, False, "silu", 0),
+    # a few hidden units, few and many rows
+    (200, 61, 1, 3, True, "silu", 8), (700, 128, 16, 128, True, "gelu", 0),
+    (20000, 61, 1, 3, True, "silu", 8), (20000, 128, 32, 100, False, "gelu", 1),
+    (20000, 70, 17, 64, True, "silu", 0), (12000, 3, 33, 5, True, "gelu", 8),
 ]
 
 
