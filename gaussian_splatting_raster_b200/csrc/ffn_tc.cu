@@ -67,6 +67,7 @@ struct TcArgs {
   int dp, op;           // D and O rounded up to 16
   RowSrc x, dy;
   int out_aligned;      // y's or dx's rows start and end at 16 bytes
+  int out_dense;        // ... lie one behind the other from a 16-byte boundary
   long long tiles;
 };
 
@@ -700,6 +701,41 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       }
       uint8_t* S = smem + h_off + p.nh * kHBytes + g * 16384;
       if (!p.staged) S = smem + h_off + (i % p.nh) * kHBytes;
+      // Rows of odd widths without gaps: the tile is put together as it lies in memory and leaves as
+      // one bulk copy. (Element by element from the swizzled block, 311,296 rows of 35 kept the
+      // groups for as long as everything else.)
+      if (p.staged && p.out_dense && first_row(n) + kTile <= p.f.M) {
+        if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        group_sync();
+        if (half * 32 < cols) {
+          uint32_t v0[16], v1[16];
+          tmem_ld(src, v0);
+          tmem_ld(src + 16, v1);
+          tmem_wait(v0);
+          tmem_wait(v1);
+          uint16_t* q = reinterpret_cast<uint16_t*>(S) + row * cols + half * 32;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const uint32_t w =
+                e < 16 ? Two<T>::pack(__uint_as_float(v0[e & 15]), __uint_as_float(v0[(e + 1) & 15]))
+                       : Two<T>::pack(__uint_as_float(v1[e & 15]), __uint_as_float(v1[(e + 1) & 15]));
+            if (half * 32 + e < cols) q[e] = (uint16_t)w;
+            if (half * 32 + e + 1 < cols) q[e + 1] = (uint16_t)(w >> 16);
+          }
+        }
+        arrive(out_free(n % p.no));
+        group_sync();
+        if (tid == 0) {
+          bulk_store((uint8_t*)(MODE == kFwd ? p.f.y : p.f.dx) + first_row(n) * cols * 2,
+                     smem_addr(S), kTile * cols * 2);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        return;
+      }
+      if (p.staged && p.out_dense) {  // (the last tile: an earlier one may still be leaving)
+        if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        group_sync();
+      }
       for (int b = 0; b * 64 < cols; ++b) {
         if (b * 64 + half * 32 < cols) {
           uint32_t v0[16], v1[16];
@@ -833,6 +869,8 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
     }
     if (MODE != kDw && p.staged && (nch == 1 ? g == (nt & 1) : g == ((nt - 1) & 1)))
       output(nt - 1, total);
+    // (shared memory is read by the bulk copies until they say so)
+    if (MODE != kDw && tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   }
 
   if (MODE == kDw && warp < kGroupWarps) {
@@ -977,8 +1015,13 @@ int launch(TcArgs p, cudaStream_t st) {
       Two<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   p.x = row_src(p.f.x, p.f.ldx, p.f.M, p.f.D, &x_map, type);
   if (MODE != kFwd) p.dy = row_src(p.f.dy, p.f.lddy, p.f.M, p.f.O, &dy_map, type);
-  if (MODE == kFwd) p.out_aligned = aligned16(p.f.y, one ? 0 : p.f.ldy, p.f.O);
-  if (MODE == kDx) p.out_aligned = aligned16(p.f.dx, one ? 0 : p.f.lddx, p.f.D);
+  if (MODE != kDw) {
+    const void* out = MODE == kFwd ? p.f.y : p.f.dx;
+    const long long ld = MODE == kFwd ? p.f.ldy : p.f.lddx;
+    const int cols = MODE == kFwd ? p.f.O : p.f.D;
+    p.out_aligned = aligned16(out, one ? 0 : ld, cols);
+    p.out_dense = !p.out_aligned && ld == cols && cols <= 64 && ((uintptr_t)out & 15) == 0;
+  }
   const int nch = MODE == kDw ? 1 : p.nch;
   if (p.x.tiled) p.x.raw = 0;
   if (p.dy.tiled) p.dy.raw = 0;

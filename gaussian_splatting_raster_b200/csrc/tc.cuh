@@ -95,6 +95,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// contiguous copy shared -> global (16-byte aligned, multiple of 16), in the thread's bulk group
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
+               "r"(bytes)
+               : "memory");
+}
+
 // a box of a two-dimensional tensor map: column x (a multiple of 16 bytes), row y
 __device__ __forceinline__ void tile_load(uint32_t dst, const void* map, int x, int y,
                                           uint32_t bar) {
