@@ -353,7 +353,7 @@ k_ffn_few(FfnArgs p) {
         a = warp_sum(a);
         float h = act_of<ACT>(a);
         if (GATED) h *= warp_sum(b);
-        if (lane == 0 && j0 + u < n) s_h[i][j0 + u] = to_f<T>(from_f<T>(h));
+        if (lane == 0 && j0 + u < n) s_h[i][j0 + u] = h;
       }
   }
   __syncthreads();
@@ -626,8 +626,18 @@ bool allow_smem(K kernel, int bytes) {
 constexpr int kSmemMax = 232448 - 1024;
 
 // Units taken at a time: 16 or 4 for a few hidden units, whose chunk of 64 would be mostly zeros (4
-// where its 256-row tiles fit).
-int chunk_of(int D, int F, int O) { return F > 32 ? 64 : F > 4 || D + O > 180 ? 16 : 4; }
+// where its 256-row tiles fit); 16 also where the other side (O forward, D for dx) is so narrow that
+// pieces of 64 columns would cost more than the better use of a load by 64 units saves, about a
+// third (566,585 rows of 13, 156 units to one column, no gate: 730 us with 64, 359 with 16).
+int chunk_of(int D, int F, int O, bool backward) {
+  if (F <= 4 && D + O <= 180) return 4;
+  if (F <= 32) return 16;
+  auto cost = [&](int UC) {
+    auto up = [&](int c) { return (c + UC - 1) / UC * UC; };
+    return backward ? 2 * D + O + 2 * up(D) : 2 * D + up(O);
+  };
+  return 3 * cost(16) < 2 * cost(64) ? 16 : 64;
+}
 
 // Rows of a tile: `most` where that leaves no SM without a tile and fits, else less. More rows a
 // thread take fewer shared loads a product; more tiles fill the machine.
@@ -648,7 +658,7 @@ int dw_rows(int UC, long long M, int D, int O) {
 // row splits of the weight gradients: enough CTAs for the machine, and at most 8,192 rows a split
 // (an fp32 sum of n products is off by about sqrt(n) 2^-25 of its size)
 int dw_splits(long long M, int D, int F, int O) {
-  const int UC = chunk_of(D, F, O), chunks = (F + UC - 1) / UC, R = dw_rows(UC, M, D, O);
+  const int UC = chunk_of(D, F, O, true), chunks = (F + UC - 1) / UC, R = dw_rows(UC, M, D, O);
   const long long tiles = (M + R - 1) / R;
   long long s = (148 + chunks - 1) / chunks;
   if (s < (M + 8191) / 8192) s = (M + 8191) / 8192;
@@ -658,14 +668,14 @@ int dw_splits(long long M, int D, int F, int O) {
 }
 
 size_t pack32_bytes(int D, int F, int O, bool backward) {
-  const int UC = chunk_of(D, F, O);
+  const int UC = chunk_of(D, F, O, backward);
   const size_t n = (size_t)((F + UC - 1) / UC) *
                    (backward ? bwd_floats(UC, D, O) : fwd_floats(UC, D, O)) * 4;
   return (n + 255) & ~(size_t)255;
 }
 
 void pack32(const FfnArgs& p, bool backward, float* img, cudaStream_t st) {
-  const int UC = chunk_of(p.D, p.F, p.O);
+  const int UC = chunk_of(p.D, p.F, p.O, backward);
   const int per = backward ? bwd_floats(UC, p.D, p.O) : fwd_floats(UC, p.D, p.O);
   k_pack32<<<dim3((per + kT - 1) / kT, (p.F + UC - 1) / UC), kT, 0, st>>>(p, UC, backward, img);
 }
@@ -683,7 +693,7 @@ int launch_fwd(const FfnArgs& p, const float* img, cudaStream_t st) {
 template <int ACT, bool GATED, int NO>
 int run_forward(const FfnArgs& p, float* img, cudaStream_t st) {
   pack32(p, false, img, st);
-  const int UC = chunk_of(p.D, p.F, p.O);
+  const int UC = chunk_of(p.D, p.F, p.O, false);
   if (UC == 4) return launch_fwd<ACT, GATED, NO, 4, 256>(p, img, st);
   if (UC == 16)
     return many(p.M) ? launch_fwd<ACT, GATED, NO, 16, 128>(p, img, st)
@@ -732,7 +742,7 @@ int launch_dw(const FfnArgs& p, const float* img, cudaStream_t st) {
 
 template <int ACT, bool GATED, int ND>
 int run_dx(const FfnArgs& p, const float* img, cudaStream_t st) {
-  const int UC = chunk_of(p.D, p.F, p.O), R = dx_rows(UC, p.M, p.D, p.O);
+  const int UC = chunk_of(p.D, p.F, p.O, true), R = dx_rows(UC, p.M, p.D, p.O);
   if (UC == 4) return launch_dx<ACT, GATED, ND, 4, 256>(p, img, st);
   if (UC == 16)
     return R == 128 ? launch_dx<ACT, GATED, ND, 16, 128>(p, img, st)
@@ -749,7 +759,7 @@ int run_backward(const FfnArgs& p, float* img, cudaStream_t st) {
   if (p.dx && p.M > 0)
     rc = p.D <= 64 ? run_dx<ACT, GATED, 1>(p, img, st) : run_dx<ACT, GATED, 2>(p, img, st);
   if (rc != SPLAT_OK || !(p.dwg || p.dwu || p.dwd)) return rc;
-  const int UC = chunk_of(p.D, p.F, p.O), R = dw_rows(UC, p.M, p.D, p.O);
+  const int UC = chunk_of(p.D, p.F, p.O, true), R = dw_rows(UC, p.M, p.D, p.O);
   if (UC == 4) return launch_dw<ACT, GATED, 4, 256>(p, img, st);
   if (UC == 16)
     return R == 128 ? launch_dw<ACT, GATED, 16, 128>(p, img, st)
@@ -773,6 +783,7 @@ int run(FfnArgs& p, int dtype, bool backward, void* scratch, cudaStream_t st) {
     p.splits = ffn_tc_splits(p.M, p.F);
     const int rc = ffn_tc_run(p, dtype, ACT, backward, scratch, st);
     if (rc != SPLAT_OK || !(p.dwg || p.dwu || p.dwd)) return rc;
+    p.splits *= ffn_tc_parts(p.F);
     return run_join<T, GATED>(p, st);
   }
 }
@@ -816,7 +827,7 @@ long long splat_ffn_scratch(int M, int D, int F, int O, int dtype, int gated, in
                    : (long long)pack32_bytes(D, F, O, backward != 0);
   if (backward)
     n += (long long)F * ((gated ? 2 : 1) * D + O) * 4 *
-         (tc ? ffn_tc_splits(M, F) : dw_splits(M, D, F, O));
+         (tc ? ffn_tc_splits(M, F) * ffn_tc_parts(F) : dw_splits(M, D, F, O));
   return (n + 255) & ~255LL;
 }
 

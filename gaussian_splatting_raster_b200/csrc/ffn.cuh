@@ -55,6 +55,7 @@ __device__ __forceinline__ float act_and_slope(float a, float& slope) {
 // weight gradients, and the kernels but for the splits' sum
 size_t ffn_tc_image_bytes(int D, int F, int O, bool gated);
 int ffn_tc_splits(long long M, int F);
+int ffn_tc_parts(int F);  // partial sums a split leaves
 int ffn_tc_run(const FfnArgs& f, int dtype, int act, bool backward, void* img, cudaStream_t st);
 
 }  // namespace rows

@@ -56,6 +56,12 @@ struct RowSrc {
   int raw;                        // else bytes of a tile as it lies in memory, 0: not staged
 };
 
+// With at most 32 hidden units the chunk's other 32 places hold the same units again, whose hidden
+// values and gradients are stored as what rounding took from the first ones: the second products
+// then have them in twice the bits at no cost. (Sums over few units have little to average the
+// roundings: the weight gradients of one unit were off by several times their own rounding.)
+__host__ __device__ constexpr bool twice(int F) { return F <= 32; }
+
 struct TcArgs {
   FfnArgs f;
   const uint8_t* img;   // packed weights, chunk after chunk
@@ -71,6 +77,12 @@ struct TcArgs {
   long long tiles;
 };
 
+// a - r, nothing where the rounded r is infinite or no number
+__device__ __forceinline__ float left(float a, float r) {
+  return fabsf(r) < __int_as_float(0x7f800000) ? a - r : 0.0f;
+}
+
+// pairs in the type: rounded, and what the rounding left (also rounded)
 template <typename T> struct Two;
 template <> struct Two<__nv_bfloat16> {
   static constexpr bool kBf16 = true;
@@ -78,12 +90,19 @@ template <> struct Two<__nv_bfloat16> {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
   }
+  static __device__ __forceinline__ uint32_t rest(float a, float b) {
+    return pack(left(a, __bfloat162float(__float2bfloat16_rn(a))),
+                left(b, __bfloat162float(__float2bfloat16_rn(b))));
+  }
 };
 template <> struct Two<__half> {
   static constexpr bool kBf16 = false;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __half2 v = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  static __device__ __forceinline__ uint32_t rest(float a, float b) {
+    return pack(left(a, __half2float(__float2half_rn(a))), left(b, __half2float(__float2half_rn(b))));
   }
 };
 
@@ -206,14 +225,15 @@ k_pack(TcArgs p, uint8_t* __restrict__ img) {
   if (q < gu) {
     row = (q >> 3) % WR;
     const int b = (q >> 3) / WR, col = b * 64 + (((q & 7) ^ (row & 7)) << 3);
-    const int f = c * kChunk + (row & 63);
+    const int f = c * kChunk + (twice(p.f.F) ? row & 31 : row & 63);
     if (f < p.f.F) {
       src = (const T*)(GATED && row < 64 ? p.f.wg : p.f.wu) + (size_t)f * p.f.D + col;
       n = p.f.D - col;
     }
   } else {
     row = (q - gu) >> 3;
-    const int col = c * kChunk + ((((q - gu) & 7) ^ (row & 7)) << 3);
+    const int unit = (((q - gu) & 7) ^ (row & 7)) << 3;
+    const int col = c * kChunk + (twice(p.f.F) ? unit & 31 : unit);
     if (row < p.f.O) {
       src = (const T*)p.f.wd + (size_t)row * p.f.F + col;
       n = p.f.F - col;
@@ -391,7 +411,63 @@ __host__ __device__ constexpr int hidden_bytes(int mode, bool gated) {
   return (mode == kFwd ? 1 : (gated ? 2 : 1) + (mode == kDw ? 1 : 0)) * 16384;
 }
 
-template <int MODE, typename T, int ACT, bool GATED>
+// values of a row's hidden operand in the type: rounded, or what rounding took from them
+template <typename T, bool AGAIN>
+__device__ __forceinline__ uint32_t held(float a, float b) {
+  return AGAIN ? Two<T>::rest(a, b) : Two<T>::pack(a, b);
+}
+
+// kUnits units of a row: accumulators (a, u, dh) to the hidden operand's 16-byte pieces piece ..
+template <int MODE, typename T, int ACT, bool GATED, bool AGAIN, int kUnits>
+__device__ __forceinline__ void hidden_units(uint8_t* Hs, int row, int piece,
+                                             const uint32_t (&ra)[kUnits],
+                                             const uint32_t (&ru)[kUnits],
+                                             const uint32_t (&rd)[kUnits]) {
+  uint32_t h[kUnits / 2], da[kUnits / 2], du[kUnits / 2];
+#pragma unroll
+  for (int e = 0; e < kUnits; e += 4) {
+    auto two = [&](const uint32_t (&r)[kUnits], int k) {
+      return make_float2(__uint_as_float(r[e + 2 * k]), __uint_as_float(r[e + 2 * k + 1]));
+    };
+    const float2 a[2] = {two(ra, 0), two(ra, 1)};
+    float2 f[2], sl[2];
+    act4<ACT, MODE != kFwd>(a, f, sl);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float2 u = make_float2(1.0f, 1.0f);
+      if (GATED) u = two(ru, k);
+      if (MODE != kDx) {
+        const float2 v = GATED ? mul2(f[k], u) : f[k];
+        h[e / 2 + k] = held<T, AGAIN>(v.x, v.y);
+      }
+      if (MODE != kFwd) {
+        const float2 dh = two(rd, k);
+        const float2 va = mul2(GATED ? mul2(dh, u) : dh, sl[k]);
+        da[e / 2 + k] = held<T, AGAIN>(va.x, va.y);
+        if (GATED) {
+          const float2 vu = mul2(dh, f[k]);
+          du[e / 2 + k] = held<T, AGAIN>(vu.x, vu.y);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kUnits; e += 8) {
+    uint8_t* at = Hs + row * 128 + (((piece + e / 8) ^ (row & 7)) << 4);
+    auto put = [&](int block, const uint32_t* v) {
+      *reinterpret_cast<uint4*>(at + block * 16384) = make_uint4(v[0], v[1], v[2], v[3]);
+    };
+    if (MODE == kFwd) {
+      put(0, h + e / 2);
+    } else {
+      put(0, da + e / 2);
+      if (GATED) put(1, du + e / 2);
+      if (MODE == kDw) put(GATED ? 2 : 1, h + e / 2);
+    }
+  }
+}
+
+template <int MODE, typename T, int ACT, bool GATED, bool TWICE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x_map,
          const __grid_constant__ CUtensorMap dy_map) {
@@ -668,6 +744,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
     const int g = warp / kGroupWarps, tid = threadIdx.x & (kGroupThreads - 1);
     const uint32_t row_lanes = (uint32_t)(warp & 3) << 21;  // 32 * quadrant in the lane field
     const int row = (warp & 3) * 32 + lane, half = (warp >> 2) & 1;
+    const bool second = TWICE && half == 1;  // this warp's units are there again
     auto arrive = [&](uint32_t bar) {
       fence_async_shared();
       fence_before();
@@ -786,49 +863,11 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
     };
     auto work = [&](uint8_t* Hs, int q, const uint32_t (&ra)[kUnits], const uint32_t (&ru)[kUnits],
                     const uint32_t (&rd)[kUnits]) {
-      uint32_t h[kUnits / 2], da[kUnits / 2], du[kUnits / 2];
-#pragma unroll
-      for (int e = 0; e < kUnits; e += 4) {
-        auto two = [&](const uint32_t (&r)[kUnits], int k) {
-          return make_float2(__uint_as_float(r[e + 2 * k]), __uint_as_float(r[e + 2 * k + 1]));
-        };
-        const float2 a[2] = {two(ra, 0), two(ra, 1)};
-        float2 f[2], sl[2];
-        act4<ACT, MODE != kFwd>(a, f, sl);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float2 u = make_float2(1.0f, 1.0f);
-          if (GATED) u = two(ru, k);
-          if (MODE != kDx) {
-            const float2 v = GATED ? mul2(f[k], u) : f[k];
-            h[e / 2 + k] = Two<T>::pack(v.x, v.y);
-          }
-          if (MODE != kFwd) {
-            const float2 dh = two(rd, k);
-            const float2 va = mul2(GATED ? mul2(dh, u) : dh, sl[k]);
-            da[e / 2 + k] = Two<T>::pack(va.x, va.y);
-            if (GATED) {
-              const float2 vu = mul2(dh, f[k]);
-              du[e / 2 + k] = Two<T>::pack(vu.x, vu.y);
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < kUnits; e += 8) {
-        const int piece = half * 4 + (q * kUnits + e) / 8;
-        uint8_t* at = Hs + row * 128 + ((piece ^ (row & 7)) << 4);
-        auto put = [&](int block, const uint32_t* v) {
-          *reinterpret_cast<uint4*>(at + block * 16384) = make_uint4(v[0], v[1], v[2], v[3]);
-        };
-        if (MODE == kFwd) {
-          put(0, h + e / 2);
-        } else {
-          put(0, da + e / 2);
-          if (GATED) put(1, du + e / 2);
-          if (MODE == kDw) put(GATED ? 2 : 1, h + e / 2);
-        }
-      }
+      const int piece = half * 4 + q * kUnits / 8;
+      if (TWICE && second)
+        hidden_units<MODE, T, ACT, GATED, true, kUnits>(Hs, row, piece, ra, ru, rd);
+      else
+        hidden_units<MODE, T, ACT, GATED, false, kUnits>(Hs, row, piece, ra, ru, rd);
     };
 
     int c = g, n = 0;
@@ -878,8 +917,10 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
     const int row = (warp & 3) * 32 + lane, half = warp >> 2;
     const uint32_t row_lanes = (uint32_t)(warp & 3) << 21;
     const size_t FD = (size_t)p.f.F * p.f.D;
-    float* part = p.f.part + (size_t)me * ((GATED ? 2 : 1) * FD + (size_t)p.f.F * p.f.O);
-    const int f = chunk0 * kChunk + (row & 63);
+    constexpr bool two = TWICE;
+    float* part = p.f.part + (size_t)(two ? 2 * me + ((row >> 5) & 1) : me) *
+                                 ((GATED ? 2 : 1) * FD + (size_t)p.f.F * p.f.O);
+    const int f = chunk0 * kChunk + (two ? row & 31 : row & 63);
     if (nt > 0) {
       mbar_drain(all_done, 0);
       fence_after();
@@ -1040,7 +1081,8 @@ int launch(TcArgs p, cudaStream_t st) {
   p.no = fit.no;
   const long long grid =
       MODE == kDw ? (long long)p.nch * p.f.splits : std::min(p.tiles, 148LL);
-  auto kernel = k_ffn_tc<MODE, T, ACT, GATED>;
+  auto kernel = twice(p.f.F) ? k_ffn_tc<MODE, T, ACT, GATED, true>
+                             : k_ffn_tc<MODE, T, ACT, GATED, false>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, fit.smem) !=
       cudaSuccess)
     return SPLAT_ERR_CUDA;
@@ -1087,6 +1129,8 @@ int ffn_tc_splits(long long M, int F) {
   const long long tiles = (M + kTile - 1) / kTile, s = 148 / chunks;
   return (int)std::max(1LL, std::min(s, tiles));
 }
+
+int ffn_tc_parts(int F) { return twice(F) ? 2 : 1; }
 
 int ffn_tc_run(const FfnArgs& f, int dtype, int act, bool backward, void* img, cudaStream_t st) {
   return dtype == SPLAT_BF16 ? run_type<__nv_bfloat16>(f, act, backward, (uint8_t*)img, st)

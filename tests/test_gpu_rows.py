@@ -76,7 +76,9 @@ LOOKUPS = [  # N, M, C, ids, pad, lead
     (70000, 20000, 8, "uniform", 0, 0), (1, 70000, 4, "uniform", 0, 0),
     (12, 40, 1025, "uniform", 0, 0), (4, 9, 8192, "uniform", 0, 0), (300, 9000, 128, "skewed", 1, 1),
     (2, 33000, 2, "uniform", 0, 0), (40, 2048, 8, "uniform", 0, 0), (40, 2049, 8, "skewed", 0, 0),
-    (500000, 2047, 3, "outside", 0, 0), (3, 1025, 60, "skewed", 4, 0),
+    (500000, 2047, 3, "outside", 0, 0), (50001, 3, 33, "uniform", 0, 0), (3, 1025, 60, "skewed", 4, 0),
+    (60000, 20000, 20, "skewed", 0, 0), (60001, 30000, 11, "same", 0, 0),
+    (60000, 2000, 130, "sorted", 0, 0), (100001, 40000, 3, "outside", 0, 0),
 ]
 
 
@@ -396,6 +398,18 @@ def test_ffn_rows_anywhere(P, dt, shift):
     dw = torch.empty_like(w[0])
     P.ffn_backward(dy.cuda(), xv, *w, dw_gate=dw, act="gelu")
     R.close(dw, ref["dw_gate"], "dw_gate")
+
+
+def test_ids_anywhere_and_status(P):
+    """Ids that do not start at 16 bytes, sorted and not; nothing of all this ran out of time."""
+    g = _gen(6)
+    for kind in ("uniform", "sorted"):
+        ids = _ids(kind, 30001, 700, g)
+        d = torch.randn(30000, 6, generator=g)
+        out = torch.empty(700, 6, device="cuda")
+        P.lookup_backward(d.cuda(), ids.cuda()[1:], out)
+        R.close(out, R.lookup_grad_ref(d, ids[1:], 700, 1.0))
+    P.rows_status()
 
 
 # -- streams, graphs, refusals --------------------------------------------------------------------
