@@ -12,16 +12,23 @@
 // hidden values twice.
 //
 // A CTA's work is one sequence of items, (tile, chunk) or tiles. Two groups of eight warps turn
-// accumulators into hidden values, item by item in turn; one warp issues all MMAs, the first
-// products of up to three items ahead of the second product of the item that is ready; one thread
-// loads weights. So the tensor cores and the groups wait for one another only at the ends of the
-// sequence: what bounds a narrow block is the groups' arithmetic (special function unit and issue
-// slots), a wide one the tensor cores. (With an accumulator per group, a group waited about as
-// long for its products as it worked on them.) Weights are packed once per call into the layout the
-// MMAs read (zeros beyond F, D and O), so a chunk is one contiguous bulk copy; all chunks stay in
-// shared memory where they fit. Row tiles are read with plain loads, which take any row distance
-// and alignment (token rows have odd widths), straight into the swizzled layout, a tile or two
-// ahead.
+// accumulators into hidden values, item by item in turn; one warp issues the first products, up to
+// three items ahead, and loads weights; one warp issues the second products of the items that are
+// ready; two warps bring row tiles in. So the tensor cores and the groups wait for one another only
+// at the ends of the sequence: what bounds a narrow block is the groups' arithmetic (special
+// function unit and issue slots), a wide one the tensor cores and L2. (With an accumulator per
+// group, a group waited about as long for its products as it worked on them.) Weights are packed
+// once per call into the layout the MMAs read (zeros beyond F, D and O), so a chunk is one
+// contiguous bulk copy; all chunks stay in shared memory where they fit. Row tiles come through a
+// tensor map where rows are 16-byte aligned; else (token rows have odd widths) as one bulk copy of
+// the bytes a tile spans, which the loaders lay out from shared memory; at the array's ends,
+// element by element.
+//
+// Measured, bf16: forward, 917,504 rows of 64 / 256 / 64 silu 196 us (307 TFLOP/s of products;
+// issue slots 57 %, special function unit 48 %, tensor pipe 22 %; 139 us without the activation,
+// 120 without the groups' work), 200,000 rows of 128 / 512 / 128 122 us (645 TFLOP/s). Gradients,
+// 311,296 rows of 64 / 128 / 64: dx 54 us, weights 63; of 35 / 128 / 48 in rows 76 bytes apart,
+// where the loaders bound it, 113 and 105. Few tiles (1,000 rows) take 8 us, 14 us a gradient.
 #include <cuda.h>
 
 #include <algorithm>
@@ -779,8 +786,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       uint8_t* S = smem + h_off + p.nh * kHBytes + g * 16384;
       if (!p.staged) S = smem + h_off + (i % p.nh) * kHBytes;
       // Rows of odd widths without gaps: the tile is put together as it lies in memory and leaves as
-      // one bulk copy. (Element by element from the swizzled block, 311,296 rows of 35 kept the
-      // groups for as long as everything else.)
+      // one bulk copy.
       if (p.staged && p.out_dense && first_row(n) + kTile <= p.f.M) {
         if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         group_sync();
