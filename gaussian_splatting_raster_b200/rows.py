@@ -16,6 +16,7 @@ from . import SplatError, load_library
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _ACTS = {"silu": 0, "gelu": 1}
+_MAX = 2**31 - 1  # the library's sizes are 32-bit
 
 
 def _rows(t, name, like, shape):
@@ -28,6 +29,8 @@ def _rows(t, name, like, shape):
         raise ValueError(f"{name} is on {t.device}, expected {like.device}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if max(shape) > _MAX:
+        raise ValueError(f"{name} has a side of more than {_MAX}: {shape}")
     if t.numel() == 0:
         return None, shape[1]
     ld, step = t.stride()
@@ -60,6 +63,8 @@ def _ids(ids, like):
         raise TypeError("ids must be a CUDA tensor")
     if ids.dtype != torch.int32:
         raise TypeError(f"ids must be torch.int32, got {ids.dtype}")
+    if ids.numel() > _MAX:
+        raise ValueError(f"ids has more than {_MAX} entries")
     if ids.dim() != 1 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous vector")
     if ids.get_device() != like.get_device():
@@ -175,9 +180,10 @@ def ffn_backward(dy, x, w_gate, w_up, w_down, dx=None, dw_gate=None, dw_up=None,
 
 
 def rows_status(stream=None):
-    """Raise SplatError(DEVICE_TIMEOUT) when a bounded wait of a feed-forward kernel ran out on the
-    current device since the last call (waits for the stream)."""
+    """Raise SplatError(DEVICE_TIMEOUT) when a bounded wait of these kernels ran out since the last
+    call, on the stream's device (None: the current stream); waits for the stream."""
     s = stream if stream is not None else torch.cuda.current_stream()
-    rc = load_library().splat_rows_status(s.cuda_stream)
+    with torch.cuda.device(s.device):
+        rc = load_library().splat_rows_status(s.cuda_stream)
     if rc != 0:
         raise SplatError(rc, "a bounded wait ran out" if rc == -6 else "reading the status failed")

@@ -109,8 +109,10 @@ class FeedForward:
 def token_features(out: Outputs, block: FeedForward, feats, stream=None):
     """The score tokens' projection (feats [G, O] from the tokens of the last score replay; the
     rendering calls are fp32, so a bf16 or fp16 block gets its tokens rounded first)."""
-    ffn(out.tokens.to(block.w_up.dtype), block.w_gate, block.w_up, block.w_down, feats, block.act,
-        stream)
+    import torch
+    with torch.cuda.stream(stream):  # None: the current stream
+        ffn(out.tokens.to(block.w_up.dtype), block.w_gate, block.w_up, block.w_down, feats,
+            block.act)
 
 
 @dataclasses.dataclass

@@ -573,3 +573,36 @@ def test_decode_render_and_back(P, dt):
     runner.token_features(out, runner.FeedForward(None, wu.cuda(), wd.cuda()), feats)
     R.close(feats, R.ffn_ref(out.tokens.to(dt).cpu(), None, wu, wd, "gelu")["y"])
     ws.close()
+
+
+def test_token_features_stream(P):
+    """Everything of the call runs on the given stream: the current one is busy meanwhile."""
+    from types import SimpleNamespace
+    from gaussian_splatting_raster_b200 import runner
+    dt = torch.bfloat16
+    x, _, wu, wd, _ = _ffn_inputs(700, 21, 40, 12, False, dt, 7)
+    out = SimpleNamespace(tokens=x.float().cuda())
+    block = runner.FeedForward(None, wu.cuda(), wd.cuda())
+    feats = torch.empty((700, 12), dtype=dt, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(200_000_000)  # about 0.1 s
+    runner.token_features(out, block, feats, stream=s)
+    s.synchronize()
+    with torch.cuda.stream(s):
+        got = feats.cpu()
+    torch.cuda.synchronize()
+    R.close(got, R.ffn_ref(x, None, wu, wd, "gelu")["y"])
+    P.rows_status(s)
+
+
+def test_sizes_beyond_32_bits(P):
+    """Sizes the library's 32-bit arguments cannot hold are refused, not cut off."""
+    n = 2**32 + 1
+    x, w, y = (torch.zeros(1, 1, device="cuda") for _ in range(3))
+    with pytest.raises(ValueError, match="more than"):
+        P.ffn(x.expand(n, 1), None, w, w, y.expand(n, 1))
+    with pytest.raises(ValueError, match="more than"):
+        P.lookup(x, torch.zeros(1, dtype=torch.int32, device="cuda").expand(n), y.expand(n, 1))
+    with pytest.raises(ValueError, match="more than"):
+        P.lookup(x.expand(n, 1), torch.zeros(1, dtype=torch.int32, device="cuda"), y)
