@@ -5,7 +5,9 @@
 // product reads along rows). Bound by the fp32 lanes and by the shared-memory loads that feed them:
 // 2 M F (2 D + O) operations against 4 M (D + O) bytes, which at D = 57, F = 256, O = 64 is 188
 // operations a byte. There 200,000 rows take 448 us (41 TFLOP/s, 55 % of the lanes' 74); the
-// gradients of 100,000 rows 493 us for dx (30 TFLOP/s) and 799 us for the weights (23).
+// gradients of 100,000 rows 490 us for dx (30 TFLOP/s) and 692 us for the weights (26).
+#include <algorithm>
+
 #include "ffn.cuh"
 
 namespace splat {
@@ -143,7 +145,7 @@ __device__ __forceinline__ void product_pair(const float* rowsT, int ldr, const 
   const int tx = threadIdx.x % (UC / 4), ty = threadIdx.x / (UC / 4);
   const float* xp = rowsT + ty * RT;
   const float* wp = w + tx * 4;
-#pragma unroll(RT <= 2 ? 8 : 2)
+#pragma unroll(RT <= 2 ? 8 : 4)
   for (int k = 0; k < K; ++k, xp += ldr, wp += ldw) {
     float xr[RT];
     if constexpr (RT == 1) {
@@ -426,8 +428,11 @@ __device__ __forceinline__ void hidden_grads(const float* Xs, const float* Ys, i
     }
 }
 
+// bufs 0: the chunk's two halves (for the hidden values, for dx) take turns in one place
 int dx_smem(int UC, int R, int D, int O, int bufs) {
-  return 4 * ((D + O) * (R + 4) + 2 * UC * (R + 4) + bufs * bwd_floats(UC, D, O));
+  const int half = std::max(dw_floats(UC, D, O), 2 * UC * down_ld(D));
+  return 4 * ((D + O) * (R + 4) + 2 * UC * (R + 4) +
+              (bufs ? bufs * bwd_floats(UC, D, O) : half));
 }
 int dw_smem(int UC, int R, int D, int O, int bufs) {
   return 4 * (bufs * (D + O) * (R + 4) + 3 * R * h_ld(UC) + dw_floats(UC, D, O));
@@ -449,7 +454,8 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __rest
   const long long r0 = (long long)blockIdx.x * R;
   copy_rows<R>((const float*)p.x, p.ldx, r0, p.M, p.D, Xs);
   copy_rows<R>((const float*)p.dy, p.lddy, r0, p.M, p.O, Ys);
-  copy_chunk(Ws, img, per);
+  const int first = dw_floats(UC, p.D, p.O);  // a chunk's part for the hidden values
+  copy_chunk(Ws, img, bufs ? per : first);
   float2 acc[ND * P][RT][2];
 #pragma unroll
   for (int n = 0; n < ND * P; ++n) clear(acc[n]);
@@ -461,6 +467,10 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __rest
     __syncthreads();
     float da[RT][4], du[RT][4], h[RT][4];
     hidden_grads<ACT, GATED, RT, UC>(Xs, Ys, ldr, W, p.D, p.O, da, du, h);
+    if (bufs == 0) {
+      __syncthreads();
+      copy_chunk(Ws, img + (size_t)ch * per + first, per - first);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float v[RT];
@@ -473,8 +483,9 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __rest
         put_rows<RT>(Us + (tx * 4 + j) * ldr + ty * RT, v);
       }
     }
+    if (bufs == 0) chunks_left(0);
     __syncthreads();
-    const float* N = W + dw_floats(UC, p.D, p.O);
+    const float* N = bufs ? W + first : Ws;
     constexpr int ldd = ND * 64 + 4;
 #pragma unroll
     for (int n = 0; n < ND * P; ++n)
@@ -483,7 +494,8 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __rest
         if (GATED) product<RT, UC>(Us, ldr, N + UC * ldd + n * UC, ldd, UC, acc[n]);
       }
     __syncthreads();
-    if (bufs == 1 && ch + 1 < nch) copy_chunk(Ws, img + (size_t)(ch + 1) * per, per);
+    if (bufs < 2 && ch + 1 < nch)
+      copy_chunk(Ws, img + (size_t)(ch + 1) * per, bufs ? per : first);
   }
   write_rows<ND * P, RT, UC, R>(acc, sm, (p.D + p.O) * ldr + 2 * UC * ldr + bufs * per,
                                 (float*)p.dx, p.lddx, p.D, r0, p.M);
@@ -550,22 +562,25 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p, const float* __rest
         g[0] = __ffma2_rn(x2, make_float2(v.x, v.y), g[0]);
         g[1] = __ffma2_rn(x2, make_float2(v.z, v.w), g[1]);
       };
+      float2 x[C], y[C];  // all loads first, then the products without a wait
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int k = ty + TY * c;
-        if (k < p.D) {
-          const float2 x = *reinterpret_cast<const float2*>(Xs + k * ldr + r);
-          add(ga[c], x.x, av[0]);
-          add(ga[c], x.y, av[1]);
+        x[c] = *reinterpret_cast<const float2*>(Xs + min(ty + TY * c, p.D - 1) * ldr + r);
+        y[c] = *reinterpret_cast<const float2*>(Ys + min(ty + TY * c, p.O - 1) * ldr + r);
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (TY * c < p.D) {
+          add(ga[c], x[c].x, av[0]);
+          add(ga[c], x[c].y, av[1]);
           if (GATED) {
-            add(gu[c], x.x, uv[0]);
-            add(gu[c], x.y, uv[1]);
+            add(gu[c], x[c].x, uv[0]);
+            add(gu[c], x[c].y, uv[1]);
           }
         }
-        if (k < p.O) {
-          const float2 y = *reinterpret_cast<const float2*>(Ys + k * ldr + r);
-          add(gd[c], y.x, hv[0]);
-          add(gd[c], y.y, hv[1]);
+        if (TY * c < p.O) {
+          add(gd[c], y[c].x, hv[0]);
+          add(gd[c], y[c].y, hv[1]);
         }
       }
     }
@@ -651,12 +666,12 @@ int dx_rows(int UC, long long M, int D, int O) {
   if (UC == 4) return 256;
   if (UC == 16) return many(M) && dx_smem(16, 128, D, O, 1) <= kSmemMax ? 128 : 64;
   if (few(M)) return 16;
-  return many(M) && dx_smem(64, 64, D, O, 1) <= kSmemMax ? 64 : 32;
+  return many(M) ? 64 : 32;
 }
 int dw_rows(int UC, long long M, int D, int O) {
   if (UC == 4) return 256;
   const int most = UC == 64 ? 64 : 128;
-  return many(M) && dw_smem(UC, most, D, O, 2) <= kSmemMax ? most : most / 2;
+  return many(M) && dw_smem(UC, most, D, O, 1) <= kSmemMax ? most : most / 2;
 }
 
 // row splits of the weight gradients: enough CTAs for the machine, and at most 8,192 rows a split
@@ -664,8 +679,11 @@ int dw_rows(int UC, long long M, int D, int O) {
 int dw_splits(long long M, int D, int F, int O) {
   const int UC = chunk_of(D, F, O, true), chunks = (F + UC - 1) / UC, R = dw_rows(UC, M, D, O);
   const long long tiles = (M + R - 1) / R;
-  long long s = (148 + chunks - 1) / chunks;
-  if (s < (M + 8191) / 8192) s = (M + 8191) / 8192;
+  const long long least = std::max((M + 8191) / 8192, 1LL), waves = (least * chunks + 147) / 148;
+  // where an SM holds one CTA, no wave of CTAs is left with a few
+  long long s = dw_smem(UC, R, D, O, 1) > kSmemMax / 2 ? waves * 148 / chunks
+                                                        : (waves * 148 + chunks - 1) / chunks;
+  if (s < least) s = least;
   if (s > tiles) s = tiles;
   if (s > 65535) s = 65535;  // the grid's limit
   return (int)(s < 1 ? 1 : s);
@@ -726,7 +744,9 @@ template <typename T, bool GATED> int run_join(const FfnArgs& p, cudaStream_t st
 
 template <int ACT, bool GATED, int ND, int UC, int R>
 int launch_dx(const FfnArgs& p, const float* img, cudaStream_t st) {
-  const int bufs = p.F > UC && dx_smem(UC, R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
+  const int bufs = p.F > UC && dx_smem(UC, R, p.D, p.O, 2) <= kSmemMax ? 2
+                   : dx_smem(UC, R, p.D, p.O, 1) <= kSmemMax           ? 1
+                                                                       : 0;
   const int smem = dx_smem(UC, R, p.D, p.O, bufs);
   if (!allow_smem(k_ffn_dx<ACT, GATED, ND, UC, R>, smem)) return SPLAT_ERR_CUDA;
   k_ffn_dx<ACT, GATED, ND, UC, R>
