@@ -230,6 +230,45 @@ __device__ __forceinline__ void write_rows(const float2 (&v)[N][RT][2], float* s
     for (int c = threadIdx.x & 31; c < cols; c += 32) dst[(r0 + r) * ld + c] = sm[c * ldr + r];
 }
 
+// The CTAs of a cluster (S of them, along y) have the same rows and every S-th chunk of units each:
+// their results are added in order, each CTA adding and writing R / S of the rows.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+constexpr int join_floats(int R, int width) { return R * (width + 4); }
+
+template <int N, int RT, int UC, int R>
+__device__ __forceinline__ void join_rows(const float2 (&v)[N][RT][2], float* sm, float* dst,
+                                          long long ld, int cols, long long r0, int M) {
+  constexpr int ldc = N * UC + 4;
+  const int tx = threadIdx.x % (UC / 4), ty = threadIdx.x / (UC / 4);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      *reinterpret_cast<float4*>(sm + (ty * RT + i) * ldc + n * UC + tx * 4) =
+          make_float4(v[n][i][0].x, v[n][i][0].y, v[n][i][1].x, v[n][i][1].y);
+  cluster_barrier();
+  const int S = gridDim.y, per = R / S, f = blockIdx.y * per;
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(sm);
+  for (int r = f + (threadIdx.x >> 5); r < f + per && r0 + r < M; r += kT / 32)
+    for (int c = threadIdx.x & 31; c < cols; c += 32) {
+      float sum = 0.0f;
+      for (int q = 0; q < S; ++q) {
+        uint32_t at;
+        float w;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(at)
+                     : "r"(base + 4 * (r * ldc + c)), "r"(q));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(at) : "memory");
+        sum += w;
+      }
+      dst[(r0 + r) * ld + c] = sum;
+    }
+  cluster_barrier();  // until all have read this CTA's sums
+}
+
 // ---------------------------------------------------------------------------------------------
 // forward, R rows a CTA
 // ---------------------------------------------------------------------------------------------
@@ -249,15 +288,16 @@ __global__ void __launch_bounds__(kT, 1) k_ffn(FfnArgs p, const float* __restric
   const int tx = threadIdx.x % (UC / 4), ty = threadIdx.x / (UC / 4);
   const long long r0 = (long long)blockIdx.x * R;
   const int nch = (p.F + UC - 1) / UC;
+  const int S = gridDim.y, c0 = blockIdx.y;  // the cluster's CTAs; the first chunk of this one
   copy_rows<R>((const float*)p.x, p.ldx, r0, p.M, p.D, Xs);
-  copy_chunk(Ws, img, per);
+  copy_chunk(Ws, img + (size_t)c0 * per, per);
   float2 yv[NO * P][RT][2];
 #pragma unroll
   for (int n = 0; n < NO * P; ++n) clear(yv[n]);
-  for (int c = 0; c < nch; ++c) {
-    float* W = Ws + (bufs > 1 ? (c & 1) * per : 0);
-    const bool ahead = bufs > 1 && c + 1 < nch;
-    if (ahead) copy_chunk(Ws + ((c + 1) & 1) * per, img + (size_t)(c + 1) * per, per);
+  for (int c = c0, b = 0; c < nch; c += S, b ^= bufs - 1) {
+    float* W = Ws + b * per;
+    const bool more = c + S < nch, ahead = bufs > 1 && more;
+    if (ahead) copy_chunk(Ws + (b ^ 1) * per, img + (size_t)(c + S) * per, per);
     chunks_left(ahead);
     __syncthreads();
     float2 a[RT][2], u[RT][2];
@@ -284,8 +324,13 @@ __global__ void __launch_bounds__(kT, 1) k_ffn(FfnArgs p, const float* __restric
       if (n * UC < p.O)
         product<RT, UC>(Hs, ldr, W + p.D * gu_ld(UC) + n * UC, ldo, UC, yv[n]);
     __syncthreads();
-    if (bufs == 1 && c + 1 < nch) copy_chunk(Ws, img + (size_t)(c + 1) * per, per);
+    if (bufs == 1 && more) copy_chunk(Ws, img + (size_t)(c + S) * per, per);
   }
+  if constexpr (UC >= 16)
+    if (S > 1) {
+      join_rows<NO * P, RT, UC, R>(yv, sm, (float*)p.y, p.ldy, p.O, r0, p.M);
+      return;
+    }
   write_rows<NO * P, RT, UC, R>(yv, sm, p.D * ldr + UC * ldr + bufs * per, (float*)p.y, p.ldy, p.O,
                                 r0, p.M);
 }
@@ -455,14 +500,15 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __rest
   copy_rows<R>((const float*)p.x, p.ldx, r0, p.M, p.D, Xs);
   copy_rows<R>((const float*)p.dy, p.lddy, r0, p.M, p.O, Ys);
   const int first = dw_floats(UC, p.D, p.O);  // a chunk's part for the hidden values
-  copy_chunk(Ws, img, bufs ? per : first);
+  const int S = gridDim.y, c0 = blockIdx.y;  // the cluster's CTAs; the first chunk of this one
+  copy_chunk(Ws, img + (size_t)c0 * per, bufs ? per : first);
   float2 acc[ND * P][RT][2];
 #pragma unroll
   for (int n = 0; n < ND * P; ++n) clear(acc[n]);
-  for (int ch = 0; ch < nch; ++ch) {
-    float* W = Ws + (bufs > 1 ? (ch & 1) * per : 0);
-    const bool ahead = bufs > 1 && ch + 1 < nch;
-    if (ahead) copy_chunk(Ws + ((ch + 1) & 1) * per, img + (size_t)(ch + 1) * per, per);
+  for (int ch = c0, b = 0; ch < nch; ch += S, b ^= bufs > 1) {
+    float* W = Ws + b * per;
+    const bool more = ch + S < nch, ahead = bufs > 1 && more;
+    if (ahead) copy_chunk(Ws + (b ^ 1) * per, img + (size_t)(ch + S) * per, per);
     chunks_left(ahead);
     __syncthreads();
     float da[RT][4], du[RT][4], h[RT][4];
@@ -494,9 +540,13 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __rest
         if (GATED) product<RT, UC>(Us, ldr, N + UC * ldd + n * UC, ldd, UC, acc[n]);
       }
     __syncthreads();
-    if (bufs < 2 && ch + 1 < nch)
-      copy_chunk(Ws, img + (size_t)(ch + 1) * per, bufs ? per : first);
+    if (bufs < 2 && more) copy_chunk(Ws, img + (size_t)(ch + S) * per, bufs ? per : first);
   }
+  if constexpr (UC >= 16)
+    if (S > 1) {
+      join_rows<ND * P, RT, UC, R>(acc, sm, (float*)p.dx, p.lddx, p.D, r0, p.M);
+      return;
+    }
   write_rows<ND * P, RT, UC, R>(acc, sm, (p.D + p.O) * ldr + 2 * UC * ldr + bufs * per,
                                 (float*)p.dx, p.lddx, p.D, r0, p.M);
 }
@@ -658,16 +708,33 @@ int chunk_of(int D, int F, int O, bool backward) {
   return 3 * cost(16) < 2 * cost(64) ? 16 : 64;
 }
 
-// Rows of a tile: `most` where that leaves no SM without a tile and fits, else less. More rows a
-// thread take fewer shared loads a product; more tiles fill the machine.
-bool many(long long M) { return M > 64 * 148; }
-bool few(long long M) { return M <= 16 * 148; }
-int dx_rows(int UC, long long M, int D, int O) {
-  if (UC == 4) return 256;
-  if (UC == 16) return many(M) && dx_smem(16, 128, D, O, 1) <= kSmemMax ? 128 : 64;
-  if (few(M)) return 16;
-  return many(M) ? 64 : 32;
+// Rows of a tile and CTAs of its cluster. A thread's products of RT rows by 4 (or, of both inputs,
+// 8) units read RT + 4 (RT + 8) words from shared memory for each input column, which is what bounds
+// them, so tall tiles read least a row; short ones and clusters, which share a tile's chunks, fill
+// the machine (of which 15 clusters of eight or 33 of four have place at once). The time of a choice
+// is about its waves of CTAs times the words a warp reads, 600 more a chunk for its barriers and
+// 1,000 a CTA, or 2,500 with a cluster's join. (Forward, 128 / 1024 / 128 gated: 300 rows 30 us, without
+// clusters 148; 20,000 rows 432 us, 667; gradients of 1,000 rows of 57 / 256 / 64: dx 13 us, 34.)
+struct Tile { int R, S; };
+Tile tile_of(int UC, int most, bool backward, long long M, int D, int F, int O, bool gated) {
+  const int nch = (F + UC - 1) / UC, wide = gated ? 8 : 4;
+  const int least = UC == 4 ? 256 : UC == 16 ? 64 : 16;
+  if (UC == 4) return {256, 1};
+  Tile best = {most, 1};
+  double t = 1e300;
+  for (int R = most; R >= least; R >>= 1)
+    for (int S = 1; S <= 8 && S <= nch; S <<= 1) {
+      const int RT = R * UC / 1024, out = ((backward ? D : O) + UC - 1) / UC * UC;
+      double words = (double)D * (RT + wide) + (double)out * (RT + 4);
+      if (backward) words += (double)O * (RT + 4) + (gated ? (double)out * (RT + 4) : 0.0);
+      const long long ctas = (M + R - 1) / R * S, fit = S == 8 ? 120 : S == 4 ? 132 : 148;
+      const double cost = (double)((ctas + fit - 1) / fit) *
+                          ((nch + S - 1) / S * (words + 600) + (S > 1 ? 2500 : 1000));
+      if (cost < t) t = cost, best = {R, S};
+    }
+  return best;
 }
+bool many(long long M) { return M > 64 * 148; }
 int dw_rows(int UC, long long M, int D, int O) {
   if (UC == 4) return 256;
   const int most = UC == 64 ? 64 : 128;
@@ -702,27 +769,52 @@ void pack32(const FfnArgs& p, bool backward, float* img, cudaStream_t st) {
   k_pack32<<<dim3((per + kT - 1) / kT, (p.F + UC - 1) / UC), kT, 0, st>>>(p, UC, backward, img);
 }
 
+// `kernel` on tiles of R rows, each taken by a cluster of S CTAs
+template <typename K>
+int launch_tiles(K kernel, const FfnArgs& p, const float* img, int bufs, int smem, int R, int S,
+                 cudaStream_t st) {
+  if (!allow_smem(kernel, smem)) return SPLAT_ERR_CUDA;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)(((long long)p.M + R - 1) / R), S);
+  c.blockDim = dim3(kT);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 1;
+  at.val.clusterDim.y = S;
+  at.val.clusterDim.z = 1;
+  c.attrs = &at;
+  c.numAttrs = S > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&c, kernel, p, img, bufs) != cudaSuccess) {
+    cudaGetLastError();
+    return SPLAT_ERR_CUDA;
+  }
+  return SPLAT_OK;
+}
+
 template <int ACT, bool GATED, int NO, int UC, int R>
-int launch_fwd(const FfnArgs& p, const float* img, cudaStream_t st) {
-  const int bufs = p.F > UC && fwd_smem(UC, R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
-  const int smem = fwd_smem(UC, R, p.D, p.O, bufs);
-  if (!allow_smem(k_ffn<ACT, GATED, NO, UC, R>, smem)) return SPLAT_ERR_CUDA;
-  k_ffn<ACT, GATED, NO, UC, R>
-      <<<(unsigned)(((long long)p.M + R - 1) / R), kT, smem, st>>>(p, img, bufs);
-  return last_error();
+int launch_fwd(const FfnArgs& p, const float* img, int S, cudaStream_t st) {
+  const int bufs = p.F > UC * S && fwd_smem(UC, R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
+  const int smem = std::max(fwd_smem(UC, R, p.D, p.O, bufs), S > 1 ? 4 * join_floats(R, NO * 64) : 0);
+  return launch_tiles(k_ffn<ACT, GATED, NO, UC, R>, p, img, bufs, smem, R, S, st);
 }
 
 template <int ACT, bool GATED, int NO>
 int run_forward(const FfnArgs& p, float* img, cudaStream_t st) {
   pack32(p, false, img, st);
   const int UC = chunk_of(p.D, p.F, p.O, false);
-  if (UC == 4) return launch_fwd<ACT, GATED, NO, 4, 256>(p, img, st);
+  const Tile t = tile_of(UC, 128, false, p.M, p.D, p.F, p.O, GATED);
+  if (UC == 4) return launch_fwd<ACT, GATED, NO, 4, 256>(p, img, 1, st);
   if (UC == 16)
-    return many(p.M) ? launch_fwd<ACT, GATED, NO, 16, 128>(p, img, st)
-                     : launch_fwd<ACT, GATED, NO, 16, 64>(p, img, st);
-  return many(p.M)  ? launch_fwd<ACT, GATED, NO, 64, 128>(p, img, st)
-         : few(p.M) ? launch_fwd<ACT, GATED, NO, 64, 16>(p, img, st)
-                    : launch_fwd<ACT, GATED, NO, 64, 32>(p, img, st);
+    return t.R == 128 ? launch_fwd<ACT, GATED, NO, 16, 128>(p, img, t.S, st)
+                      : launch_fwd<ACT, GATED, NO, 16, 64>(p, img, t.S, st);
+  switch (t.R) {
+    case 128: return launch_fwd<ACT, GATED, NO, 64, 128>(p, img, t.S, st);
+    case 64: return launch_fwd<ACT, GATED, NO, 64, 64>(p, img, t.S, st);
+    case 32: return launch_fwd<ACT, GATED, NO, 64, 32>(p, img, t.S, st);
+  }
+  return launch_fwd<ACT, GATED, NO, 64, 16>(p, img, t.S, st);
 }
 
 template <typename T, int ACT, bool GATED>
@@ -743,15 +835,12 @@ template <typename T, bool GATED> int run_join(const FfnArgs& p, cudaStream_t st
 }
 
 template <int ACT, bool GATED, int ND, int UC, int R>
-int launch_dx(const FfnArgs& p, const float* img, cudaStream_t st) {
-  const int bufs = p.F > UC && dx_smem(UC, R, p.D, p.O, 2) <= kSmemMax ? 2
-                   : dx_smem(UC, R, p.D, p.O, 1) <= kSmemMax           ? 1
-                                                                       : 0;
-  const int smem = dx_smem(UC, R, p.D, p.O, bufs);
-  if (!allow_smem(k_ffn_dx<ACT, GATED, ND, UC, R>, smem)) return SPLAT_ERR_CUDA;
-  k_ffn_dx<ACT, GATED, ND, UC, R>
-      <<<(unsigned)(((long long)p.M + R - 1) / R), kT, smem, st>>>(p, img, bufs);
-  return last_error();
+int launch_dx(const FfnArgs& p, const float* img, int S, cudaStream_t st) {
+  const int bufs = p.F > UC * S && dx_smem(UC, R, p.D, p.O, 2) <= kSmemMax ? 2
+                   : dx_smem(UC, R, p.D, p.O, 1) <= kSmemMax               ? 1
+                                                                           : 0;
+  const int smem = std::max(dx_smem(UC, R, p.D, p.O, bufs), S > 1 ? 4 * join_floats(R, ND * 64) : 0);
+  return launch_tiles(k_ffn_dx<ACT, GATED, ND, UC, R>, p, img, bufs, smem, R, S, st);
 }
 
 template <int ACT, bool GATED, int UC, int R>
@@ -766,14 +855,16 @@ int launch_dw(const FfnArgs& p, const float* img, cudaStream_t st) {
 
 template <int ACT, bool GATED, int ND>
 int run_dx(const FfnArgs& p, const float* img, cudaStream_t st) {
-  const int UC = chunk_of(p.D, p.F, p.O, true), R = dx_rows(UC, p.M, p.D, p.O);
-  if (UC == 4) return launch_dx<ACT, GATED, ND, 4, 256>(p, img, st);
+  const int UC = chunk_of(p.D, p.F, p.O, true);
+  const int most = UC == 16 && dx_smem(16, 128, p.D, p.O, 1) > kSmemMax ? 64 : UC == 16 ? 128 : 64;
+  const Tile t = tile_of(UC, most, true, p.M, p.D, p.F, p.O, GATED);
+  if (UC == 4) return launch_dx<ACT, GATED, ND, 4, 256>(p, img, 1, st);
   if (UC == 16)
-    return R == 128 ? launch_dx<ACT, GATED, ND, 16, 128>(p, img, st)
-                    : launch_dx<ACT, GATED, ND, 16, 64>(p, img, st);
-  return R == 64   ? launch_dx<ACT, GATED, ND, 64, 64>(p, img, st)
-         : R == 32 ? launch_dx<ACT, GATED, ND, 64, 32>(p, img, st)
-                   : launch_dx<ACT, GATED, ND, 64, 16>(p, img, st);
+    return t.R == 128 ? launch_dx<ACT, GATED, ND, 16, 128>(p, img, t.S, st)
+                      : launch_dx<ACT, GATED, ND, 16, 64>(p, img, t.S, st);
+  return t.R == 64   ? launch_dx<ACT, GATED, ND, 64, 64>(p, img, t.S, st)
+         : t.R == 32 ? launch_dx<ACT, GATED, ND, 64, 32>(p, img, t.S, st)
+                     : launch_dx<ACT, GATED, ND, 64, 16>(p, img, t.S, st);
 }
 
 template <int ACT, bool GATED>
