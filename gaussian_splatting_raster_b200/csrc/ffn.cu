@@ -170,6 +170,22 @@ __device__ __forceinline__ void product_pair(const float* rowsT, int ldr, const 
   }
 }
 
+// acc[n] += the product with columns n UC .. of w, up to `cols` of them, two sets at a time
+template <int N, int RT, int UC>
+__device__ __forceinline__ void products(const float* rowsT, int ldr, const float* w, int ldw, int K,
+                                         int cols, float2 (&acc)[N][RT][2]) {
+#pragma unroll
+  for (int n = 0; n < N; n += 2) {
+    if constexpr (N > 1) {
+      if ((n + 1) * UC < cols) {
+        product_pair<RT, UC>(rowsT, ldr, w + n * UC, ldw, K, acc[n], acc[n + 1]);
+        continue;
+      }
+    }
+    if (n * UC < cols) product<RT, UC>(rowsT, ldr, w + n * UC, ldw, K, acc[n]);
+  }
+}
+
 template <int N>
 __device__ __forceinline__ void clear(float2 (&a)[N][2]) {
 #pragma unroll
@@ -319,10 +335,7 @@ __global__ void __launch_bounds__(kT, 1) k_ffn(FfnArgs p, const float* __restric
       put_rows<RT>(Hs + (tx * 4 + j) * ldr + ty * RT, h);
     }
     __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NO * P; ++n)
-      if (n * UC < p.O)
-        product<RT, UC>(Hs, ldr, W + p.D * gu_ld(UC) + n * UC, ldo, UC, yv[n]);
+    products<NO * P, RT, UC>(Hs, ldr, W + p.D * gu_ld(UC), ldo, UC, p.O, yv);
     __syncthreads();
     if (bufs == 1 && more) copy_chunk(Ws, img + (size_t)(c + S) * per, per);
   }
@@ -533,12 +546,8 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dx(FfnArgs p, const float* __rest
     __syncthreads();
     const float* N = bufs ? W + first : Ws;
     constexpr int ldd = ND * 64 + 4;
-#pragma unroll
-    for (int n = 0; n < ND * P; ++n)
-      if (n * UC < p.D) {
-        product<RT, UC>(As, ldr, N + n * UC, ldd, UC, acc[n]);
-        if (GATED) product<RT, UC>(Us, ldr, N + UC * ldd + n * UC, ldd, UC, acc[n]);
-      }
+    products<ND * P, RT, UC>(As, ldr, N, ldd, UC, p.D, acc);
+    if (GATED) products<ND * P, RT, UC>(Us, ldr, N + UC * ldd, ldd, UC, p.D, acc);
     __syncthreads();
     if (bufs < 2 && more) copy_chunk(Ws, img + (size_t)(ch + S) * per, bufs ? per : first);
   }
@@ -725,8 +734,9 @@ Tile tile_of(int UC, int most, bool backward, long long M, int D, int F, int O, 
   for (int R = most; R >= least; R >>= 1)
     for (int S = 1; S <= 8 && S <= nch; S <<= 1) {
       const int RT = R * UC / 1024, out = ((backward ? D : O) + UC - 1) / UC * UC;
-      double words = (double)D * (RT + wide) + (double)out * (RT + 4);
-      if (backward) words += (double)O * (RT + 4) + (gated ? (double)out * (RT + 4) : 0.0);
+      const double second = out > UC ? out * 0.5 * (RT + 8) : (double)out * (RT + 4);
+      double words = (double)D * (RT + wide) + second;
+      if (backward) words += (double)O * (RT + 4) + (gated ? second : 0.0);
       const long long ctas = (M + R - 1) / R * S, fit = S == 8 ? 120 : S == 4 ? 132 : 148;
       const double cost = (double)((ctas + fit - 1) / fit) *
                           ((nch + S - 1) / S * (words + 600) + (S > 1 ? 2500 : 1000));

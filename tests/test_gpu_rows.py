@@ -196,6 +196,9 @@ FFNS = [  # M, D, F, O, gated, act, pad
     (40000, 128, 200, 128, True, "silu", 0), (40000, 100, 64, 20, False, "gelu", 0),
     (40000, 40, 70, 128, True, "silu", 0), (60000, 128, 60, 40, True, "gelu", 0),
     (40000, 33, 520, 33, False, "silu", 1), (30000, 128, 100, 128, False, "silu", 0),
+    # chunks of units that a cluster cannot share evenly
+    (5001, 57, 700, 64, True, "gelu", 3), (1500, 90, 449, 127, False, "silu", 1),
+    (300, 128, 1000, 3, True, "silu", 0),
     # a few hidden units, few and many rows
     (200, 61, 1, 3, True, "silu", 8), (700, 128, 16, 128, True, "gelu", 0),
     (20000, 61, 1, 3, True, "silu", 8), (20000, 128, 32, 100, False, "gelu", 1),
