@@ -905,10 +905,10 @@ int run(FfnArgs& p, int dtype, bool backward, void* scratch, cudaStream_t st) {
                      : run_forward<ACT, GATED, 2>(p, (float*)scratch, st);
   } else {
     p.part = (float*)((char*)scratch + ffn_tc_image_bytes(p.D, p.F, p.O, GATED));
-    p.splits = ffn_tc_splits(p.M, p.F);
+    p.splits = ffn_tc_splits(p.M, p.D, p.F, p.O);
     const int rc = ffn_tc_run(p, dtype, ACT, backward, scratch, st);
     if (rc != SPLAT_OK || !(p.dwg || p.dwu || p.dwd)) return rc;
-    p.splits *= ffn_tc_parts(p.F);
+    p.splits *= ffn_tc_parts(p.D, p.F, p.O);
     return run_join<T, GATED>(p, st);
   }
 }
@@ -952,7 +952,7 @@ long long splat_ffn_scratch(int M, int D, int F, int O, int dtype, int gated, in
                    : (long long)pack32_bytes(D, F, O, backward != 0);
   if (backward)
     n += (long long)F * ((gated ? 2 : 1) * D + O) * 4 *
-         (tc ? ffn_tc_splits(M, F) * ffn_tc_parts(F) : dw_splits(M, D, F, O));
+         (tc ? ffn_tc_splits(M, D, F, O) * ffn_tc_parts(D, F, O) : dw_splits(M, D, F, O));
   return (n + 255) & ~255LL;
 }
 

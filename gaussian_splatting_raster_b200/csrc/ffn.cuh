@@ -54,8 +54,8 @@ __device__ __forceinline__ float act_and_slope(float a, float& slope) {
 // tensor-core kernels (ffn_tc.cu; bf16 and fp16): bytes of the packed weights, row splits of the
 // weight gradients, and the kernels but for the splits' sum
 size_t ffn_tc_image_bytes(int D, int F, int O, bool gated);
-int ffn_tc_splits(long long M, int F);
-int ffn_tc_parts(int F);  // partial sums a split leaves
+int ffn_tc_splits(long long M, int D, int F, int O);
+int ffn_tc_parts(int D, int F, int O);  // partial sums a split leaves
 int ffn_tc_run(const FfnArgs& f, int dtype, int act, bool backward, void* img, cudaStream_t st);
 
 }  // namespace rows

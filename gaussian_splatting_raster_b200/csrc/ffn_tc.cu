@@ -63,16 +63,22 @@ struct RowSrc {
   int raw;                        // else bytes of a tile as it lies in memory, 0: not staged
 };
 
-// With at most 32 hidden units the chunk's other 32 places hold the same units again, whose hidden
-// values and gradients are stored as what rounding took from the first ones: the second products
-// then have them in twice the bits at no cost. (Sums over few units have little to average the
-// roundings: the weight gradients of one unit were off by several times their own rounding.)
-__host__ __device__ constexpr bool twice(int F) { return F <= 32; }
+// Narrow blocks take 32 hidden units a chunk, and its other 32 places hold the same units again,
+// whose hidden values and gradients are stored as what rounding took from the first ones: the second
+// products then have them in twice the bits. With at most 32 hidden units that is free; otherwise it
+// costs the groups' work twice (758,527 rows of 2 / 104 / 21: 236 us instead of 120). Sums over few units, or
+// over units that are functions of few inputs, have little to average the roundings: the weight
+// gradients of one unit were off by several times their own rounding, outputs of two inputs by 1.5
+// times. (About D^2 / 4 products of inputs in O outputs are independent.)
+__host__ __device__ constexpr bool twice(int D, int F, int O) { return F <= 32 || D * D * O < 512; }
+// units of a chunk
+__host__ __device__ constexpr int units(int D, int F, int O) { return twice(D, F, O) ? 32 : kChunk; }
 
 struct TcArgs {
   FfnArgs f;
   const uint8_t* img;   // packed weights, chunk after chunk
   int nch, stage_bytes; // chunks; bytes of one
+  int units;            // hidden units of a chunk: 64, or 32 that are there twice
   int nst, nx, nh;      // weight stages, row tiles and hidden operands in shared memory
   int ngu, no;          // accumulators of first products and of outputs in TMEM
   int staged;           // outputs have places of their own in shared memory
@@ -232,7 +238,7 @@ k_pack(TcArgs p, uint8_t* __restrict__ img) {
   if (q < gu) {
     row = (q >> 3) % WR;
     const int b = (q >> 3) / WR, col = b * 64 + (((q & 7) ^ (row & 7)) << 3);
-    const int f = c * kChunk + (twice(p.f.F) ? row & 31 : row & 63);
+    const int f = c * p.units + (row & (p.units - 1));
     if (f < p.f.F) {
       src = (const T*)(GATED && row < 64 ? p.f.wg : p.f.wu) + (size_t)f * p.f.D + col;
       n = p.f.D - col;
@@ -240,7 +246,7 @@ k_pack(TcArgs p, uint8_t* __restrict__ img) {
   } else {
     row = (q - gu) >> 3;
     const int unit = (((q - gu) & 7) ^ (row & 7)) << 3;
-    const int col = c * kChunk + (twice(p.f.F) ? unit & 31 : unit);
+    const int col = c * p.units + (unit & (p.units - 1));
     if (row < p.f.O) {
       src = (const T*)p.f.wd + (size_t)row * p.f.F + col;
       n = p.f.F - col;
@@ -926,7 +932,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
     constexpr bool two = TWICE;
     float* part = p.f.part + (size_t)(two ? 2 * me + ((row >> 5) & 1) : me) *
                                  ((GATED ? 2 : 1) * FD + (size_t)p.f.F * p.f.O);
-    const int f = chunk0 * kChunk + (two ? row & 31 : row & 63);
+    const int f = chunk0 * p.units + (two ? row & 31 : row & 63);
     if (nt > 0) {
       mbar_drain(all_done, 0);
       fence_after();
@@ -1087,8 +1093,8 @@ int launch(TcArgs p, cudaStream_t st) {
   p.no = fit.no;
   const long long grid =
       MODE == kDw ? (long long)p.nch * p.f.splits : std::min(p.tiles, 148LL);
-  auto kernel = twice(p.f.F) ? k_ffn_tc<MODE, T, ACT, GATED, true>
-                             : k_ffn_tc<MODE, T, ACT, GATED, false>;
+  auto kernel = p.units < kChunk ? k_ffn_tc<MODE, T, ACT, GATED, true>
+                                 : k_ffn_tc<MODE, T, ACT, GATED, false>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, fit.smem) !=
       cudaSuccess)
     return SPLAT_ERR_CUDA;
@@ -1101,7 +1107,8 @@ int run(const FfnArgs& f, bool backward, uint8_t* img, cudaStream_t st) {
   TcArgs p = {};
   p.f = f;
   p.img = img;
-  p.nch = (f.F + kChunk - 1) / kChunk;
+  p.units = units(f.D, f.F, f.O);
+  p.nch = (f.F + p.units - 1) / p.units;
   p.stage_bytes = stage_bytes(f.D, f.O, GATED);
   p.dp = pad16(f.D);
   p.op = pad16(f.O);
@@ -1127,16 +1134,17 @@ int run_type(const FfnArgs& f, int act, bool backward, uint8_t* img, cudaStream_
 }  // namespace
 
 size_t ffn_tc_image_bytes(int D, int F, int O, bool gated) {
-  return (size_t)((F + kChunk - 1) / kChunk) * stage_bytes(D, O, gated);
+  const int n = units(D, F, O);
+  return (size_t)((F + n - 1) / n) * stage_bytes(D, O, gated);
 }
 
-int ffn_tc_splits(long long M, int F) {
-  const int chunks = (F + kChunk - 1) / kChunk;
+int ffn_tc_splits(long long M, int D, int F, int O) {
+  const int n = units(D, F, O), chunks = (F + n - 1) / n;
   const long long tiles = (M + kTile - 1) / kTile, s = 148 / chunks;
   return (int)std::max(1LL, std::min(s, tiles));
 }
 
-int ffn_tc_parts(int F) { return twice(F) ? 2 : 1; }
+int ffn_tc_parts(int D, int F, int O) { return twice(D, F, O) ? 2 : 1; }
 
 int ffn_tc_run(const FfnArgs& f, int dtype, int act, bool backward, void* img, cudaStream_t st) {
   return dtype == SPLAT_BF16 ? run_type<__nv_bfloat16>(f, act, backward, (uint8_t*)img, st)

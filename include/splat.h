@@ -392,14 +392,15 @@ int splat_lookup_backward(const void* dout, long long ld_dout, const int* ids, i
  * x [M, D], w_gate, w_up [F, D], w_down [O, F], y [M, O]; M >= 0, 1 <= D, O <= 128,
  * 1 <= F <= 1024 (SPLAT_ERR_CAPACITY above). The hidden row act(a) * u is kept on chip. Before the
  * second product it is rounded once to dtype (an fp16 hidden value above 65504 is infinite), except
- * that up to 128 rows keep it in fp32 and up to 32 hidden units in twice dtype's bits. A row of x
+ * that up to 128 rows keep it in fp32 and narrow blocks (F <= 32 or D D O < 512) in twice dtype's
+ * bits. A row of x
  * that holds an infinity or a NaN gets a y row that is not finite, which of its values is not
  * specified; other rows do not depend on it.
  *
  * splat_ffn_backward: from dy [M, O] the gradients dx [M, D], dw_gate, dw_up [F, D] and dw_down
  * [O, F] (each may be NULL, not all; dw_gate only with w_gate). The hidden values are computed
- * again from x; they and their gradients are rounded once to dtype (with up to 32 hidden units, to
- * twice its bits) before the products that use them; weight gradients are fp32 sums over all rows,
+ * again from x; they and their gradients are rounded once to dtype (in narrow blocks, to twice
+ * its bits) before the products that use them; weight gradients are fp32 sums over all rows,
  * rounded once. With M = 0 the weight gradients are zero.
  */
 long long splat_ffn_scratch(int M, int D, int F, int O, int dtype, int gated, int backward);

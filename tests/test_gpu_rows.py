@@ -199,6 +199,9 @@ FFNS = [  # M, D, F, O, gated, act, pad
     # chunks of units that a cluster cannot share evenly
     (5001, 57, 700, 64, True, "gelu", 3), (1500, 90, 449, 127, False, "silu", 1),
     (300, 128, 1000, 3, True, "silu", 0),
+    # few inputs and outputs of many hidden units
+    (700, 2, 104, 21, True, "gelu", 3), (20000, 3, 1000, 9, False, "silu", 0),
+    (3000, 15, 70, 2, True, "silu", 0), (30000, 1, 1024, 1, True, "gelu", 0),
     # a few hidden units, few and many rows
     (200, 61, 1, 3, True, "silu", 8), (700, 128, 16, 128, True, "gelu", 0),
     (20000, 61, 1, 3, True, "silu", 8), (20000, 128, 32, 100, False, "gelu", 1),
@@ -609,3 +612,18 @@ def test_sizes_beyond_32_bits(P):
         P.lookup(x, torch.zeros(1, dtype=torch.int32, device="cuda").expand(n), y.expand(n, 1))
     with pytest.raises(ValueError, match="more than"):
         P.lookup(x.expand(n, 1), torch.zeros(1, dtype=torch.int32, device="cuda"), y)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=str)
+def test_narrow_blocks_round_once(P, dt):
+    """Blocks of few inputs hold hidden values in twice the bits: their outputs are rounded once."""
+    M, D, F, O = 20000, 2, 104, 21
+    x, wg, wu, wd, _ = _ffn_inputs(M, D, F, O, True, dt, 8)
+    y = torch.empty((M, O), dtype=dt, device="cuda")
+    P.ffn(x.cuda(), wg.cuda(), wu.cuda(), wd.cuda(), y, act="gelu")
+    x, wg, wu, wd = (t.double() for t in (x, wg, wu, wd))
+    want = (R.act(x @ wg.T, "gelu")[0] * (x @ wu.T)) @ wd.T
+    # hidden values off by 2 u^2 of their size and by fp32 roundings of their arguments and of the sum
+    mag = (1.13 * (x.abs() @ wg.abs().T) * (x.abs() @ wu.abs().T)) @ wd.abs().T
+    e = (4 * R.U[dt] ** 2 + (F + 64) * R.ACC) * mag + F * R.TINY[dt]
+    R.close(y, (want, R._held(want, e, dt)))
