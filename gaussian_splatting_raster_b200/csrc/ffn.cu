@@ -4,8 +4,9 @@
 // hidden units pass in chunks of 64 (their weights staged per chunk, transposed so that every inner
 // product reads along rows). Bound by the fp32 lanes and by the shared-memory loads that feed them:
 // 2 M F (2 D + O) operations against 4 M (D + O) bytes, which at D = 57, F = 256, O = 64 is 188
-// operations a byte. There 200,000 rows take 448 us (41 TFLOP/s, 55 % of the lanes' 74); the
-// gradients of 100,000 rows 490 us for dx (30 TFLOP/s) and 692 us for the weights (26).
+// operations a byte. There 200,000 rows take 446 us (41 TFLOP/s, 55 % of the lanes' 74); the
+// gradients of 100,000 rows 498 us for dx (30 TFLOP/s) and 690 us for the weights (26). 50,000 rows of
+// 128 / 512 / 128 silu take 472 us (42), dx 933 us (35), weights 1,082 us (36).
 #include <algorithm>
 
 #include "ffn.cuh"
@@ -15,8 +16,9 @@ namespace rows {
 namespace {
 
 constexpr int kT = 256;
-// UC units are taken at a time: 64 (16 x 16 threads), or 16 (4 x 64) or 4 (1 x 256) for a few hidden
-// units. Thread (tx, ty) has rows ty * RT .. and units (or output columns) tx * 4 .. of every UC.
+// UC units are taken at a time: 64 (16 x 16 threads), or 16 (4 x 64) or 4 (1 x 256) for a few
+// hidden units. Thread (tx, ty) has rows ty * RT .. and units (or output columns) tx * 4 .. of
+// every UC.
 
 // ---------------------------------------------------------------------------------------------
 // packed weights and staging
@@ -86,8 +88,8 @@ __device__ __forceinline__ void chunks_left(int left) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// rows [r0, r0 + R) of src transposed into dst[k * (R + 4) + r] by asynchronous copies; rows >= M are
-// zero
+// rows [r0, r0 + R) of src transposed into dst[k * (R + 4) + r] by asynchronous copies; rows >= M
+// are zero
 template <int R>
 __device__ __forceinline__ void copy_rows(const float* src, long long lds, long long r0, int M,
                                           int cols, float* dst) {
@@ -172,8 +174,8 @@ __device__ __forceinline__ void product_pair(const float* rowsT, int ldr, const 
 
 // acc[n] += the product with columns n UC .. of w, up to `cols` of them, two sets at a time
 template <int N, int RT, int UC>
-__device__ __forceinline__ void products(const float* rowsT, int ldr, const float* w, int ldw, int K,
-                                         int cols, float2 (&acc)[N][RT][2]) {
+__device__ __forceinline__ void products(const float* rowsT, int ldr, const float* w, int ldw,
+                                         int K, int cols, float2 (&acc)[N][RT][2]) {
 #pragma unroll
   for (int n = 0; n < N; n += 2) {
     if constexpr (N > 1) {
@@ -566,7 +568,8 @@ __global__ void __launch_bounds__(kT, 1) k_ffn_dw(FfnArgs p, const float* __rest
                                                   int bufs) {
   extern __shared__ __align__(16) float sm[];
   constexpr int RT = R * UC / 1024, ldr = R + 4, kLd = h_ld(UC);
-  constexpr int TY = 1024 / UC, C = TY < kMaxWidth ? kMaxWidth / TY : 1;  // rows of D or O a thread has: ty + TY c
+  // rows of D or O a thread has: ty + TY c
+  constexpr int TY = 1024 / UC, C = TY < kMaxWidth ? kMaxWidth / TY : 1;
   float* rows = sm;                  // [bufs] of X [D][ldr] and dY [O][ldr]
   const int both = (p.D + p.O) * ldr;
   float* As = rows + bufs * both;       // [R rows][kLd units] da, du, h
@@ -704,9 +707,9 @@ bool allow_smem(K kernel, int bytes) {
 constexpr int kSmemMax = 232448 - 1024;
 
 // Units taken at a time: 16 or 4 for a few hidden units, whose chunk of 64 would be mostly zeros (4
-// where its 256-row tiles fit); 16 also where the other side (O forward, D for dx) is so narrow that
-// pieces of 64 columns would cost more than the better use of a load by 64 units saves, about a
-// third (566,585 rows of 13, 156 units to one column, no gate: 730 us with 64, 359 with 16).
+// where its 256-row tiles fit); 16 also where the other side (O forward, D for dx) is so narrow
+// that pieces of 64 columns would cost more than the better use of a load by 64 units saves, about
+// a third (566,585 rows of 13, 156 units to one column, no gate: 730 us with 64, 359 with 16).
 int chunk_of(int D, int F, int O, bool backward) {
   if (F <= 4 && D + O <= 180) return 4;
   if (F <= 32) return 16;
@@ -718,12 +721,13 @@ int chunk_of(int D, int F, int O, bool backward) {
 }
 
 // Rows of a tile and CTAs of its cluster. A thread's products of RT rows by 4 (or, of both inputs,
-// 8) units read RT + 4 (RT + 8) words from shared memory for each input column, which is what bounds
-// them, so tall tiles read least a row; short ones and clusters, which share a tile's chunks, fill
-// the machine (of which 15 clusters of eight or 33 of four have place at once). The time of a choice
-// is about its waves of CTAs times the words a warp reads, 600 more a chunk for its barriers and
-// 1,000 a CTA, or 2,500 with a cluster's join. (Forward, 128 / 1024 / 128 gated: 300 rows 30 us, without
-// clusters 148; 20,000 rows 432 us, 667; gradients of 1,000 rows of 57 / 256 / 64: dx 13 us, 34.)
+// 8) units read RT + 4 (RT + 8) words from shared memory for each input column, which is what
+// bounds them, so tall tiles read least a row; short ones and clusters, which share a tile's
+// chunks, fill the machine (of which 15 clusters of eight or 33 of four have place at once). The
+// time of a choice is about its waves of CTAs times the words a warp reads, 600 more a chunk for
+// its barriers and 1,000 a CTA, or 2,500 with a cluster's join. (Forward, 128 / 1024 / 128 gated:
+// 300 rows 30 us, without clusters 148; 20,000 rows 432 us, 667; gradients of 1,000 rows of 57 /
+// 256 / 64: dx 13 us, 34.)
 struct Tile { int R, S; };
 Tile tile_of(int UC, int most, bool backward, long long M, int D, int F, int O, bool gated) {
   const int nch = (F + UC - 1) / UC, wide = gated ? 8 : 4;
@@ -806,7 +810,8 @@ int launch_tiles(K kernel, const FfnArgs& p, const float* img, int bufs, int sme
 template <int ACT, bool GATED, int NO, int UC, int R>
 int launch_fwd(const FfnArgs& p, const float* img, int S, cudaStream_t st) {
   const int bufs = p.F > UC * S && fwd_smem(UC, R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
-  const int smem = std::max(fwd_smem(UC, R, p.D, p.O, bufs), S > 1 ? 4 * join_floats(R, NO * 64) : 0);
+  const int smem =
+      std::max(fwd_smem(UC, R, p.D, p.O, bufs), S > 1 ? 4 * join_floats(R, NO * 64) : 0);
   return launch_tiles(k_ffn<ACT, GATED, NO, UC, R>, p, img, bufs, smem, R, S, st);
 }
 
@@ -849,7 +854,8 @@ int launch_dx(const FfnArgs& p, const float* img, int S, cudaStream_t st) {
   const int bufs = p.F > UC * S && dx_smem(UC, R, p.D, p.O, 2) <= kSmemMax ? 2
                    : dx_smem(UC, R, p.D, p.O, 1) <= kSmemMax               ? 1
                                                                            : 0;
-  const int smem = std::max(dx_smem(UC, R, p.D, p.O, bufs), S > 1 ? 4 * join_floats(R, ND * 64) : 0);
+  const int smem =
+      std::max(dx_smem(UC, R, p.D, p.O, bufs), S > 1 ? 4 * join_floats(R, ND * 64) : 0);
   return launch_tiles(k_ffn_dx<ACT, GATED, ND, UC, R>, p, img, bufs, smem, R, S, st);
 }
 

@@ -64,15 +64,17 @@ struct RowSrc {
 };
 
 // Narrow blocks take 32 hidden units a chunk, and its other 32 places hold the same units again,
-// whose hidden values and gradients are stored as what rounding took from the first ones: the second
-// products then have them in twice the bits. With at most 32 hidden units that is free; otherwise it
-// costs the groups' work twice (758,527 rows of 2 / 104 / 21: 236 us instead of 120). Sums over few units, or
-// over units that are functions of few inputs, have little to average the roundings: the weight
-// gradients of one unit were off by several times their own rounding, outputs of two inputs by 1.5
-// times. (About D^2 / 4 products of inputs in O outputs are independent.)
+// whose hidden values and gradients are stored as what rounding took from the first ones: the
+// second products then have them in twice the bits. With at most 32 hidden units that is free;
+// otherwise it costs the groups' work twice (758,527 rows of 2 / 104 / 21: 236 us instead of 120).
+// Sums over few units, or over units that are functions of few inputs, have little to average the
+// roundings: the weight gradients of one unit were off by several times their own rounding, outputs
+// of two inputs by 1.5 times. (About D^2 / 4 products of inputs in O outputs are independent.)
 __host__ __device__ constexpr bool twice(int D, int F, int O) { return F <= 32 || D * D * O < 512; }
 // units of a chunk
-__host__ __device__ constexpr int units(int D, int F, int O) { return twice(D, F, O) ? 32 : kChunk; }
+__host__ __device__ constexpr int units(int D, int F, int O) {
+  return twice(D, F, O) ? 32 : kChunk;
+}
 
 struct TcArgs {
   FfnArgs f;
