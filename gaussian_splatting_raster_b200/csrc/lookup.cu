@@ -15,8 +15,8 @@
 // device when the ids are in order already, as they are for anchors), then sums each id's run of
 // rows in fp32. The order of every sum depends only on the ids, so results are the same bits on
 // every run. Work is split over sorted entries, not over table rows: one id may own any share of
-// them. A group of lanes that spans one row sums kRun consecutive entries; runs that end inside
-// the group are written at once, the rest are joined first within the CTA (shared memory), then
+// them. A group of lanes that spans one row sums up to kRun consecutive entries; runs that end
+// inside the group are written at once, the rest are joined first within the CTA (shared memory), then
 // across CTAs from fp32 partial rows by the finishing kernel, which also zeroes rows nobody uses.
 //
 // The sums are bound by memory where rows are read in an order of their own (5.9 M rows of 19 fp16
@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRun = 32;         // sorted entries one lane group sums
+constexpr int kRun = 32;         // sorted entries one lane group sums, at most
 constexpr int kMaxBits = 10;     // digit width of one radix pass
 constexpr int kMaxDigits = 1 << kMaxBits;
 constexpr int kMaxC = 8192;
@@ -428,6 +428,15 @@ __global__ void __launch_bounds__(kSortThreads, 2) k_sort_pass(SortArgs a) {
 // sums of runs
 // ---------------------------------------------------------------------------------------------
 
+// Entries a lane group sums, one after the other: fewer while 64 groups a CTA (4 lanes a row) would
+// leave SMs without one. (The whole gradient at 4,000 rows of 32 fp32 columns, in a graph: 22.5 us,
+// with 32 entries always 28.8.)
+int run_of(long long M) {
+  int run = kRun;
+  while (run > 4 && M < 148LL * 64 * run) run >>= 1;
+  return run;
+}
+
 struct RunArgs {
   const int* ids;
   const uint2* pairs;
@@ -436,6 +445,7 @@ struct RunArgs {
   uint32_t N;
   int C;
   int gl_log;  // log2 of the lanes per row
+  int run;     // entries a lane group sums
   float scale;
   uint2* bounds;  // [N] first and one-past-last sorted entry of each id
   float* head;    // [CTAs][C] part of the run that entered the CTA
@@ -478,8 +488,8 @@ k_runs(RunArgs a, const T* __restrict__ dout, long long ldd, T* __restrict__ dta
   const int left = a.C - col;  // elements of the row from here on
   const bool act = left > 0;
   const bool sorted = !*a.unsorted;
-  const unsigned blk0 = blockIdx.x * (unsigned)(NG * kRun);
-  const int count = (int)min((unsigned)(NG * kRun), a.M - blk0);
+  const unsigned blk0 = blockIdx.x * (unsigned)(NG * a.run);
+  const int count = (int)min((unsigned)(NG * a.run), a.M - blk0);
   // entries blk0 - 1 .. blk0 + count: entry i of the CTA is s_entry[i + 1]
   for (int i = threadIdx.x; i < count + 2; i += kThreads) {
     uint2 kv = make_uint2(0xFFFFFFFFu, 0u);  // no id
@@ -491,7 +501,7 @@ k_runs(RunArgs a, const T* __restrict__ dout, long long ldd, T* __restrict__ dta
   }
   __syncthreads();
   const T* end = dout + (long long)(a.M - 1) * ldd + a.C;
-  const int i0 = min(count, g * kRun), i1 = min(count, i0 + kRun);
+  const int i0 = min(count, g * a.run), i1 = min(count, i0 + a.run);
   const bool mark = gl == 0 && blockIdx.y == 0;
   int kind = 0;
   uint32_t leaving = a.N;  // the id of the run that leaves
@@ -614,7 +624,7 @@ k_join(RunArgs a, T* __restrict__ dtable, long long ldt) {
   const int col = (blockIdx.y * GL + gl) * VE;
   const int left = a.C - col, cnt = min(left, VE);
   const bool act = left > 0;
-  const unsigned per_cta = NG * kRun;
+  const unsigned per_cta = NG * a.run;
   uint32_t n = blockIdx.x * NG + g;
   if (a.cleared) {
     const long long i = ((long long)n + 1) * per_cta;
@@ -736,7 +746,7 @@ Plan make_plan(long long M, long long N, int C) {
   p.pairs0 = take((size_t)M * 8);
   p.pairs1 = take(p.passes > 1 ? (size_t)M * 8 : 0);
   p.bounds = take((size_t)N * 8);
-  const size_t ctas = ((size_t)M + kWarps * kRun - 1) / (kWarps * kRun);  // at 32 lanes a row
+  const size_t some = kWarps * run_of(M), ctas = ((size_t)M + some - 1) / some;  // at 32 lanes a row
   p.head = take(ctas * C * 4);
   p.tail = take(ctas * C * 4);
   p.bytes = o;
@@ -765,7 +775,7 @@ int run_sums(RunArgs a, const T* dout, long long ldd, T* dtable, long long ldt, 
   while (a.gl_log < 5 && (1 << a.gl_log) < vpr) ++a.gl_log;
   const int GL = 1 << a.gl_log, NG = kThreads / GL;
   const unsigned cols = (vpr + GL - 1) / GL;
-  const unsigned per = NG * kRun;
+  const unsigned per = NG * a.run;
   k_runs<T, VB><<<dim3((a.M + per - 1) / per, cols), kThreads, 0, st>>>(a, dout, ldd, dtable, ldt);
   const unsigned groups = a.cleared ? (a.M - 1) / per : a.N;
   if (groups > 0)
@@ -825,6 +835,7 @@ int run_backward(const T* dout, long long ldd, const int* ids, long long M, int 
   a.N = (uint32_t)N;
   a.C = C;
   a.gl_log = 0;
+  a.run = run_of(M);
   a.scale = scale;
   a.bounds = q.bounds;
   a.head = (float*)(scratch + p.head);
