@@ -368,4 +368,15 @@ class Workspace:
                 for i in range(n)}
 
 
-from .rows import ffn, ffn_backward, lookup, lookup_backward, rows_status  # noqa: E402
+_ROWS = ("lookup", "lookup_backward", "ffn", "ffn_backward", "rows_status")
+
+
+def __getattr__(name):
+    """The per-row operators, imported at their first use: they need torch when they are defined,
+    the rest of the package (building and loading the library among it) does not."""
+    if name not in _ROWS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import rows
+    for n in _ROWS:
+        globals()[n] = getattr(rows, n)
+    return globals()[name]

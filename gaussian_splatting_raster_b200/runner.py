@@ -4,7 +4,7 @@ from __future__ import annotations
 
 import dataclasses
 
-from . import Workspace, ffn, ffn_backward, lookup, lookup_backward, token_dim
+from . import Workspace, token_dim
 
 
 @dataclasses.dataclass
@@ -110,6 +110,7 @@ def token_features(out: Outputs, block: FeedForward, feats, stream=None):
     """The score tokens' projection (feats [G, O] from the tokens of the last score replay; the
     rendering calls are fp32, so a bf16 or fp16 block gets its tokens rounded first)."""
     import torch
+    from . import ffn
     with torch.cuda.stream(stream):  # None: the current stream
         ffn(out.tokens.to(block.w_up.dtype), block.w_gate, block.w_up, block.w_down, feats,
             block.act)
@@ -129,6 +130,7 @@ def decode_and_render(ws: Workspace, table, ids, scale: float, block: FeedForwar
     [N, D], times scale, decoded by the block to C attributes per Gaussian and composited by the
     last render into maps [V, H, W, C]."""
     import torch
+    from . import ffn, lookup
     G, C = ids.shape[0], block.w_down.shape[0]
     with torch.cuda.stream(stream):  # None: the current stream
         d = Decoded(torch.empty((G, table.shape[1]), dtype=table.dtype, device=table.device),
@@ -144,6 +146,7 @@ def decode_backward(ws: Workspace, ids, scale: float, block: FeedForward, d: Dec
     """Gradients of decode_and_render with the render held, from dmaps [V, H, W, C]: into dtable
     [N, D] and the weights of dblock."""
     import torch
+    from . import ffn_backward, lookup_backward
     with torch.cuda.stream(stream):
         dfeats = torch.empty(d.feats.shape, dtype=torch.float32, device=d.feats.device)
         ws.scatter(dmaps, dfeats)
