@@ -698,13 +698,15 @@ int last_error() {
   return cudaGetLastError() == cudaSuccess ? SPLAT_OK : SPLAT_ERR_CUDA;
 }
 
+constexpr int kSmemMax = 232448 - 1024;
+
+// A kernel's limit is always the same: it belongs to the kernel, not to a launch, and another host
+// thread may set it between this thread's setting it and its launch.
 template <typename K>
-bool allow_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+bool allow_smem(K kernel) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) ==
          cudaSuccess;
 }
-
-constexpr int kSmemMax = 232448 - 1024;
 
 // Units taken at a time: 16 or 4 for a few hidden units, whose chunk of 64 would be mostly zeros (4
 // where its 256-row tiles fit); 16 also where the other side (O forward, D for dx) is so narrow
@@ -787,7 +789,7 @@ void pack32(const FfnArgs& p, bool backward, float* img, cudaStream_t st) {
 template <typename K>
 int launch_tiles(K kernel, const FfnArgs& p, const float* img, int bufs, int smem, int R, int S,
                  cudaStream_t st) {
-  if (!allow_smem(kernel, smem)) return SPLAT_ERR_CUDA;
+  if (!allow_smem(kernel)) return SPLAT_ERR_CUDA;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)(((long long)p.M + R - 1) / R), S);
   c.blockDim = dim3(kT);
@@ -863,7 +865,7 @@ template <int ACT, bool GATED, int UC, int R>
 int launch_dw(const FfnArgs& p, const float* img, cudaStream_t st) {
   const int bufs = dw_smem(UC, R, p.D, p.O, 2) <= kSmemMax ? 2 : 1;
   const int smem = dw_smem(UC, R, p.D, p.O, bufs);
-  if (!allow_smem(k_ffn_dw<ACT, GATED, UC, R>, smem)) return SPLAT_ERR_CUDA;
+  if (!allow_smem(k_ffn_dw<ACT, GATED, UC, R>)) return SPLAT_ERR_CUDA;
   const dim3 grid((p.F + UC - 1) / UC, p.splits);
   k_ffn_dw<ACT, GATED, UC, R><<<grid, kT, smem, st>>>(p, img, bufs);
   return run_join<float, GATED>(p, st);

@@ -1097,8 +1097,9 @@ int launch(TcArgs p, cudaStream_t st) {
       MODE == kDw ? (long long)p.nch * p.f.splits : std::min(p.tiles, 148LL);
   auto kernel = p.units < kChunk ? k_ffn_tc<MODE, T, ACT, GATED, true>
                                  : k_ffn_tc<MODE, T, ACT, GATED, false>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, fit.smem) !=
-      cudaSuccess)
+  // (the same for every launch: the limit is the kernel's, and other host threads set it too)
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmemLimit + 1024) != cudaSuccess)
     return SPLAT_ERR_CUDA;
   kernel<<<(unsigned)grid, kTcThreads, fit.smem, st>>>(p, x_map, dy_map);
   return cudaGetLastError() == cudaSuccess ? SPLAT_OK : SPLAT_ERR_CUDA;

@@ -133,6 +133,9 @@ k_lookup(const T* __restrict__ table, long long ldt, unsigned N, const int* __re
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
+// most shared memory of a pass: lanes of a digit or the tile, places, counts
+constexpr int kSortSmem = 65536 + kMaxDigits * 8 + kSortWarps * kMaxDigits * 2;
+static_assert(kSortWarps * kMaxDigits * 4 <= 65536 && kSortThreads * 16 * 8 <= 65536, "");
 
 __device__ unsigned int g_lookup_status;
 
@@ -817,7 +820,8 @@ int run_backward(const T* dout, long long ldd, const int* ids, long long M, int 
     const int smem = std::max(kSortWarps * p.nd * 4, kSortThreads * p.items * 8) + p.nd * 8 +
                      kSortWarps * p.nd * 2;
     auto pass = p.items == 16 ? k_sort_pass<16> : k_sort_pass<4>;
-    if (cudaFuncSetAttribute(pass, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+    // (the same for every launch: the limit is the kernel's, and other host threads set it too)
+    if (cudaFuncSetAttribute(pass, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem) !=
         cudaSuccess)
       return last_error();
     for (int i = 0; i < p.passes; ++i) {
