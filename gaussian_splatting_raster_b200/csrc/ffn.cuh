@@ -30,6 +30,18 @@ struct FfnArgs {
   int splits;
 };
 
+// 2^v and 1 / v of the special function unit: relative errors below 2^-22 and 2^-23.
+__device__ __forceinline__ float ex2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // act(a) and act'(a) in fp32.
 //   silu: a s, s (1 + a (1 - s)) with s = 1 / (1 + e^-a)
 //   gelu: a Phi(a), Phi(a) + a phi(a), Phi the normal distribution function, phi its density

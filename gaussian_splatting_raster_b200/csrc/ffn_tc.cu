@@ -121,21 +121,6 @@ template <> struct Two<__half> {
   }
 };
 
-// 2^v and 1 / v of the special function unit: relative error below 2^-22 each, for results that are
-// rounded to 8 or 11 bits. The unit takes one value per lane group and cycle (16 an SM), which is
-// what bounds these kernels at narrow widths, so four reciprocals are taken as one: with
-// r = 1 / (p0 p1 p2 p3) each is r times the product of the other three.
-__device__ __forceinline__ float ex2_fast(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float rcp_fast(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-
 // two fp32 lanes of one instruction
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   unsigned long long r;
@@ -164,32 +149,58 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-__device__ __forceinline__ void rcp4(const float2 (&p)[2], float2 (&r)[2]) {
+// Four reciprocals are taken as one, since the special function unit takes one value per lane group
+// and cycle (16 an SM), which is what bounds these kernels at narrow widths: with
+// r = 1 / (p0 p1 p2 p3) each is r times the product of the other three. False
+// where the product is out of range or no number: the four mean nothing then.
+__device__ __forceinline__ bool rcp4(const float2 (&p)[2], float2 (&r)[2]) {
   const float2 m = mul2(p[0], p[1]);  // p0 p2, p1 p3
-  const float i = rcp_fast(m.x * m.y);
+  const float all = m.x * m.y;
+  const float i = rcp_fast(all);
   const float2 w = make_float2(i * m.y, i * m.x);
   r[0] = mul2(w, p[1]);
   r[1] = mul2(w, p[0]);
+  return all < 4.253529586511731e37f;  // 2^125
 }
 
 // act and its slope for four values (without SLOPE the slope is not formed).
-//   silu: s = 1 / (1 + 2^t), t = -a log2 e held at 31 so that four factors stay finite: s is then
-//         never below 2^-31, less than half an fp32 step of 1 away from the true value.
+//   silu: s = 1 / (1 + 2^t), t = -a log2 e. Where the four factors' product leaves the range (a is
+//         then far on the left, or no number) the result is false and f and slope mean nothing,
+//         unless CAREFUL: each value is then taken by itself, with s = 2^-t from kFar on (the next
+//         term is 2^-t of that), so that a s goes to zero with s. (So for all values it would take two
+//         results of the special function unit a value.)
 //   gelu: Phi by Abramowitz and Stegun 7.1.26 (erfc at z = |a| / sqrt 2, absolute error 0.75e-7 in
-//         Phi), z held at 10 where Phi(-|a|) has long become zero; one power e^{-a^2/2} serves Phi
-//         and the density.
+//         Phi; relative error of Phi(-|a|) 0.05 % at -4, 0.8 % at -7.5), z held at 10 where
+//         Phi(-|a|) has long become zero; one power e^{-a^2/2} serves Phi and the density.
 // An argument that is no number gives no number: both are multiplied by a, or built from it.
-template <int ACT, bool SLOPE>
-__device__ __forceinline__ void act4(const float2 (&a)[2], float2 (&f)[2], float2 (&slope)[2]) {
+constexpr float kFar = -21.0f;
+
+__device__ __forceinline__ float min_nan(float a, float b) {  // no number if one of them is none
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float logistic_far(float a) {
+  const float t = a * -1.4426950408889634f;
+  return a < kFar ? ex2_fast(-t) : rcp_fast(1.0f + ex2_fast(t));
+}
+
+template <int ACT, bool SLOPE, bool CAREFUL>
+__device__ __forceinline__ bool act4(const float2 (&a)[2], float2 (&f)[2], float2 (&slope)[2]) {
   float2 p[2], r[2];
+  bool ok = true;
   if (ACT == SPLAT_ACT_SILU) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float2 t = mul2(a[i], both(-1.4426950408889634f));
-      p[i] = add2(make_float2(ex2_fast(fminf(t.x, 31.0f)), ex2_fast(fminf(t.y, 31.0f))),
-                  both(1.0f));
+      p[i] = add2(make_float2(ex2_fast(t.x), ex2_fast(t.y)), both(1.0f));
     }
-    rcp4(p, r);
+    ok = rcp4(p, r);
+    if (CAREFUL && !ok) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) r[i] = make_float2(logistic_far(a[i].x), logistic_far(a[i].y));
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       f[i] = mul2(a[i], r[i]);
@@ -220,6 +231,7 @@ __device__ __forceinline__ void act4(const float2 (&a)[2], float2 (&f)[2], float
       if (SLOPE) slope[i] = fma2(mul2(a[i], both(0.3989422804014327f)), e, c);
     }
   }
+  return ok;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -432,13 +444,15 @@ __device__ __forceinline__ uint32_t held(float a, float b) {
   return AGAIN ? Two<T>::rest(a, b) : Two<T>::pack(a, b);
 }
 
-// kUnits units of a row: accumulators (a, u, dh) to the hidden operand's 16-byte pieces piece ..
-template <int MODE, typename T, int ACT, bool GATED, bool AGAIN, int kUnits>
-__device__ __forceinline__ void hidden_units(uint8_t* Hs, int row, int piece,
+// kUnits units of a row: accumulators (a, u, dh) to the hidden operand's 16-byte pieces piece .. The
+// result is false where some activation has to be taken CAREFUL.
+template <int MODE, typename T, int ACT, bool GATED, bool AGAIN, bool CAREFUL, int kUnits>
+__device__ __forceinline__ bool hidden_units(uint8_t* Hs, int row, int piece,
                                              const uint32_t (&ra)[kUnits],
                                              const uint32_t (&ru)[kUnits],
                                              const uint32_t (&rd)[kUnits]) {
   uint32_t h[kUnits / 2], da[kUnits / 2], du[kUnits / 2];
+  bool ok = true;
 #pragma unroll
   for (int e = 0; e < kUnits; e += 4) {
     auto two = [&](const uint32_t (&r)[kUnits], int k) {
@@ -446,7 +460,7 @@ __device__ __forceinline__ void hidden_units(uint8_t* Hs, int row, int piece,
     };
     const float2 a[2] = {two(ra, 0), two(ra, 1)};
     float2 f[2], sl[2];
-    act4<ACT, MODE != kFwd>(a, f, sl);
+    ok &= act4<ACT, MODE != kFwd, CAREFUL>(a, f, sl);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       float2 u = make_float2(1.0f, 1.0f);
@@ -480,6 +494,7 @@ __device__ __forceinline__ void hidden_units(uint8_t* Hs, int row, int piece,
       if (MODE == kDw) put(GATED ? 2 : 1, h + e / 2);
     }
   }
+  return ok;
 }
 
 template <int MODE, typename T, int ACT, bool GATED, bool TWICE>
@@ -879,9 +894,28 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
                     const uint32_t (&rd)[kUnits]) {
       const int piece = half * 4 + q * kUnits / 8;
       if (TWICE && second)
-        hidden_units<MODE, T, ACT, GATED, true, kUnits>(Hs, row, piece, ra, ru, rd);
-      else
-        hidden_units<MODE, T, ACT, GATED, false, kUnits>(Hs, row, piece, ra, ru, rd);
+        return hidden_units<MODE, T, ACT, GATED, true, false, kUnits>(Hs, row, piece, ra, ru, rd);
+      return hidden_units<MODE, T, ACT, GATED, false, false, kUnits>(Hs, row, piece, ra, ru, rd);
+    };
+    // Once more from the accumulators, each set of four as its own values want it (so that a row's
+    // results do not depend on the other rows of its warp). Rare; kept out of the other way's
+    // registers, where a second look at a set's values would cost 4 to 9 % of the kernel.
+    auto work_careful = [&](uint8_t* Hs, uint32_t d) {
+#pragma unroll 1
+      for (int e = 0; e < 32; e += 8) {
+        uint32_t ra[8], ru[8], rd[8];
+        const uint32_t at = d + half * 32 + e;
+        tmem_ld(at, ra);
+        if (GATED) tmem_ld(at + 64, ru);
+        if (MODE != kFwd) tmem_ld(at + WR, rd);
+        tmem_wait(ra);
+        if (GATED) tmem_wait(ru);
+        if (MODE != kFwd) tmem_wait(rd);
+        if (TWICE && second)
+          hidden_units<MODE, T, ACT, GATED, true, true, 8>(Hs, row, half * 4 + e / 8, ra, ru, rd);
+        else
+          hidden_units<MODE, T, ACT, GATED, false, true, 8>(Hs, row, half * 4 + e / 8, ra, ru, rd);
+      }
     };
 
     int c = g, n = 0;
@@ -895,19 +929,35 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       // the hidden operand's place was item i - nh's (asked before this item is handed over: the
       // barrier's next phase cannot be complete yet)
       if (i >= p.nh) wait(done((i - p.nh) & 1), (i - p.nh) >> 1);
+      bool ok = true;
 #pragma unroll
       for (int q = 0; q < kSteps; q += 2) {
         landed(a0, u0, d0);
         get(d, q + 1, a1, u1, d1);
-        work(Hs, q, a0, u0, d0);
+        ok &= work(Hs, q, a0, u0, d0);
         landed(a1, u1, d1);
         if (q + 2 < kSteps) {
           get(d, q + 2, a0, u0, d0);
-        } else {
+          ok &= work(Hs, q + 1, a1, u1, d1);
+          continue;
+        }
+        // the accumulators are free once the last values are here, unless some have to be asked again
+        auto release = [&]() {
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(gu_free(i % p.ngu));
+        };
+        if (ACT == SPLAT_ACT_SILU) {
+          float least = __uint_as_float(a1[0]);
+#pragma unroll
+          for (int e = 1; e < kUnits; ++e) least = min_nan(least, __uint_as_float(a1[e]));
+          if (__any_sync(0xffffffffu, !ok || !(least >= kFar))) {
+            work_careful(Hs, d);
+            release();
+            break;
+          }
         }
+        release();
         work(Hs, q + 1, a1, u1, d1);
       }
       arrive(h_ready(i & 1));
