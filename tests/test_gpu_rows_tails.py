@@ -13,7 +13,16 @@ Bounds. u = R.U of the type, U32 = 2^-24.
   division are nearer), products and sums by U32 each: (16 + 2 |a|) U32 of the value. The slope is
   s (1 + a (1 - s)), its error that of s (1 + |a| (1 - s)). Where e^-a overflows (-a > 88.7) the
   fp32 lanes give zero for |a| e^a < 2^-121.
+  gelu, fp32 lanes: Phi(-|a|) = r P(r) e^{-a^2/2}, r = 1 / (1 + c |a|). r is off by 3 U32 (argument,
+  reciprocal) and moves r P(r) by no more than its share; P is off by 0.2 U32 from the function and
+  by 2 U32 from its last steps' roundings; the power 4 U32 and the exponent a^2 / 2 twice U32 of
+  itself, two products U32 each: (12 + 2 a^2) U32 of Phi(-|a|), and U32 of 1 - Phi(-|a|). The value
+  6 U32 more. The slope adds a phi(a): (8 + a^2) U32 of |a| phi.
+  gelu, tensor cores: Phi by the published formula (Abramowitz and Stegun 7.1.26), whose own error is
+  taken in 64 bits; e^{-a^2/2} as above, (24 + a^2) U32 of Phi(-|a|) and 2 U32 of Phi.
 """
+import math
+
 import pytest
 import torch
 
@@ -37,6 +46,11 @@ def P():
     return P
 
 
+def _phi(a):
+    """The normal distribution function. (1 + erf, and torch.special.ndtr, give zero at -9.)"""
+    return 0.5 * torch.special.erfc(-a / math.sqrt(2))
+
+
 def _expected(a, kind, dt, tensor):
     """(value, bound) of act(a) and act'(a); tensor: by the tensor-core kernels."""
     m = a.abs()
@@ -46,6 +60,20 @@ def _expected(a, kind, dt, tensor):
         v, d = a * s, s + a * s * n
         ev = (16 + 2 * m) * R.U32 * v.abs()
         ed = (16 + 2 * m) * R.U32 * s * (1 + m * n)
+    else:
+        phi = torch.exp(-a * a / 2) / math.sqrt(2 * math.pi)
+        cdf, tail = _phi(a), _phi(-m)
+        v, d = a * cdf, cdf + a * phi
+        if tensor:
+            z = m / math.sqrt(2)
+            r = 1 / (1 + 0.3275911 * z)
+            q = 0.5 * r * (0.254829592 + r * (-0.284496736 + r * (1.421413741 + r * (
+                -1.453152027 + r * 1.061405429)))) * torch.exp(-z * z)
+            ec = (q - tail).abs() + (24 + a * a) * R.U32 * tail + 2 * R.U32 * cdf
+        else:
+            ec = (12 + 2 * a * a) * R.U32 * tail + R.U32 * cdf
+        ev = m * ec + 6 * R.U32 * v.abs()
+        ed = ec + (8 + a * a) * R.U32 * m * phi + 2 * R.U32 * d.abs()
     flush = 2.0 ** -126 * (1 + 2 * m)
     if kind == "silu" and not tensor:
         flush = 2.0 ** -121
@@ -58,7 +86,7 @@ SHAPES = [  # D, F, O, gated: one unit; hidden values in twice the bits; a plain
 
 
 @pytest.mark.parametrize("dt", DTYPES, ids=str)
-@pytest.mark.parametrize("kind", ["silu"])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
 @pytest.mark.parametrize("M", [39, 200, 3000])
 def test_activation_alone(P, M, shape, kind, dt):
@@ -100,7 +128,7 @@ def test_activation_alone(P, M, shape, kind, dt):
 
 
 @pytest.mark.parametrize("dt", DTYPES, ids=str)
-@pytest.mark.parametrize("kind", ["silu"])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
 @pytest.mark.parametrize("M", [3, 200])
 def test_no_number_stays_with_its_row(P, M, kind, dt):
     """Rows of NaN, and of infinities of either sign, give rows that are not finite; rows beside
