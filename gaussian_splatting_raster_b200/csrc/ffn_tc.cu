@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x_map,
          const __grid_constant__ CUtensorMap dy_map) {
   extern __shared__ uint8_t raw[];
-  constexpr int kBars = 2 * kMaxStages + 2 * kMaxGu + 2 * kMaxRows + 2 + 2 + 2 + 2 + 2;
+  constexpr int kBars = 2 * kMaxStages + 2 * kMaxGu + 2 * kMaxRows + 2 + 2 + 2 + 2 + 3;
   __shared__ __align__(8) uint64_t s_bar[kBars];
   __shared__ uint32_t s_tmem;
   __shared__ int s_failed;
@@ -531,6 +531,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
   auto out_full = [&](int k) { return bars + 8 * (kB1 + 4 + k); };  // a tile's output is complete
   auto out_free = [&](int k) { return bars + 8 * (kB1 + 6 + k); };  // ... has been read
   const uint32_t all_done = bars + 8 * (kB1 + 8), raw_full = bars + 8 * (kB1 + 9);
+  const uint32_t raw_free = bars + 8 * (kB1 + 10);  // both loader warps have read the staged tile
   volatile int* failed = &s_failed;
   unsigned int* status = &g_rows_status;
 
@@ -539,7 +540,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
     for (int k = 0; k < kBars; ++k) {
       const bool by_group = (k >= kB0 + kMaxGu && k < kB2) || k == kB1 || k == kB1 + 1 ||
                             k == kB1 + 6 || k == kB1 + 7;
-      const bool by_loaders = k >= kB2 && k < kB2 + kMaxRows;
+      const bool by_loaders = (k >= kB2 && k < kB2 + kMaxRows) || k == kB1 + 10;
       mbar_init(bars + 8 * k, by_group ? kGroupWarps : by_loaders ? kLoaders / 32
                                                                     : k == kB1 + 8 ? 2 : 1);
     }
@@ -723,12 +724,19 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       if (yn) bulk_load(raw + p.x.raw, ya, yn, raw_full);
     };
     const bool staged = p.x.raw || (y_too && p.dy.raw);
-    int xb = 0, taken = 0;
+    // After a failed wait a warp stops at its next tile (the last round's phase may still be open) or
+    // does not start the next copy, whenever it sees the failure: neither warp waits for the other
+    // but at barriers with a limit.
+    auto stop = [&]() { return *failed != 0; };
+    int xb = 0, taken = 0, fetched = 0;
     uint32_t pf = 1;  // (the first round is free)
-    if (staged && tid == 0) fetch(0);
+    if (staged && tid < 32) {
+      if (tid == 0) fetch(0);
+      fetched = 1;
+    }
     for (int n = 0; n < nt; ++n) {
       mbar_wait(x_free(xb), pf, failed, status);
-      if (*failed) break;  // (the last round's phase may still be open)
+      if (stop()) break;
       const long long r0 = ((long long)me + (long long)n * ctas) * kTile;
       const long long rows = p.f.M - r0;
       uint8_t* Xs = smem + x_off + xb * xbytes;
@@ -759,16 +767,23 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(x_ready(xb));
-      if (staged && n + 1 < nt) {  // (the staged tile has been read by both warps)
-        asm volatile("bar.sync 3, %0;" ::"n"(kLoaders) : "memory");
-        if (tid == 0) fetch(n + 1);
+      if (staged && n + 1 < nt) {
+        if (lane == 0) mbar_arrive(raw_free);
+        if (tid < 32) {
+          mbar_wait(raw_free, n & 1, failed, status);
+          if (!stop()) {
+            if (tid == 0) fetch(n + 1);
+            ++fetched;
+          }
+        }
       }
       if (++xb == p.nx) xb = 0, pf ^= 1;
       ++taken;
     }
     // no copy may be in flight when the CTA ends, after a failed wait either
-    for (int n = max(0, taken - p.nx); n < taken; ++n) mbar_drain(x_ready(n % p.nx), (n / p.nx) & 1);
-    if (staged) mbar_drain(raw_full, min(taken, nt - 1) & 1);
+    for (int n = max(0, taken - p.nx); n < taken; ++n)
+      mbar_drain(x_ready(n % p.nx), (n / p.nx) & 1);
+    if (fetched) mbar_drain(raw_full, (fetched - 1) & 1);
   } else if (nt > 0) {
     // ------------------------------------------------------------------------- row groups
     const int g = warp / kGroupWarps, tid = threadIdx.x & (kGroupThreads - 1);
