@@ -646,7 +646,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       }
       // no copy may be in flight when the CTA ends, after a failed wait either (the drain of a
       // stage that was not started runs out, in that case)
-      for (int k = max(0, j - p.nst); k < j; ++k) mbar_drain(full(k % p.nst), (k / p.nst) & 1);
+      for (int k = max(0, j - p.nst); k < j; ++k) mbar_drain(full(k % p.nst), (k / p.nst) & 1, status);
       if (elect_one()) commit(all_done);
       __syncwarp();
     }
@@ -751,7 +751,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
           for (int b = 0; b < nby; ++b)
             tile_load(smem_addr(Ys) + b * 16384, &dy_map, b * 64, (int)r0, x_ready(xb));
       }
-      if (staged) mbar_drain(raw_full, n & 1);
+      if (staged) mbar_wait(raw_full, n & 1, failed, status);
       auto take = [&](const RowSrc& src, int blocks, uint32_t at, uint8_t* dst) {
         const uint8_t* start;
         if (src.raw && raw_span(src, r0, p.f.M, start)) {
@@ -782,8 +782,8 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
     }
     // no copy may be in flight when the CTA ends, after a failed wait either
     for (int n = max(0, taken - p.nx); n < taken; ++n)
-      mbar_drain(x_ready(n % p.nx), (n / p.nx) & 1);
-    if (fetched) mbar_drain(raw_full, (fetched - 1) & 1);
+      mbar_drain(x_ready(n % p.nx), (n / p.nx) & 1, status);
+    if (fetched) mbar_drain(raw_full, (fetched - 1) & 1, status);
   } else if (nt > 0) {
     // ------------------------------------------------------------------------- row groups
     const int g = warp / kGroupWarps, tid = threadIdx.x & (kGroupThreads - 1);
@@ -1001,7 +1001,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
                                  ((GATED ? 2 : 1) * FD + (size_t)p.f.F * p.f.O);
     const int f = chunk0 * p.units + (two ? row & 31 : row & 63);
     if (nt > 0) {
-      mbar_drain(all_done, 0);
+      mbar_wait(all_done, 0, failed, status);
       fence_after();
     }
     for (int which = 0; which < 2; ++which) {
@@ -1024,7 +1024,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
   __syncthreads();
   if (warp == 2 * kGroupWarps) {
     // every MMA is done before TMEM is given back
-    if (nt > 0) mbar_drain(all_done, 0);
+    if (nt > 0) mbar_drain(all_done, 0, status);
     fence_after();
     __syncwarp();
     tmem_free(tmem, kCols);

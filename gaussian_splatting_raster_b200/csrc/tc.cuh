@@ -78,11 +78,15 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// The same for what must be over before a kernel goes on even after a failed wait: copies and MMAs
-// in flight, which end by themselves.
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+// For what must be over before a CTA ends, also after a failed wait: copies and MMAs in flight, which
+// end by themselves. It lasts twice as long as a wait, which may have run out shortly before.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, unsigned int* status) {
   const long long t0 = clock64();
-  while (!mbar_try(bar, parity) && clock64() - t0 < kWaitClocks) {
+  while (!mbar_try(bar, parity)) {
+    if (clock64() - t0 > 2 * kWaitClocks) {
+      atomicOr(status, 1u);
+      return;
+    }
   }
 }
 
