@@ -592,7 +592,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       uint32_t pe = 1;
       auto load_weights = [&]() {
         // (after a failed wait a stage's last phase may still be open: nothing more is started)
-        if (!*failed) {
+        if (!__any_sync(0xffffffffu, *failed)) {
           if (elect_one()) {
             mbar_expect(full(sj), p.stage_bytes);
             bulk_load(sbase + sj * p.stage_bytes,
@@ -727,7 +727,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
     // After a failed wait a warp stops at its next tile (the last round's phase may still be open) or
     // does not start the next copy, whenever it sees the failure: neither warp waits for the other
     // but at barriers with a limit.
-    auto stop = [&]() { return *failed != 0; };
+    auto stop = [&]() { return __any_sync(0xffffffffu, *failed) != 0; };
     int xb = 0, taken = 0, fetched = 0;
     uint32_t pf = 1;  // (the first round is free)
     if (staged && tid < 32) {

@@ -63,19 +63,23 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Wait for the completion of the phase of the given parity. `failed` is the CTA's failure flag.
+// Wait for the completion of the phase of the given parity, by whole warps, which leave together.
+// `failed` is the CTA's failure flag. (What a warp decides by that flag it decides by a vote: its lanes
+// may read it on either side of its being set.)
 __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int* failed,
                                           unsigned int* status) {
-  if (mbar_try(bar, parity)) return;
-  const long long t0 = clock64();
-  while (!mbar_try(bar, parity)) {
-    if (*failed) return;
-    if (clock64() - t0 > kWaitClocks) {
-      *failed = 1;
-      atomicOr(status, 1u);
-      return;
+  if (!mbar_try(bar, parity)) {
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity)) {
+      if (*failed) break;
+      if (clock64() - t0 > kWaitClocks) {
+        *failed = 1;
+        atomicOr(status, 1u);
+        break;
+      }
     }
   }
+  __syncwarp();
 }
 
 // For what must be over before a CTA ends, also after a failed wait: copies and MMAs in flight, which
@@ -85,9 +89,10 @@ __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, unsign
   while (!mbar_try(bar, parity)) {
     if (clock64() - t0 > 2 * kWaitClocks) {
       atomicOr(status, 1u);
-      return;
+      break;
     }
   }
+  __syncwarp();
 }
 
 // contiguous copy global -> shared, completing on the barrier (16-byte aligned, multiple of 16)
