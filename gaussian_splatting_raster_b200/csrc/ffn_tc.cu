@@ -588,11 +588,12 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       uint32_t pg = 1, px = 0, pw = 0;  // (the first round of accumulators is free)
       // the next chunk's weights: number, chunk, stage
       const int uses = ring ? total : nch;
-      int j = 0, cj = 0, sj = 0;
+      int j = 0, cj = 0, sj = 0, loads = 0;  // loads: those that were started
       uint32_t pe = 1;
       auto load_weights = [&]() {
         // (after a failed wait a stage's last phase may still be open: nothing more is started)
         if (!__any_sync(0xffffffffu, *failed)) {
+          ++loads;
           if (elect_one()) {
             mbar_expect(full(sj), p.stage_bytes);
             bulk_load(sbase + sj * p.stage_bytes,
@@ -644,9 +645,9 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
           if (++x1 == p.nx) x1 = 0, px ^= 1;
         }
       }
-      // no copy may be in flight when the CTA ends, after a failed wait either (the drain of a
-      // stage that was not started runs out, in that case)
-      for (int k = max(0, j - p.nst); k < j; ++k) mbar_drain(full(k % p.nst), (k / p.nst) & 1, status);
+      // no copy may be in flight when the CTA ends, after a failed wait either
+      for (int k = max(0, loads - p.nst); k < loads; ++k)
+        mbar_drain(full(k % p.nst), (k / p.nst) & 1, status);
       if (elect_one()) commit(all_done);
       __syncwarp();
     }

@@ -29,7 +29,8 @@ def test_late_copies_end_and_are_reported():
     assert reported > 300
 
 
-@pytest.mark.parametrize("mistakes", [("meet", "silent"), ("go on",), ("silent",), ("apart",)], ids="-".join)
+@pytest.mark.parametrize("mistakes", [("meet", "silent"), ("apart",), ("silent",), ("go on",),
+                                      ("count skipped",)], ids="-".join)
 def test_planted_mistakes_are_seen(mistakes):
     R = random.Random(3)
     for seed in range(4000):
