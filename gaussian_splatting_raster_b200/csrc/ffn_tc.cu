@@ -502,10 +502,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x_map,
          const __grid_constant__ CUtensorMap dy_map) {
   extern __shared__ uint8_t raw[];
-  constexpr int kBars = 2 * kMaxStages + 2 * kMaxGu + 2 * kMaxRows + 2 + 2 + 2 + 2 + 3;
+  constexpr int kBars = 2 * kMaxStages + 2 * kMaxGu + 2 * kMaxRows + 2 + 2 + 2 + 2 + 2;
   __shared__ __align__(8) uint64_t s_bar[kBars];
   __shared__ uint32_t s_tmem;
   __shared__ int s_failed;
+  __shared__ unsigned s_read;  // staged tiles that the loader warps have read, both counted
   constexpr int WR = GATED ? 128 : 64;
   constexpr bool BF = Two<T>::kBf16;
   constexpr uint32_t kGu = gu_cols(MODE, GATED);
@@ -531,16 +532,16 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
   auto out_full = [&](int k) { return bars + 8 * (kB1 + 4 + k); };  // a tile's output is complete
   auto out_free = [&](int k) { return bars + 8 * (kB1 + 6 + k); };  // ... has been read
   const uint32_t all_done = bars + 8 * (kB1 + 8), raw_full = bars + 8 * (kB1 + 9);
-  const uint32_t raw_free = bars + 8 * (kB1 + 10);  // both loader warps have read the staged tile
   volatile int* failed = &s_failed;
   unsigned int* status = &g_rows_status;
 
   if (threadIdx.x == 0) {
     s_failed = 0;
+    s_read = 0;
     for (int k = 0; k < kBars; ++k) {
       const bool by_group = (k >= kB0 + kMaxGu && k < kB2) || k == kB1 || k == kB1 + 1 ||
                             k == kB1 + 6 || k == kB1 + 7;
-      const bool by_loaders = (k >= kB2 && k < kB2 + kMaxRows) || k == kB1 + 10;
+      const bool by_loaders = k >= kB2 && k < kB2 + kMaxRows;
       mbar_init(bars + 8 * k, by_group ? kGroupWarps : by_loaders ? kLoaders / 32
                                                                     : k == kB1 + 8 ? 2 : 1);
     }
@@ -725,19 +726,15 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       if (yn) bulk_load(raw + p.x.raw, ya, yn, raw_full);
     };
     const bool staged = p.x.raw || (y_too && p.dy.raw);
-    // After a failed wait a warp stops at its next tile (the last round's phase may still be open) or
-    // does not start the next copy, whenever it sees the failure: neither warp waits for the other
-    // but at barriers with a limit.
-    auto stop = [&]() { return __any_sync(0xffffffffu, *failed) != 0; };
-    int xb = 0, taken = 0, fetched = 0;
+    // The warp that has read a staged tile last starts the next copy: neither waits for the other.
+    // A warp stops at its next row tile once a wait of the CTA has failed (places become free then that
+    // were not filled), and after a staged tile that did not come: its phase is still open, and the
+    // next one's parity would be an older one's.
+    int xb = 0, taken = 0, staged_tile = 0;  // staged_tile: the last known to be on its way
     uint32_t pf = 1;  // (the first round is free)
-    if (staged && tid < 32) {
-      if (tid == 0) fetch(0);
-      fetched = 1;
-    }
+    if (staged && tid == 0) fetch(0);
     for (int n = 0; n < nt; ++n) {
-      mbar_wait(x_free(xb), pf, failed, status);
-      if (stop()) break;
+      if (!mbar_wait<true>(x_free(xb), pf, failed, status)) break;
       const long long r0 = ((long long)me + (long long)n * ctas) * kTile;
       const long long rows = p.f.M - r0;
       uint8_t* Xs = smem + x_off + xb * xbytes;
@@ -752,7 +749,11 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
           for (int b = 0; b < nby; ++b)
             tile_load(smem_addr(Ys) + b * 16384, &dy_map, b * 64, (int)r0, x_ready(xb));
       }
-      if (staged) mbar_wait(raw_full, n & 1, failed, status);
+      bool came = true;
+      if (staged) {
+        came = mbar_wait(raw_full, n & 1, failed, status);
+        staged_tile = n;
+      }
       auto take = [&](const RowSrc& src, int blocks, uint32_t at, uint8_t* dst) {
         const uint8_t* start;
         if (src.raw && raw_span(src, r0, p.f.M, start)) {
@@ -769,22 +770,22 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       __syncwarp();
       if (lane == 0) mbar_arrive(x_ready(xb));
       if (staged && n + 1 < nt) {
-        if (lane == 0) mbar_arrive(raw_free);
-        if (tid < 32) {
-          mbar_wait(raw_free, n & 1, failed, status);
-          if (!stop()) {
-            if (tid == 0) fetch(n + 1);
-            ++fetched;
-          }
+        unsigned read = 0;
+        if (lane == 0) read = count_one(smem_addr(&s_read));
+        if (__shfl_sync(0xffffffffu, read, 0) == 2u * n + 1u && came) {
+          if (lane == 0) fetch(n + 1);
+          staged_tile = n + 1;
         }
       }
       if (++xb == p.nx) xb = 0, pf ^= 1;
       ++taken;
+      if (!came) break;
     }
     // no copy may be in flight when the CTA ends, after a failed wait either
     for (int n = max(0, taken - p.nx); n < taken; ++n)
       mbar_drain(x_ready(n % p.nx), (n / p.nx) & 1, status);
-    if (fetched) mbar_drain(raw_full, (fetched - 1) & 1, status);
+    // (when the other warp has started one more since, its phase is the one that is waited for)
+    if (staged) mbar_drain(raw_full, staged_tile & 1, status);
   } else if (nt > 0) {
     // ------------------------------------------------------------------------- row groups
     const int g = warp / kGroupWarps, tid = threadIdx.x & (kGroupThreads - 1);
@@ -891,8 +892,9 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       }
     };
     // this thread: row `row` of the tile, units half * 32 .. + 32, taken kUnits at a time; the
-    // next units' accumulators are on their way while one set is worked on
-    constexpr int kUnits = MODE == kFwd ? 16 : 8;
+    // next units' accumulators are on their way while one set is worked on (16 with rests as well would
+    // spill: 758,527 rows of 2 / 104 / 21 take 257 us so, 239 with 8)
+    constexpr int kUnits = MODE == kFwd && !TWICE ? 16 : 8;
     constexpr int kSteps = 32 / kUnits;
     auto get = [&](uint32_t d, int q, uint32_t (&ra)[kUnits], uint32_t (&ru)[kUnits],
                    uint32_t (&rd)[kUnits]) {

@@ -63,14 +63,16 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Wait for the completion of the phase of the given parity, by whole warps, which leave together.
-// `failed` is the CTA's failure flag. (What a warp decides by that flag it decides by a vote: its lanes
-// may read it on either side of its being set.)
-__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int* failed,
+// Wait for the completion of the phase of the given parity, by whole warps: true where the phase is over
+// (and, SURE, no wait of the CTA has failed so far). `failed` is the CTA's failure flag. A warp leaves
+// together and with one result, a vote: its lanes may read the flag on either side of its being set.
+template <bool SURE = false>
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* failed,
                                           unsigned int* status) {
-  if (!mbar_try(bar, parity)) {
+  bool over = mbar_try(bar, parity);
+  if (!over) {
     const long long t0 = clock64();
-    while (!mbar_try(bar, parity)) {
+    while (!(over = mbar_try(bar, parity))) {
       if (*failed) break;
       if (clock64() - t0 > kWaitClocks) {
         *failed = 1;
@@ -79,7 +81,8 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatil
       }
     }
   }
-  __syncwarp();
+  if (SURE) over = over && !*failed;
+  return __all_sync(0xffffffffu, over);
 }
 
 // For what must be over before a CTA ends, also after a failed wait: copies and MMAs in flight, which
@@ -119,6 +122,13 @@ __device__ __forceinline__ void tile_load(uint32_t dst, const void* map, int x, 
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+
+// a count in shared memory before this one: what the counters before did is seen by those behind
+__device__ __forceinline__ unsigned count_one(uint32_t addr) {
+  unsigned n;
+  asm volatile("atom.add.acq_rel.cta.shared::cta.u32 %0, [%1], 1;" : "=r"(n) : "r"(addr) : "memory");
+  return n;
 }
 
 __device__ __forceinline__ void fence_async_shared() {

@@ -10,7 +10,10 @@ in flight at the end is waited for twice as long as data, no longer).
 
 Mistakes that can be planted: "meet" (the loader warps meet at a barrier without a limit, after a look
 at the failure flag each on its own), "apart" (the lanes of a warp look at it each on its own), "silent"
-(a wait for data that runs out says nothing), "go on" (a loader starts its next copy after a failed wait).
+(a wait for data that runs out says nothing), "go on" (a loader goes on after a staged tile that did not
+come), "trust" (it goes by its barriers alone, which other roles move on after a failed wait), "count
+skipped" (the weights waited for at the end include some that were not asked for after
+a failed wait).
 """
 import random
 
@@ -33,6 +36,8 @@ class Bar:
         self.count, self.pending, self.open, self.phase = count, count, 0, 0
 
     def arrive(self):
+        if self.pending == 0:
+            raise Wrong("an arrival too many: the phase's copies are not there")
         self.pending -= 1
         self._turn()
 
@@ -93,13 +98,13 @@ class Cta:
         self.x_ready = [Bar(2) for _ in range(p.nx)]
         self.x_free = [Bar() for _ in range(p.nx)]
         self.h_ready, self.done, self.out_full, self.out_free = ([Bar(), Bar()] for _ in range(4))
-        self.raw_full, self.raw_free, self.all_done = Bar(), Bar(2), Bar(2)
+        self.raw_full, self.all_done, self.read = Bar(), Bar(2), 0
         # what lies where
         self.W, self.X, self.raw = [None] * p.nst, [[None, None] for _ in range(p.nx)], None
         self.GU, self.H, self.A = [None] * p.ngu, [None] * p.nh, [None, None]
         self.outs, self.sums = [], []
         self.queue = {"first": [], "second": []}
-        self.met, self.gone = 0, 0
+        self.met = 0
 
     # -- time ---------------------------------------------------------------------------------
     def start(self, kind, effect, steps):
@@ -132,7 +137,7 @@ class Cta:
         t0, limit = None, limit + self.R.randint(0, 200)
         while not bar.over(parity & 1):
             if self.failed and not silent:
-                return
+                return False
             if t0 is None:
                 t0 = self.now
                 yield None  # (what came before this wait was a step)
@@ -141,9 +146,10 @@ class Cta:
                 if not silent:
                     self.failed = True
                     self.status = True
-                return
+                return False
             yield t0 + limit + 1
         yield None
+        return True
 
     def drain(self, bar, parity):  # before the end: what is in flight
         yield from self.wait(bar, parity, silent=True, limit=2 * LIMIT)
@@ -290,7 +296,7 @@ class Cta:
 
     def loader(self, w):
         p = self.p
-        xb, pf, taken, fetched = 0, 1, 0, 0
+        xb, pf, taken, staged_tile = 0, 1, 0, 0
         half = w  # each warp lays out half the rows
 
         def fetch(n):
@@ -304,11 +310,14 @@ class Cta:
             self.start("copy", there, COPY)
         if p.staged and w == 0:
             fetch(0)
-            fetched = 1
         for n in range(p.nt):
-            yield from self.wait(self.x_free[xb], pf)
-            if (yield from self.stop()):
+            over = yield from self.wait(self.x_free[xb], pf)
+            if "trust" in self.bad:
+                if not over:
+                    break
+            elif (yield from self.stop()):
                 break
+            came = True
             if not p.staged:
                 if w == 0:
                     b = xb
@@ -322,7 +331,9 @@ class Cta:
                 yield None
             else:
                 self.X[xb][half] = "filling"
-                yield from self.wait(self.raw_full, n, silent="silent" in self.bad)
+                came = yield from self.wait(self.raw_full, n, silent="silent" in self.bad)
+                came |= bool({"silent", "go on"} & self.bad)
+                staged_tile = n
                 for _ in range(2):
                     self.need(self.raw == n, f"staged tile {n}: {self.raw}")
                     right = self.raw == n
@@ -338,22 +349,22 @@ class Cta:
                         yield "forever"
                     if w == 0:
                         fetch(n + 1)
-                        fetched += 1
+                        staged_tile = n + 1
                 else:
-                    self.raw_free.arrive()
-                    if w == 0:
-                        yield from self.wait(self.raw_free, n)
-                        if "go on" in self.bad or not (yield from self.stop()):
-                            fetch(n + 1)
-                            fetched += 1
+                    self.read += 1
+                    if self.read == 2 * n + 2 and came:
+                        fetch(n + 1)
+                        staged_tile = n + 1
             xb += 1
             if xb == p.nx:
                 xb, pf = 0, pf ^ 1
             taken += 1
+            if not came:
+                break
         for n in range(max(0, taken - p.nx), taken):
             yield from self.drain(self.x_ready[n % p.nx], n // p.nx)
-        if fetched:
-            yield from self.drain(self.raw_full, fetched - 1)
+        if p.staged:
+            yield from self.drain(self.raw_full, staged_tile)
 
     def group(self, g):
         p, total = self.p, self.p.nt * self.p.nch

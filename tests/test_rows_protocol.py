@@ -30,7 +30,7 @@ def test_late_copies_end_and_are_reported():
 
 
 @pytest.mark.parametrize("mistakes", [("meet", "silent"), ("apart",), ("silent",), ("go on",),
-                                      ("count skipped",)], ids="-".join)
+                                      ("trust",), ("count skipped",)], ids="-".join)
 def test_planted_mistakes_are_seen(mistakes):
     R = random.Random(3)
     for seed in range(4000):
