@@ -137,6 +137,11 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortSmem = 65536 + kMaxDigits * 8 + kSortWarps * kMaxDigits * 2;
 static_assert(kSortWarps * kMaxDigits * 4 <= 65536 && kSortThreads * 16 * 8 <= 65536, "");
 
+// how long a CTA waits for its predecessors' counts: about four seconds
+#ifndef SPLAT_LOOKUP_WAIT_CLOCKS
+#define SPLAT_LOOKUP_WAIT_CLOCKS 8000000000LL
+#endif
+
 __device__ unsigned int g_lookup_status;
 
 __device__ __forceinline__ uint32_t key_of(int id, uint32_t N) {
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(kSortThreads, 2) k_sort_pass(SortArgs a) {
         }
       }
       if (done) break;
-      if (p == asked && clock64() - t0 > 8000000000LL) {
+      if (p == asked && clock64() - t0 > SPLAT_LOOKUP_WAIT_CLOCKS) {
         atomicOr(&g_lookup_status, 1u);
         break;
       }
@@ -616,6 +621,13 @@ k_runs(RunArgs a, const T* __restrict__ dout, long long ldd, T* __restrict__ dta
 // added in order.
 constexpr int kLong = 32;
 
+// The entries of row n. Nothing where its bounds do not fit together, as when a wait of the sort ran out
+// and the entries are in no order: CTAs are told from them.
+__device__ __forceinline__ uint2 entries_of(const RunArgs& a, uint32_t n) {
+  const uint2 se = a.bounds[n];
+  return se.x < se.y && se.y <= a.M ? se : make_uint2(0u, 0u);
+}
+
 template <typename T, int VB>
 __global__ void __launch_bounds__(kThreads)
 k_join(RunArgs a, T* __restrict__ dtable, long long ldt) {
@@ -640,7 +652,7 @@ k_join(RunArgs a, T* __restrict__ dtable, long long ldt) {
 #pragma unroll
   for (int e = 0; e < VE; ++e) acc[e] = 0.0f;
   if (n < a.N) {
-    const uint2 se = a.bounds[n];
+    const uint2 se = entries_of(a, n);
     T* dst = dtable + (long long)n * ldt + col;
     if (se.x == se.y) {
       if (act) put_row<T, VB>(dst, acc, 0.0f, left);
@@ -667,7 +679,7 @@ k_join(RunArgs a, T* __restrict__ dtable, long long ldt) {
   for (int r = 0; r < NG; ++r) {
     const uint32_t m = s_long[r];
     if (m >= a.N) continue;  // the same for every thread
-    const uint2 se = a.bounds[m];
+    const uint2 se = entries_of(a, m);
     const unsigned b0 = se.x / per_cta, b1 = (se.y - 1) / per_cta;
     const unsigned share = (b1 - b0 + NG - 1) / NG;
     const unsigned h0 = b0 + 1 + g * share, h1 = min(b1 + 1, h0 + share);
