@@ -51,6 +51,11 @@ constexpr int kTcThreads = 2 * kGroupThreads + 64 + kLoaders;  // + both product
 constexpr int kMaxStages = 16;
 constexpr int kMaxGu = 3, kMaxRows = 3;  // accumulators of first products; row tiles
 constexpr int kTile = 128;
+// Rows whose weight gradients one accumulator takes: a launch has at most so many a split, and adds its
+// sums to those of the launch before. The tensor cores add with truncation, so a sum of one sign loses
+// up to 2^-23 of what it holds with every 16 rows: at 8,192 rows 2^-15 of itself, an eighth of fp16's
+// rounding. (One launch for all lost 3e-4 over 222,000 rows a split.)
+constexpr long long kSumRows = 8192;
 constexpr int kSmemLimit = 232448 - 2048;  // 227 KB less the alignment slack and the barriers
 
 __device__ unsigned int g_rows_status;
@@ -90,6 +95,7 @@ struct TcArgs {
   int out_aligned;      // y's or dx's rows start and end at 16 bytes
   int out_dense;        // ... lie one behind the other from a 16-byte boundary
   long long tiles;
+  int again;            // weight gradients: the CTAs' sums are added to
 };
 
 // a - r, nothing where the rounded r is infinite or no number
@@ -1019,7 +1025,9 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
         if (mine)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (e0 + e < cols) dst[e0 + e] = nt > 0 ? __uint_as_float(v[e]) : 0.0f;
+            if (e0 + e < cols)
+              dst[e0 + e] =
+                  (nt > 0 ? __uint_as_float(v[e]) : 0.0f) + (p.again ? dst[e0 + e] : 0.0f);
       }
     }
   }
@@ -1189,7 +1197,16 @@ int run(const FfnArgs& f, bool backward, uint8_t* img, cudaStream_t st) {
   int rc = SPLAT_OK;
   if (!backward) return launch<kFwd, T, ACT, GATED>(p, st);
   if (f.dx && f.M > 0) rc = launch<kDx, T, ACT, GATED>(p, st);
-  if (rc == SPLAT_OK && (f.dwg || f.dwu || f.dwd)) rc = launch<kDw, T, ACT, GATED>(p, st);
+  if (!(f.dwg || f.dwu || f.dwd)) return rc;
+  const long long most = kSumRows * f.splits;
+  for (long long r = 0; rc == SPLAT_OK && (r == 0 || r < f.M); r += most) {
+    p.f.x = (const T*)f.x + r * f.ldx;
+    p.f.dy = (const T*)f.dy + r * f.lddy;
+    p.f.M = (int)std::min(most, f.M - r);
+    p.tiles = (p.f.M + kTile - 1) / kTile;
+    p.again = r > 0;
+    rc = launch<kDw, T, ACT, GATED>(p, st);
+  }
   return rc;
 }
 
