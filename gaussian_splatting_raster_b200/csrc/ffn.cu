@@ -914,6 +914,9 @@ int run(FfnArgs& p, int dtype, bool backward, void* scratch, cudaStream_t st) {
   } else {
     p.part = (float*)((char*)scratch + ffn_tc_image_bytes(p.D, p.F, p.O, GATED));
     p.splits = ffn_tc_splits(p.M, p.D, p.F, p.O);
+    if (backward && dtype == SPLAT_F16)
+      p.dy_max = (unsigned*)(p.part + (size_t)p.F * ((GATED ? 2 : 1) * p.D + p.O) * p.splits *
+                                          ffn_tc_parts(p.D, p.F, p.O));
     const int rc = ffn_tc_run(p, dtype, ACT, backward, scratch, st);
     if (rc != SPLAT_OK || !(p.dwg || p.dwu || p.dwd)) return rc;
     p.splits *= ffn_tc_parts(p.D, p.F, p.O);
@@ -961,6 +964,7 @@ long long splat_ffn_scratch(int M, int D, int F, int O, int dtype, int gated, in
   if (backward)
     n += (long long)F * ((gated ? 2 : 1) * D + O) * 4 *
          (tc ? ffn_tc_splits(M, D, F, O) * ffn_tc_parts(D, F, O) : dw_splits(M, D, F, O));
+  if (backward && dtype == SPLAT_F16) n += kMaxParts * 4;
   return (n + 255) & ~255LL;
 }
 

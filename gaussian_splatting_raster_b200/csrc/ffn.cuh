@@ -28,7 +28,9 @@ struct FfnArgs {
   int M, D, F, O;
   float* part;   // [splits] partial weight gradients, fp32: dWg, dWu [F, D] each, dWd^T [F, O]
   int splits;
+  unsigned* dy_max;  // fp16 gradients: [kMaxParts] largest finite |dy|, by CTAs
 };
+constexpr int kMaxParts = 592;
 
 // 2^v and 1 / v of the special function unit: relative errors below 2^-22 and 2^-23.
 __device__ __forceinline__ float ex2_fast(float v) {
