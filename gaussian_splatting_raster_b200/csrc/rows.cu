@@ -27,8 +27,9 @@ static bool share(const Span& a, const Span& b) {
   extent(a, al, ah);
   extent(b, bl, bh);
   if (ah <= bl || bh <= al) return false;
-  const long long ld = a.ld * a.elem;
-  if (ld != b.ld * b.elem || ld == 0) return true;
+  // (a single row has no stride of its own: it lies beside the other's rows, or not)
+  const long long ld = (a.rows > 1 ? a.ld * a.elem : b.ld * b.elem);
+  if (ld != (b.rows > 1 ? b.ld * b.elem : ld) || ld == 0) return true;
   // equal strides: they interleave when the column ranges are apart modulo the stride
   const long long d = (((long long)(bl - al)) % ld + ld) % ld;
   return !(d >= a.cols * a.elem && d + b.cols * b.elem <= ld);
