@@ -586,7 +586,6 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
   __shared__ __align__(8) uint64_t s_bar[kBars];
   __shared__ uint32_t s_tmem;
   __shared__ int s_failed;
-  __shared__ unsigned s_read;  // staged tiles that the loader warps have read, both counted
   constexpr int WR = GATED ? 128 : 64;
   constexpr bool BF = Two<T>::kBf16;
   constexpr uint32_t kGu = gu_cols(MODE, GATED);
@@ -625,7 +624,6 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
 
   if (threadIdx.x == 0) {
     s_failed = 0;
-    s_read = 0;
     for (int k = 0; k < kBars; ++k) {
       const bool by_group = (k >= kB0 + kMaxGu && k < kB2) || k == kB1 || k == kB1 + 1 ||
                             k == kB1 + 6 || k == kB1 + 7;
@@ -856,12 +854,12 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       if (y_too && !p.dy.tiled) take(p.dy, nby, raw + p.x.raw, Ys);
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(x_ready(xb));
-      if (staged && n + 1 < nt) {
-        unsigned read = 0;
-        if (lane == 0) read = count_one(smem_addr(&s_read));
-        if (__shfl_sync(0xffffffffu, read, 0) == 2u * n + 1u && came) {
-          if (lane == 0) fetch(n + 1);
+      // (the second of the two warps to arrive has read the staged tile last)
+      if (lane == 0) {
+        const bool second = mbar_arrive_pending(x_ready(xb)) == 1;
+        if (staged && n + 1 < nt && second && came) {
+          asm volatile("fence.acq_rel.cta;" ::: "memory");  // (the other warp's reads)
+          fetch(n + 1);
           staged_tile = n + 1;
         }
       }
@@ -873,6 +871,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
     for (int n = max(0, taken - p.nx); n < taken; ++n)
       mbar_drain(x_ready(n % p.nx), (n / p.nx) & 1, status);
     // (when the other warp has started one more since, its phase is the one that is waited for)
+    staged_tile = __shfl_sync(0xffffffffu, staged_tile, 0);
     if (staged) mbar_drain(raw_full, staged_tile & 1, status);
   } else if (nt > 0) {
     // ------------------------------------------------------------------------- row groups

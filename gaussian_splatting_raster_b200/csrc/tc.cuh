@@ -28,6 +28,18 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// arrivals that were pending before this one
+__device__ __forceinline__ unsigned mbar_arrive_pending(uint32_t bar) {
+  unsigned n;
+  asm volatile(
+      "{\n.reg .b64 s;\n"
+      "mbarrier.arrive.shared::cta.b64 s, [%1];\n"
+      "mbarrier.pending_count.b64 %0, s;\n}\n"
+      : "=r"(n)
+      : "r"(bar)
+      : "memory");
+  return n;
+}
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
@@ -122,13 +134,6 @@ __device__ __forceinline__ void tile_load(uint32_t dst, const void* map, int x, 
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
-}
-
-// a count in shared memory before this one: what the counters before did is seen by those behind
-__device__ __forceinline__ unsigned count_one(uint32_t addr) {
-  unsigned n;
-  asm volatile("atom.add.acq_rel.cta.shared::cta.u32 %0, [%1], 1;" : "=r"(n) : "r"(addr) : "memory");
-  return n;
 }
 
 __device__ __forceinline__ void fence_async_shared() {
