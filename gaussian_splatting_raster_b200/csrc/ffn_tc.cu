@@ -24,11 +24,12 @@
 // the bytes a tile spans, which the loaders lay out from shared memory; at the array's ends,
 // element by element.
 //
-// Measured, bf16: forward, 917,504 rows of 64 / 256 / 64 silu 196 us (307 TFLOP/s of products;
-// issue slots 57 %, special function unit 48 %, tensor pipe 22 %; 139 us without the activation,
-// 120 without the groups' work), 200,000 rows of 128 / 512 / 128 122 us (645 TFLOP/s). Gradients,
-// 311,296 rows of 64 / 128 / 64: dx 54 us, weights 63; of 35 / 128 / 48 in rows 76 bytes apart,
-// where the loaders bound it, 113 and 105. Few tiles (1,000 rows) take 8 us, 14 us a gradient.
+// Measured, bf16, silu, gated, the kernel by itself: forward, 917,504 rows of 64 / 256 / 64 178 us (507
+// TFLOP/s of products; issue slots 57 %, special function unit 48 %, tensor pipe 23 %; without a gate
+// 168 us), 200,000 rows of 128 / 512 / 128 123 us (640 TFLOP/s). Gradients, 311,296 rows of
+// 64 / 128 / 64: dx 50 us, weights 61; of 35 / 128 / 48 in rows 76 bytes apart, where the loaders
+// bound it, 116 and 113. Few tiles (1,000 rows of 57 / 256 / 64, nothing in L2) take 9 us, dx 20,
+// weights 17.
 #include <cuda.h>
 
 #include <algorithm>
