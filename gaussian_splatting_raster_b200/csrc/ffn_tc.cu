@@ -812,7 +812,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       if (xn) bulk_load(raw, xa, xn, raw_full);
       if (yn) bulk_load(raw + p.x.raw, ya, yn, raw_full);
     };
-    const bool staged = p.x.raw || (y_too && p.dy.raw);
+    const bool staged = nt > 0 && (p.x.raw || (y_too && p.dy.raw));
     // The warp that has read a staged tile last starts the next copy: neither waits for the other.
     // A warp stops at its next row tile once a wait of the CTA has failed (places become free then that
     // were not filled), and after a staged tile that did not come: its phase is still open, and the
@@ -1294,7 +1294,8 @@ int run(const FfnArgs& f, bool backward, uint8_t* img, cudaStream_t st) {
     p.f.x = (const T*)f.x + r * f.ldx;
     p.f.dy = (const T*)f.dy + r * f.lddy;
     p.f.M = (int)std::min(most, f.M - r);
-    p.tiles = (p.f.M + kTile - 1) / kTile;
+    p.tiles = ((long long)p.f.M + kTile - 1) / kTile;
+    p.f.splits = (int)std::max(1LL, std::min((long long)f.splits, p.tiles));  // (the others' sums stay)
     p.again = r > 0;
     rc = launch<kDw, T, ACT, GATED>(p, st);
   }

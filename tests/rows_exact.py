@@ -52,7 +52,10 @@ FFNS = [  # M, D, F, O, gated, pad
     (20000, 128, 32, 100, False, 1), (20000, 3, 1000, 9, False, 0),
     (65000, 9, 300, 11, True, 0),
     # several launches of the weight gradients: 9 splits, and 4, of 8,192 rows
-    (160000, 8, 1024, 16, True, 0), (100000, 4, 1024, 8, True, 0)]
+    (160000, 8, 1024, 16, True, 0), (100000, 4, 1024, 8, True, 0),
+    # ... the last of them with fewer tiles than splits
+    (9 * 8192 + 1, 9, 1024, 11, True, 3), (9 * 8192 + 300, 9, 1024, 11, True, 0),
+    (2 * 4 * 8192 + 130, 4, 1024, 8, True, 1)]
 
 
 def lookup_inputs(N, M, C, kind, seed):
