@@ -374,9 +374,10 @@ _ROWS = ("lookup", "lookup_backward", "ffn", "ffn_backward", "rows_status")
 def __getattr__(name):
     """The per-row operators, imported at their first use: they need torch when they are defined,
     the rest of the package (building and loading the library among it) does not."""
-    if name not in _ROWS:
+    if name not in _ROWS and name != "rows":
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import rows
+    import importlib
+    rows = importlib.import_module(".rows", __name__)
     for n in _ROWS:
         globals()[n] = getattr(rows, n)
     return globals()[name]

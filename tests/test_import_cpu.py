@@ -26,7 +26,12 @@ def test_operators_are_public():
              "from gaussian_splatting_raster_b200 import *\n"
              "assert all(callable(getattr(P, n)) for n in "
              "('lookup', 'lookup_backward', 'ffn', 'ffn_backward', 'rows_status'))\n"
-             "assert P.ffn is ffn\n"
+             "assert P.ffn is ffn and P.rows.ffn is ffn\n"
              "try:\n    P.nothing\nexcept AttributeError as e:\n    assert 'nothing' in str(e)\n"
              "else:\n    raise SystemExit(1)")
+    assert r.returncode == 0, r.stderr
+
+
+def test_the_operators_module_is_an_attribute():
+    r = _run("import gaussian_splatting_raster_b200 as P\nassert P.rows.lookup is P.lookup")
     assert r.returncode == 0, r.stderr
