@@ -419,7 +419,7 @@ int splat_ffn_backward(const void* dy, long long ld_dy, const void* x, long long
 
 /*
  * Waits inside these kernels (for their own copies, products and earlier blocks) are bounded at
- * about four seconds. When one ran out on the current device since the last call, the results of the
+ * about four seconds, and those for what is in flight at a kernel's end at eight. When one ran out on the current device since the last call, the results of the
  * call it belonged to mean nothing and this returns SPLAT_ERR_DEVICE_TIMEOUT once. Waits for
  * `stream`; not to be captured.
  */
