@@ -53,10 +53,12 @@ constexpr int kMaxStages = 16;
 constexpr int kMaxGu = 3, kMaxRows = 3;  // accumulators of first products; row tiles
 constexpr int kTile = 128;
 // Rows whose weight gradients one accumulator takes: a launch has at most so many a split, and adds its
-// sums to those of the launch before. The tensor cores add with truncation, so a sum of one sign loses
-// up to 2^-23 of what it holds with every 16 rows: at 8,192 rows 2^-15 of itself, an eighth of fp16's
-// rounding. (One launch for all lost 3e-4 over 222,000 rows a split.)
-constexpr long long kSumRows = 8192;
+// sums to those of the launch before. The tensor cores add with truncation: a sum of one sign loses up
+// to 2^-22 of what it holds with every 16 rows (measured: 0.82 of that), so 5e-5 of itself over 8,192
+// rows and 4e-4 over 65,536, a tenth of the type's rounding; over 131,072 it was 8e-4 in fp16 too. Each
+// launch more costs about 12 us: 917,504 rows of 64 / 256 / 64 take 280 us in bf16, which is one, and
+// 320 in fp16, which is four.
+constexpr long long sum_rows(bool bf16) { return bf16 ? 65536 : 8192; }
 constexpr int kSmemLimit = 232448 - 2048;  // 227 KB less the alignment slack and the barriers
 
 __device__ unsigned int g_rows_status;
@@ -1107,17 +1109,35 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       const bool mine = f < p.f.F && (which ? row >= 64 : GATED || row < 64);
       float* dst = part + (which ? (GATED ? 2 : 1) * FD + (size_t)f * p.f.O
                                  : (row >= 64 ? FD : 0) + (size_t)f * p.f.D);
-      for (int e0 = half * 8; e0 < cols; e0 += 16) {
-        uint32_t v[8];
-        tmem_ld(acc + which * acc_step + row_lanes + e0, v);
-        tmem_wait(v);
-        if (mine)
+      // 32 columns at a time: what the launch before left is asked for at once (one after the other, as
+      // the stores would have it, a launch took 80 us more)
+#pragma unroll 1
+      for (int e0 = half * 8; e0 < cols; e0 += 64) {
+        float sum[4][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int c = e0 + 16 * j + e;
+            sum[j][e] = p.again && mine && c < cols ? dst[c] : 0.0f;
+          }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (e0 + 16 * j >= cols) break;
+          uint32_t v[8];
+          tmem_ld(acc + which * acc_step + row_lanes + e0 + 16 * j, v);
+          tmem_wait(v);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (e0 + e < cols)
-              dst[e0 + e] =
-                  (nt > 0 ? __uint_as_float(v[e]) * (kScaled && which == 0 ? back : 1.0f) : 0.0f) +
-                  (p.again ? dst[e0 + e] : 0.0f);
+            if (nt > 0)
+              sum[j][e] += __uint_as_float(v[e]) * (kScaled && which == 0 ? back : 1.0f);
+        }
+        if (mine)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e0 + 16 * j + e < cols) dst[e0 + 16 * j + e] = sum[j][e];
       }
     }
   }
@@ -1290,7 +1310,7 @@ int run(const FfnArgs& f, bool backward, uint8_t* img, cudaStream_t st) {
   if (!backward) return launch<kFwd, T, ACT, GATED>(p, st);
   if (f.dx && f.M > 0) rc = launch<kDx, T, ACT, GATED>(p, st);
   if (!(f.dwg || f.dwu || f.dwd)) return rc;
-  const long long most = kSumRows * f.splits;
+  const long long most = sum_rows(Two<T>::kBf16) * f.splits;
   for (long long r = 0; rc == SPLAT_OK && (r == 0 || r < f.M); r += most) {
     p.f.x = (const T*)f.x + r * f.ldx;
     p.f.dy = (const T*)f.dy + r * f.lddy;

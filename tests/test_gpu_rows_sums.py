@@ -3,8 +3,10 @@ what an accumulator loses by truncation adds up instead of averaging out.
 
 Bounds, relative to the sum (u = R.U of the type): u for its rounding; the hidden values' own
 roundings are independent, n of them, at most u each: 8 u / sqrt n; the accumulator holds at most
-8,192 rows, added 16 at a time with a loss of up to 2^-23 of what it holds, half of the whole on
-average: 8192 / 16 / 2 * 2^-23 = 2^-15; the sums of those are fp32, M / 8192 + 148 of them at most.
+8,192 rows (bf16: 65,536), added 16 at a time by two truncations (of the products' sum, and of the
+addition) that lose less than a unit in its last place each, 2^-22 of what it holds, which on average
+is half of the whole: 8192 / 16 / 2 * 2^-22 = 2^-14 (2^-11), u / 8; the sums of those are fp32,
+M / 8192 + 148 of them at most.
 The mean of (got - exact) / exact has the last two, and of the roundings u / sqrt(3 F), taken five
 times: the sums of one hidden unit lie closer to one another than the type's steps (their inputs are
 averages over all rows), so only units round independently."""
@@ -74,7 +76,7 @@ def test_sums_of_one_sign(P, case, dt):
     u = R.U[dt]
     held = 0.0 if dt == torch.float32 else 8 * u / math.sqrt(M)
     # (fp32: 8,192 additions, each rounded: 2^-24 sqrt(8192) of the sum, taken eight times)
-    kept = 2.0 ** -15 if dt != torch.float32 else 8 * 2.0 ** -24 * math.sqrt(8192)
+    kept = u / 8 if dt != torch.float32 else 8 * 2.0 ** -24 * math.sqrt(8192)
     kept += (M / 8192 + 148) * R.U32
     for name, a, b in zip(("dw_gate", "dw_up", "dw_down"), got,
                           _exact(x, wg, wu, wd, dy, act)):
