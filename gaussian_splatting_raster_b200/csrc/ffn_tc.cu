@@ -176,16 +176,15 @@ __device__ __forceinline__ bool rcp4(const float2 (&p)[2], float2 (&r)[2]) {
 }
 
 // act and its slope for four values (without SLOPE the slope is not formed).
-//   silu: s = 1 / (1 + 2^t), t = -a log2 e. Where the four factors' product leaves the range (a is
-//         then far on the left, or no number) the result is false and f and slope mean nothing,
-//         unless CAREFUL: each value is then taken by itself, with s = 2^-t from kFar on (the next
-//         term is 2^-t of that), so that a s goes to zero with s. (So for all values it would take two
-//         results of the special function unit a value.)
+//   silu: s = 1 / (1 + 2^t), t = -a log2 e. Where the four factors' product leaves the range (some a
+//         are far on the left, or no number) the result is false and f and slope mean nothing; then
+//         ALONE: a reciprocal for each value, zero once 2^t is infinite, so that a s goes to zero with
+//         s. (That way for all values would take two results of the special function unit a value.)
 //   gelu: Phi by Abramowitz and Stegun 7.1.26 (erfc at z = |a| / sqrt 2, absolute error 0.75e-7 in
 //         Phi; relative error of Phi(-|a|) 0.05 % at -4, 0.8 % at -7.5), z held at 10 where
 //         Phi(-|a|) has long become zero; one power e^{-a^2/2} serves Phi and the density.
 // An argument that is no number gives no number: both are multiplied by a, or built from it.
-constexpr float kFar = -21.0f;
+constexpr float kFar = -21.0f;  // four values from here on keep the product below 2^122
 
 __device__ __forceinline__ float min_nan(float a, float b) {  // no number if one of them is none
   float r;
@@ -193,12 +192,7 @@ __device__ __forceinline__ float min_nan(float a, float b) {  // no number if on
   return r;
 }
 
-__device__ __forceinline__ float logistic_far(float a) {
-  const float t = a * -1.4426950408889634f;
-  return a < kFar ? ex2_fast(-t) : rcp_fast(1.0f + ex2_fast(t));
-}
-
-template <int ACT, bool SLOPE, bool CAREFUL>
+template <int ACT, bool SLOPE, bool ALONE>
 __device__ __forceinline__ bool act4(const float2 (&a)[2], float2 (&f)[2], float2 (&slope)[2]) {
   float2 p[2], r[2];
   bool ok = true;
@@ -208,10 +202,11 @@ __device__ __forceinline__ bool act4(const float2 (&a)[2], float2 (&f)[2], float
       const float2 t = mul2(a[i], both(-1.4426950408889634f));
       p[i] = add2(make_float2(ex2_fast(t.x), ex2_fast(t.y)), both(1.0f));
     }
-    ok = rcp4(p, r);
-    if (CAREFUL && !ok) {
+    if (ALONE) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) r[i] = make_float2(logistic_far(a[i].x), logistic_far(a[i].y));
+      for (int i = 0; i < 2; ++i) r[i] = make_float2(rcp_fast(p[i].x), rcp_fast(p[i].y));
+    } else {
+      ok = rcp4(p, r);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -528,14 +523,15 @@ __device__ __forceinline__ uint32_t held(float a, float b) {
   return AGAIN ? Two<T>::rest(a, b) : Two<T>::pack(a, b);
 }
 
-// kUnits units of a row: accumulators (a, u, dh) to the hidden operand's 16-byte pieces piece .. The
-// result is false where some activation has to be taken CAREFUL.
-template <int MODE, typename T, int ACT, bool GATED, bool AGAIN, bool CAREFUL, int kUnits>
-__device__ __forceinline__ bool hidden_units(uint8_t* Hs, int row, int piece,
-                                             const uint32_t (&ra)[kUnits],
-                                             const uint32_t (&ru)[kUnits],
-                                             const uint32_t (&rd)[kUnits], float scale) {
-  uint32_t h[kUnits / 2], da[kUnits / 2], du[kUnits / 2];
+// Units of a row: accumulators (a, u, dh) to values of the hidden operand, as pairs; false where some
+// four units have to be taken ALONE.
+template <int MODE, typename T, int ACT, bool GATED, bool AGAIN, bool ALONE, int kUnits>
+__device__ __forceinline__ bool hidden_values(const uint32_t (&ra)[kUnits],
+                                              const uint32_t (&ru)[kUnits],
+                                              const uint32_t (&rd)[kUnits], float scale,
+                                              uint32_t (&h)[kUnits / 2],
+                                              uint32_t (&da)[kUnits / 2],
+                                              uint32_t (&du)[kUnits / 2]) {
   bool ok = true;
 #pragma unroll
   for (int e = 0; e < kUnits; e += 4) {
@@ -544,7 +540,7 @@ __device__ __forceinline__ bool hidden_units(uint8_t* Hs, int row, int piece,
     };
     const float2 a[2] = {two(ra, 0), two(ra, 1)};
     float2 f[2], sl[2];
-    ok &= act4<ACT, MODE != kFwd, CAREFUL>(a, f, sl);
+    ok &= act4<ACT, MODE != kFwd, ALONE>(a, f, sl);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       float2 u = make_float2(1.0f, 1.0f);
@@ -564,21 +560,52 @@ __device__ __forceinline__ bool hidden_units(uint8_t* Hs, int row, int piece,
       }
     }
   }
+  return ok;
+}
+
+// the operand's blocks: put(block, its pairs)
+template <int MODE, bool GATED, typename F>
+__device__ __forceinline__ void hidden_blocks(const uint32_t* h, const uint32_t* da,
+                                              const uint32_t* du, F put) {
+  if (MODE == kFwd) {
+    put(0, h);
+  } else {
+    put(0, da);
+    if (GATED) put(1, du);
+    if (MODE == kDw) put(GATED ? 2 : 1, h);
+  }
+}
+
+// ... into the operand's 16-byte pieces piece ..
+template <int MODE, typename T, int ACT, bool GATED, bool AGAIN, int kUnits>
+__device__ __forceinline__ bool hidden_units(uint8_t* Hs, int row, int piece,
+                                             const uint32_t (&ra)[kUnits],
+                                             const uint32_t (&ru)[kUnits],
+                                             const uint32_t (&rd)[kUnits], float scale) {
+  uint32_t h[kUnits / 2], da[kUnits / 2], du[kUnits / 2];
+  const bool ok =
+      hidden_values<MODE, T, ACT, GATED, AGAIN, false, kUnits>(ra, ru, rd, scale, h, da, du);
 #pragma unroll
   for (int e = 0; e < kUnits; e += 8) {
     uint8_t* at = Hs + row * 128 + (((piece + e / 8) ^ (row & 7)) << 4);
-    auto put = [&](int block, const uint32_t* v) {
+    hidden_blocks<MODE, GATED>(h + e / 2, da + e / 2, du + e / 2, [&](int block, const uint32_t* v) {
       *reinterpret_cast<uint4*>(at + block * 16384) = make_uint4(v[0], v[1], v[2], v[3]);
-    };
-    if (MODE == kFwd) {
-      put(0, h + e / 2);
-    } else {
-      put(0, da + e / 2);
-      if (GATED) put(1, du + e / 2);
-      if (MODE == kDw) put(GATED ? 2 : 1, h + e / 2);
-    }
+    });
   }
   return ok;
+}
+
+// four units ALONE, into half a piece, for the lanes that want them
+template <int MODE, typename T, int ACT, bool GATED, bool AGAIN>
+__device__ __forceinline__ void hidden_alone(uint8_t* at, bool want, const uint32_t (&ra)[4],
+                                             const uint32_t (&ru)[4], const uint32_t (&rd)[4],
+                                             float scale) {
+  uint32_t h[2], da[2], du[2];
+  hidden_values<MODE, T, ACT, GATED, AGAIN, true, 4>(ra, ru, rd, scale, h, da, du);
+  if (want)
+    hidden_blocks<MODE, GATED>(h, da, du, [&](int block, const uint32_t* v) {
+      *reinterpret_cast<uint2*>(at + block * 16384) = make_uint2(v[0], v[1]);
+    });
 }
 
 template <int MODE, typename T, int ACT, bool GATED, bool TWICE>
@@ -1007,29 +1034,35 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
                     const uint32_t (&rd)[kUnits]) {
       const int piece = half * 4 + q * kUnits / 8;
       if (TWICE && second)
-        return hidden_units<MODE, T, ACT, GATED, true, false, kUnits>(Hs, row, piece, ra, ru, rd, scale);
-      return hidden_units<MODE, T, ACT, GATED, false, false, kUnits>(Hs, row, piece, ra, ru, rd, scale);
+        return hidden_units<MODE, T, ACT, GATED, true, kUnits>(Hs, row, piece, ra, ru, rd, scale);
+      return hidden_units<MODE, T, ACT, GATED, false, kUnits>(Hs, row, piece, ra, ru, rd, scale);
     };
-    // Once more from the accumulators, each set of four as its own values want it (so that a row's
-    // results do not depend on the other rows of its warp). Rare; kept out of the other way's
-    // registers, where a second look at a set's values would cost 4 to 9 % of the kernel.
-    auto work_careful = [&](uint8_t* Hs, uint32_t d) {
+    // Sets of four of the thread's 32 units that have to be taken ALONE, from the accumulators once more
+    // (a row's results do not depend on the other rows of its warp). Kept out of the other way's
+    // registers, where a second look at a set's values would cost 4 to 9 % of the kernel. (917,504 rows of
+    // 64 / 256 / 64: 196 us with a of deviation 1 to 4, 200 with 8, 265 with 15, 320 from 30 on.)
+    auto work_alone = [&](uint8_t* Hs, uint32_t d) {
 #pragma unroll 1
-      for (int e = 0; e < 32; e += 8) {
-        uint32_t ra[8], ru[8], rd[8];
-        const uint32_t at = d + half * 32 + e;
+      for (int k = 0; k < 8; ++k) {
+        uint32_t ra[4], ru[4], rd[4];
+        const uint32_t at = d + half * 32 + k * 4;
         tmem_ld(at, ra);
+        tmem_wait(ra);
+        const float2 a[2] = {make_float2(__uint_as_float(ra[0]), __uint_as_float(ra[1])),
+                             make_float2(__uint_as_float(ra[2]), __uint_as_float(ra[3]))};
+        float2 f[2], sl[2];
+        const bool want = !act4<ACT, false, false>(a, f, sl);
+        if (!__any_sync(0xffffffffu, want)) continue;
         if (GATED) tmem_ld(at + 64, ru);
         if (MODE != kFwd) tmem_ld(at + WR, rd);
-        tmem_wait(ra);
         if (GATED) tmem_wait(ru);
         if (MODE != kFwd) tmem_wait(rd);
+        uint8_t* dst = Hs + row * 128 + (((half * 4 + k / 2) ^ (row & 7)) << 4) + (k & 1) * 8;
         if (TWICE && second)
-          hidden_units<MODE, T, ACT, GATED, true, true, 8>(Hs, row, half * 4 + e / 8, ra, ru, rd,
-                                                             scale);
+          hidden_alone<MODE, T, ACT, GATED, true>(dst, want, ra, ru, rd, scale);
         else
-          hidden_units<MODE, T, ACT, GATED, false, true, 8>(Hs, row, half * 4 + e / 8, ra, ru, rd,
-                                                              scale);
+          hidden_alone<MODE, T, ACT, GATED, false>(dst, want, ra, ru, rd, scale);
+        __syncwarp();
       }
     };
 
@@ -1056,7 +1089,7 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
           ok &= work(Hs, q + 1, a1, u1, d1);
           continue;
         }
-        // the accumulators are free once the last values are here, unless some have to be asked again
+        // the accumulators are free once the last values are here, unless some may be asked for again
         auto release = [&]() {
           fence_before();
           __syncwarp();
@@ -1066,14 +1099,17 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
           float least = __uint_as_float(a1[0]);
 #pragma unroll
           for (int e = 1; e < kUnits; ++e) least = min_nan(least, __uint_as_float(a1[e]));
-          if (__any_sync(0xffffffffu, !ok || !(least >= kFar))) {
-            work_careful(Hs, d);
+          const bool done_with = __all_sync(0xffffffffu, ok && least >= kFar);
+          if (done_with) release();
+          ok &= work(Hs, q + 1, a1, u1, d1);
+          if (!done_with) {
+            if (!__all_sync(0xffffffffu, ok)) work_alone(Hs, d);
             release();
-            break;
           }
+        } else {
+          release();
+          work(Hs, q + 1, a1, u1, d1);
         }
-        release();
-        work(Hs, q + 1, a1, u1, d1);
       }
       arrive(h_ready(i & 1));
       if (MODE != kDw) {

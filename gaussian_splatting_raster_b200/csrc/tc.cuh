@@ -205,7 +205,7 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, ui
       : "memory");
 }
 
-// 32 lanes x 16 (8) columns of fp32 from TMEM; lane = the warp's quadrant of rows
+// 32 lanes x 16 (8, 4) columns of fp32 from TMEM; lane = the warp's quadrant of rows
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -222,12 +222,22 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[8]) {
         "=r"(v[7])
       : "r"(addr));
 }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr));
+}
 // Wait for this thread's TMEM loads. The loaded registers pass through, so that no use of them is
 // moved before the wait.
 template <int N>
 __device__ __forceinline__ void tmem_wait(uint32_t (&v)[N]) {
-  static_assert(N == 8 || N == 16, "");
-  if constexpr (N == 16)
+  static_assert(N == 4 || N == 8 || N == 16, "");
+  if constexpr (N == 4)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3])
+                 :
+                 : "memory");
+  else if constexpr (N == 16)
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
                    "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
