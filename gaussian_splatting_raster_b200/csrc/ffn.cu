@@ -1,13 +1,13 @@
 // Feed-forward block over rows: entry points, and the kernels on the fp32 lanes.
 //
 // One CTA takes a tile of rows through all products: its rows stay in shared memory while the
-// hidden units pass in chunks of 64, 16 or 4 (their weights staged per chunk, transposed so that every
-// inner product reads along rows). Bound by the fp32 lanes and by the shared-memory loads that feed them:
-// 2 M F (2 D + O) operations against 4 M (D + O) bytes, which at D = 57, F = 256, O = 64 is 188
-// operations a byte. There, gated, 200,000 rows take 438 us with gelu (42 TFLOP/s, 56 % of the lanes'
-// 74) and 492 with silu (37); the gradients of 100,000 rows 491 and 514 us for dx (30 and 29 TFLOP/s),
-// 664 and 692 us for the weights (27 and 26). 50,000 rows of 128 / 512 / 128 silu take 473 us (42),
-// dx 938 us (35), weights 1,085 us (36).
+// hidden units pass in chunks of 64, 16 or 4 (their weights staged per chunk, transposed so that
+// every inner product reads along rows). Bound by the fp32 lanes and by the shared-memory loads
+// that feed them: 2 M F (2 D + O) operations against 4 M (D + O) bytes, which at D = 57, F = 256, O
+// = 64 is 188 operations a byte. There, gated, 200,000 rows take 438 us with gelu (42 TFLOP/s, 56 %
+// of the lanes' 74) and 492 with silu (37); the gradients of 100,000 rows 491 and 514 us for dx (30
+// and 29 TFLOP/s), 664 and 692 us for the weights (27 and 26). 50,000 rows of 128 / 512 / 128 silu
+// take 473 us (42), dx 938 us (35), weights 1,085 us (36).
 #include <algorithm>
 
 #include "ffn.cuh"
@@ -358,10 +358,10 @@ __global__ void __launch_bounds__(kT, 1) k_ffn(FfnArgs p, const float* __restric
 // rows; each CTA takes every eighth group of hidden units, a warp four units at a time (its lanes
 // along D, then one sum over the warp for each), and forms its part of y from them; the first CTA
 // adds the eight parts in order through distributed shared memory. x and the weights are read in
-// whole rows by neighbouring lanes whatever their alignment. (57 / 256 / 64, nothing in L2, fp32: one
-// row 8.8 us, 64 rows 9.5, 128 rows 9.8, in one launch; by tiles 129 to 300 rows take 8.0 after 2.5 for
-// the packing. bf16: 128 rows 11.1 us; on the tensor cores 129 take 11.6 after 2.3.) Hidden values
-// stay in fp32.
+// whole rows by neighbouring lanes whatever their alignment. (57 / 256 / 64, nothing in L2, fp32:
+// one row 8.8 us, 64 rows 9.5, 128 rows 9.8, in one launch; by tiles 129 to 300 rows take 8.0 after
+// 2.5 for the packing. bf16: 128 rows 11.1 us; on the tensor cores 129 take 11.6 after 2.3.) Hidden
+// values stay in fp32.
 constexpr int kCluster = 8;
 constexpr int kFew = 4;        // rows of a cluster
 constexpr int kFewThreads = 256;

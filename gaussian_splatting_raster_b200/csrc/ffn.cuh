@@ -47,9 +47,9 @@ __device__ __forceinline__ float rcp_fast(float v) {
 // Phi(a), and e = e^{-a^2/2}, which the density shares. Phi(-|a|) = r P(r) e with
 // r = 1 / (1 + 0.375 z), z = |a| / sqrt 2: erfc(z) e^{z^2} / 2 is smooth in r, and P of degree 8 (a
 // minimax fit of the relative error over z in [0, 9.45], weights from a linear program on Chebyshev
-// nodes) is off by 1.2e-8 of it. So Phi keeps its digits on the left, where 1 + erf cancels (57 % off
-// at a = -5.5, zero from -5.7 on): rounding adds at most (12 + 2 a^2) 2^-24 of Phi(-|a|), most of it
-// the exponent's. e is zero below 2^-126.
+// nodes) is off by 1.2e-8 of it. So Phi keeps its digits on the left, where 1 + erf cancels (57 %
+// off at a = -5.5, zero from -5.7 on): rounding adds at most (12 + 2 a^2) 2^-24 of Phi(-|a|), most
+// of it the exponent's. e is zero below 2^-126.
 __device__ __forceinline__ float normal_cdf(float a, float& e) {
   const float r = rcp_fast(fmaf(0.375f * 0.70710678118654752f, fabsf(a), 1.0f));
   float q = fmaf(r, 0.030848359689116478f, -0.14403793215751648f);

@@ -24,9 +24,9 @@
 // the bytes a tile spans, which the loaders lay out from shared memory; at the array's ends,
 // element by element.
 //
-// Measured, bf16, silu, gated, the kernel by itself: forward, 917,504 rows of 64 / 256 / 64 178 us (507
-// TFLOP/s of products; issue slots 57 %, special function unit 48 %, tensor pipe 23 %; without a gate
-// 168 us), 200,000 rows of 128 / 512 / 128 123 us (640 TFLOP/s). Gradients, 311,296 rows of
+// Measured, bf16, silu, gated, the kernel by itself: forward, 917,504 rows of 64 / 256 / 64 178 us
+// (507 TFLOP/s of products; issue slots 57 %, special function unit 48 %, tensor pipe 23 %; without
+// a gate 168 us), 200,000 rows of 128 / 512 / 128 123 us (640 TFLOP/s). Gradients, 311,296 rows of
 // 64 / 128 / 64: dx 50 us, weights 61; of 35 / 128 / 48 in rows 76 bytes apart, where the loaders
 // bound it, 116 and 113. Few tiles (1,000 rows of 57 / 256 / 64, nothing in L2) take 9 us, dx 20,
 // weights 17.
@@ -52,12 +52,12 @@ constexpr int kTcThreads = 2 * kGroupThreads + 64 + kLoaders;  // + both product
 constexpr int kMaxStages = 16;
 constexpr int kMaxGu = 3, kMaxRows = 3;  // accumulators of first products; row tiles
 constexpr int kTile = 128;
-// Rows whose weight gradients one accumulator takes: a launch has at most so many a split, and adds its
-// sums to those of the launch before. The tensor cores add with truncation: a sum of one sign loses up
-// to 2^-22 of what it holds with every 16 rows (measured: 0.82 of that), so 5e-5 of itself over 8,192
-// rows and 4e-4 over 65,536, a tenth of the type's rounding; over 131,072 it was 8e-4 in fp16 too. Each
-// launch more costs about 12 us: 917,504 rows of 64 / 256 / 64 take 280 us in bf16, which is one, and
-// 320 in fp16, which is four.
+// Rows whose weight gradients one accumulator takes: a launch has at most so many a split, and adds
+// its sums to those of the launch before. The tensor cores add with truncation: a sum of one sign
+// loses up to 2^-22 of what it holds with every 16 rows (measured: 0.82 of that), so 5e-5 of itself
+// over 8,192 rows and 4e-4 over 65,536, a tenth of the type's rounding; over 131,072 it was 8e-4 in
+// fp16 too. Each launch more costs about 12 us: 917,504 rows of 64 / 256 / 64 take 280 us in bf16,
+// which is one, and 320 in fp16, which is four.
 constexpr long long sum_rows(bool bf16) { return bf16 ? 65536 : 8192; }
 constexpr int kSmemLimit = 232448 - 2048;  // 227 KB less the alignment slack and the barriers
 
@@ -74,11 +74,12 @@ struct RowSrc {
 // Narrow blocks take 32 hidden units a chunk, and its other 32 places hold the same units again,
 // whose hidden values and gradients are stored as what rounding took from the first ones: the
 // second products then have them in twice the bits. With at most 32 hidden units that is free;
-// otherwise it costs the groups' work twice (758,527 rows of 2 / 104 / 21: 236 us instead of 120).
+// otherwise it costs the groups' work twice (758,527 rows of 2 / 104 / 21: 239 us instead of 120).
 // Sums over few units, or over units that are functions of few inputs, have little to average the
 // roundings: the weight gradients of one unit were off by several times their own rounding, outputs
-// of two inputs by 1.5 times. In other blocks the one rounding stays: it brings outputs from 0.17 % off
-// (their own rounding, in bf16) to 0.24 %, and twice the bits would cost twice the groups' work there. (About D^2 / 4 products of inputs in O outputs are independent.)
+// of two inputs by 1.5 times. (About D^2 / 4 products of inputs in O outputs are independent.) In
+// other blocks the one rounding stays: it brings outputs from 0.17 % off (their own rounding, in
+// bf16) to 0.24 %, and twice the bits would cost twice the groups' work there.
 __host__ __device__ constexpr bool twice(int D, int F, int O) { return F <= 32 || D * D * O < 512; }
 // units of a chunk
 __host__ __device__ constexpr int units(int D, int F, int O) {
@@ -244,13 +245,13 @@ __device__ __forceinline__ bool act4(const float2 (&a)[2], float2 (&f)[2], float
 // ---------------------------------------------------------------------------------------------
 // packed weights
 // ---------------------------------------------------------------------------------------------
-// In fp16 the gradients of hidden values, da and du, are held times a power of two: gradients of a mean
-// over many rows are near fp16's smallest step (6e-8) and below it they would be zero, large ones
-// infinite. The power is 1 while the largest finite |dy| is in [2^-6, 16), else it brings it into
-// [2^-6, 2^-5) or [1, 2): da and du keep fp16's digits down to 2^-8 of the largest |dy| and may grow to
-// 2^11 times it (small |dy|: 2^21, large: 2^15). Sums are fp32 and are scaled back, exactly. It costs
-// one pass over dy, along with the packing of the weights, and a product a hidden value: gradients of
-// 311,296 rows of 35 / 128 / 48 take 12 us and 5 % more than in bf16.
+// In fp16 the gradients of hidden values, da and du, are held times a power of two: gradients of a
+// mean over many rows are near fp16's smallest step (6e-8) and below it they would be zero, large
+// ones infinite. The power is 1 while the largest finite |dy| is in [2^-6, 16), else it brings it
+// into [2^-6, 2^-5) or [1, 2): da and du keep fp16's digits down to 2^-8 of the largest |dy| and
+// may grow to 2^11 times it (small |dy|: 2^21, large: 2^15). Sums are fp32 and are scaled back,
+// exactly. It costs one pass over dy, along with the packing of the weights, and a product a hidden
+// value: gradients of 311,296 rows of 35 / 128 / 48 take 12 us and 5 % more than in bf16.
 __device__ __forceinline__ int hidden_shift(unsigned max_bits) {  // fp16 bits, without a sign
   const float m = __half2float(__ushort_as_half((unsigned short)max_bits));
   const int e = ((__float_as_int(m) >> 23) & 255) - 127;  // (subnormal fp16 values are normal here)
@@ -258,8 +259,8 @@ __device__ __forceinline__ int hidden_shift(unsigned max_bits) {  // fp16 bits, 
 }
 __device__ __forceinline__ float power_of_two(int k) { return __int_as_float((127 + k) << 23); }
 
-// The largest finite |dy| of rows part, part + parts, ... by 16 a warp: lanes have the words of a row (every
-// 32nd of H), and the elements before the first and behind the last word of a row each.
+// The largest finite |dy| of rows part, part + parts, ... by 16 a warp: lanes have the words of a
+// row (every 32nd of H), and the elements before the first and behind the last word of a row each.
 template <int H>
 __device__ __forceinline__ unsigned dy_rows(const FfnArgs& f, int part, int parts) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -523,8 +524,8 @@ __device__ __forceinline__ uint32_t held(float a, float b) {
   return AGAIN ? Two<T>::rest(a, b) : Two<T>::pack(a, b);
 }
 
-// Units of a row: accumulators (a, u, dh) to values of the hidden operand, as pairs; false where some
-// four units have to be taken ALONE.
+// Units of a row: accumulators (a, u, dh) to values of the hidden operand, as pairs; false where
+// some four units have to be taken ALONE.
 template <int MODE, typename T, int ACT, bool GATED, bool AGAIN, bool ALONE, int kUnits>
 __device__ __forceinline__ bool hidden_values(const uint32_t (&ra)[kUnits],
                                               const uint32_t (&ru)[kUnits],
@@ -844,9 +845,9 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
     };
     const bool staged = nt > 0 && (p.x.raw || (y_too && p.dy.raw));
     // The warp that has read a staged tile last starts the next copy: neither waits for the other.
-    // A warp stops at its next row tile once a wait of the CTA has failed (places become free then that
-    // were not filled), and after a staged tile that did not come: its phase is still open, and the
-    // next one's parity would be an older one's.
+    // A warp stops at its next row tile once a wait of the CTA has failed (places become free then
+    // that were not filled), and after a staged tile that did not come: its phase is still open,
+    // and the next one's parity would be an older one's.
     int xb = 0, taken = 0, staged_tile = 0;  // staged_tile: the last known to be on its way
     uint32_t pf = 1;  // (the first round is free)
     if (staged && tid == 0) fetch(0);
@@ -1014,8 +1015,8 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       }
     };
     // this thread: row `row` of the tile, units half * 32 .. + 32, taken kUnits at a time; the
-    // next units' accumulators are on their way while one set is worked on (16 with rests as well would
-    // spill: 758,527 rows of 2 / 104 / 21 take 257 us so, 239 with 8)
+    // next units' accumulators are on their way while one set is worked on (16 with rests as well
+    // would spill: 758,527 rows of 2 / 104 / 21 take 257 us so, 239 with 8)
     constexpr int kUnits = MODE == kFwd && !TWICE ? 16 : 8;
     constexpr int kSteps = 32 / kUnits;
     auto get = [&](uint32_t d, int q, uint32_t (&ra)[kUnits], uint32_t (&ru)[kUnits],
@@ -1037,10 +1038,11 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
         return hidden_units<MODE, T, ACT, GATED, true, kUnits>(Hs, row, piece, ra, ru, rd, scale);
       return hidden_units<MODE, T, ACT, GATED, false, kUnits>(Hs, row, piece, ra, ru, rd, scale);
     };
-    // Sets of four of the thread's 32 units that have to be taken ALONE, from the accumulators once more
-    // (a row's results do not depend on the other rows of its warp). Kept out of the other way's
-    // registers, where a second look at a set's values would cost 4 to 9 % of the kernel. (917,504 rows of
-    // 64 / 256 / 64: 196 us with a of deviation 1 to 4, 200 with 8, 265 with 15, 320 from 30 on.)
+    // Sets of four of the thread's 32 units that have to be taken ALONE, from the accumulators once
+    // more (a row's results do not depend on the other rows of its warp). Kept out of the other
+    // way's registers, where a second look at a set's values would cost 4 to 9 % of the kernel.
+    // (917,504 rows of 64 / 256 / 64: 196 us with a of deviation 1 to 4, 200 with 8, 265 with 15,
+    // 320 from 30 on.)
     auto work_alone = [&](uint8_t* Hs, uint32_t d) {
 #pragma unroll 1
       for (int k = 0; k < 8; ++k) {
@@ -1089,7 +1091,8 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
           ok &= work(Hs, q + 1, a1, u1, d1);
           continue;
         }
-        // the accumulators are free once the last values are here, unless some may be asked for again
+        // the accumulators are free once the last values are here, unless some may be asked for
+        // again
         auto release = [&]() {
           fence_before();
           __syncwarp();
@@ -1145,8 +1148,8 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
       const bool mine = f < p.f.F && (which ? row >= 64 : GATED || row < 64);
       float* dst = part + (which ? (GATED ? 2 : 1) * FD + (size_t)f * p.f.O
                                  : (row >= 64 ? FD : 0) + (size_t)f * p.f.D);
-      // 32 columns at a time: what the launch before left is asked for at once (one after the other, as
-      // the stores would have it, a launch took 80 us more)
+      // 32 columns at a time: what the launch before left is asked for at once (one after the
+      // other, as the stores would have it, a launch took 80 us more)
 #pragma unroll 1
       for (int e0 = half * 8; e0 < cols; e0 += 64) {
         float sum[4][8];

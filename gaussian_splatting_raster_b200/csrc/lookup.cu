@@ -621,8 +621,8 @@ k_runs(RunArgs a, const T* __restrict__ dout, long long ldd, T* __restrict__ dta
 // added in order.
 constexpr int kLong = 32;
 
-// The entries of row n. Nothing where its bounds do not fit together, as when a wait of the sort ran out
-// and the entries are in no order: CTAs are told from them.
+// The entries of row n. Nothing where its bounds do not fit together, as when a wait of the sort
+// ran out and the entries are in no order: CTAs are told from them.
 __device__ __forceinline__ uint2 entries_of(const RunArgs& a, uint32_t n) {
   const uint2 se = a.bounds[n];
   return se.x < se.y && se.y <= a.M ? se : make_uint2(0u, 0u);

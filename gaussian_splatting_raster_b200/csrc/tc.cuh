@@ -75,9 +75,10 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Wait for the completion of the phase of the given parity, by whole warps: true where the phase is over
-// (and, SURE, no wait of the CTA has failed so far). `failed` is the CTA's failure flag. A warp leaves
-// together and with one result, a vote: its lanes may read the flag on either side of its being set.
+// Wait for the completion of the phase of the given parity, by whole warps: true where the phase is
+// over (and, SURE, no wait of the CTA has failed so far). `failed` is the CTA's failure flag. A
+// warp leaves together and with one result, a vote: its lanes may read the flag on either side of
+// its being set.
 template <bool SURE = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* failed,
                                           unsigned int* status) {
@@ -97,8 +98,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, over);
 }
 
-// For what must be over before a CTA ends, also after a failed wait: copies and MMAs in flight, which
-// end by themselves. It lasts twice as long as a wait, which may have run out shortly before.
+// For what must be over before a CTA ends, also after a failed wait: copies and MMAs in flight,
+// which end by themselves. It lasts twice as long as a wait, which may have run out shortly before.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, unsigned int* status) {
   const long long t0 = clock64();
   while (!mbar_try(bar, parity)) {

@@ -400,12 +400,12 @@ int splat_lookup_backward(const void* dout, long long ld_dout, const int* ids, i
  * splat_ffn_backward: from dy [M, O] the gradients dx [M, D], dw_gate, dw_up [F, D] and dw_down
  * [O, F] (each may be NULL, not all; dw_gate only with w_gate). The hidden values are computed
  * again from x; they and their gradients are rounded once to dtype (in narrow blocks, to twice
- * its bits) before the products that use them (fp32: not rounded); weight gradients are fp32 sums over
- * all rows, rounded once. In fp16 the hidden values' gradients are held times a power of two that
- * depends on the largest finite |dy| of the call (1 from 2^-6 up to 16): they have fp16's digits from
- * 2^-8 of that |dy| on and may grow to 2^11 times it (2^21 times where it is below 2^-6, 2^15 from 16
- * on); beyond that they are infinite. Hidden values themselves are limited as in the forward call.
- * With M = 0 the weight gradients are zero.
+ * its bits) before the products that use them (fp32: not rounded); weight gradients are fp32 sums
+ * over all rows, rounded once. In fp16 the hidden values' gradients are held times a power of two
+ * that depends on the largest finite |dy| of the call (1 from 2^-6 up to 16): they have fp16's
+ * digits from 2^-8 of that |dy| on and may grow to 2^11 times it (2^21 times where it is below
+ * 2^-6, 2^15 from 16 on); beyond that they are infinite. Hidden values themselves are limited as in
+ * the forward call. With M = 0 the weight gradients are zero.
  */
 long long splat_ffn_scratch(int M, int D, int F, int O, int dtype, int gated, int backward);
 int splat_ffn(const void* x, long long ld_x, const void* w_gate, const void* w_up,
@@ -419,9 +419,9 @@ int splat_ffn_backward(const void* dy, long long ld_dy, const void* x, long long
 
 /*
  * Waits inside these kernels (for their own copies, products and earlier blocks) are bounded at
- * about four seconds, and those for what is in flight at a kernel's end at eight. When one ran out on the current device since the last call, the results of the
- * call it belonged to mean nothing and this returns SPLAT_ERR_DEVICE_TIMEOUT once. Waits for
- * `stream`; not to be captured.
+ * about four seconds, and those for what is in flight at a kernel's end at eight. When one ran out
+ * on the current device since the last call, the results of the call it belonged to mean nothing
+ * and this returns SPLAT_ERR_DEVICE_TIMEOUT once. Waits for `stream`; not to be captured.
  */
 int splat_rows_status(void* stream);
 

@@ -74,8 +74,8 @@ def test_far_from_one(P, case):
 
 @pytest.mark.parametrize("gated", [True, False])
 def test_powers_of_two_pass_through(P, gated):
-    """dy times 2^k gives results times 2^k, bit by bit, where they have all their digits: from -12 on
-    all |dy| of both calls are scaled to the same values."""
+    """Two calls whose dy differ by a power of two, both small enough to be scaled to the same values:
+    their results differ by that power, bit by bit, where they have all their digits."""
     x, wg, wu, wd, dy = _inputs(2000, 24, 128, 32, gated, 5, 1.0, 1.0)
     a = _run(P, x, wg, wu, wd, (dy * 2.0 ** -7).to(H), "gelu")
     b = _run(P, x, wg, wu, wd, (dy * 2.0 ** -9).to(H), "gelu")

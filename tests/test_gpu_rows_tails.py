@@ -32,8 +32,8 @@ pytestmark = pytest.mark.gpu
 
 DTYPES = [torch.float32, torch.bfloat16, torch.float16]
 VALUES = [-6e4, -1e4, -1e3, -300.0, -120.0, -90.0, -88.0, -86.0, -60.0, -40.0, -30.0, -23.0,
-          -22.0, -21.5, -21.25, -21.0, -20.0, -15.0, -12.0, -9.0, -7.0, -5.5, -5.0, -4.0, -3.0, -2.0, -1.25, -1.0,
-          -0.5, -1e-3, 0.0, 1e-3, 0.5, 1.0, 3.0, 5.0, 9.0, 21.5, 60.0, 300.0, 6e4]
+          -22.0, -21.5, -21.25, -21.0, -20.0, -15.0, -12.0, -9.0, -7.0, -5.5, -5.0, -4.0, -3.0,
+          -2.0, -1.25, -1.0, -0.5, -1e-3, 0.0, 1e-3, 0.5, 1.0, 3.0, 5.0, 9.0, 21.5, 60.0, 300.0, 6e4]
 BEYOND = [-3e38, -1e30, -1e6, 1e6, 1e30]  # not in fp16
 
 
