@@ -24,11 +24,11 @@
 // the bytes a tile spans, which the loaders lay out from shared memory; at the array's ends,
 // element by element.
 //
-// Measured, bf16, silu, gated, the kernel by itself: forward, 917,504 rows of 64 / 256 / 64 178 us
-// (507 TFLOP/s of products; issue slots 57 %, special function unit 48 %, tensor pipe 23 %; without
-// a gate 168 us), 200,000 rows of 128 / 512 / 128 123 us (640 TFLOP/s). Gradients, 311,296 rows of
-// 64 / 128 / 64: dx 50 us, weights 61; of 35 / 128 / 48 in rows 76 bytes apart, where the loaders
-// bound it, 116 and 113. Few tiles (1,000 rows of 57 / 256 / 64, nothing in L2) take 9 us, dx 20,
+// Measured, bf16, silu, gated, the kernel by itself: forward, 917,504 rows of 64 / 256 / 64 187 us
+// (482 TFLOP/s of products; issue slots 57 %, special function unit 48 %, tensor pipe 23 %; without
+// a gate 175 us), 200,000 rows of 128 / 512 / 128 127 us (617 TFLOP/s). Gradients, 311,296 rows of
+// 64 / 128 / 64: dx 51 us, weights 63; of 35 / 128 / 48 in rows 76 bytes apart, where the loaders
+// bound it, 116 and 115. Few tiles (1,000 rows of 57 / 256 / 64, nothing in L2) take 9 us, dx 20,
 // weights 17.
 #include <cuda.h>
 
@@ -1041,8 +1041,8 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
     // Sets of four of the thread's 32 units that have to be taken ALONE, from the accumulators once
     // more (a row's results do not depend on the other rows of its warp). Kept out of the other
     // way's registers, where a second look at a set's values would cost 4 to 9 % of the kernel.
-    // (917,504 rows of 64 / 256 / 64: 196 us with a of deviation 1 to 4, 200 with 8, 265 with 15,
-    // 320 from 30 on.)
+    // (A call of 917,504 rows of 64 / 256 / 64, nothing in L2: 191 us with a of deviation 1 to 4, 200
+    // with 8, 269 with 15, 324 from 30 on.)
     auto work_alone = [&](uint8_t* Hs, uint32_t d) {
 #pragma unroll 1
       for (int k = 0; k < 8; ++k) {
@@ -1102,10 +1102,14 @@ k_ffn_tc(const __grid_constant__ TcArgs p, const __grid_constant__ CUtensorMap x
           float least = __uint_as_float(a1[0]);
 #pragma unroll
           for (int e = 1; e < kUnits; ++e) least = min_nan(least, __uint_as_float(a1[e]));
+          // (two copies of the last units' work: with one, whose result is looked at, the call took
+          // 196 us)
           const bool done_with = __all_sync(0xffffffffu, ok && least >= kFar);
-          if (done_with) release();
-          ok &= work(Hs, q + 1, a1, u1, d1);
-          if (!done_with) {
+          if (done_with) {
+            release();
+            work(Hs, q + 1, a1, u1, d1);
+          } else {
+            ok &= work(Hs, q + 1, a1, u1, d1);
             if (!__all_sync(0xffffffffu, ok)) work_alone(Hs, d);
             release();
           }
